@@ -28,13 +28,16 @@ FTD_ERR_BAD_PAGE = 7
 
 FTD_F32, FTD_F16, FTD_BF16, FTD_I8 = 0, 1, 2, 3
 FTD_KERNEL_AUTO, FTD_KERNEL_CUDA_CORE = 0, 1
+FTD_ROPE_HALVES, FTD_ROPE_ADJACENT = 0, 1
+FTD_ROPE_SECTIONS, FTD_ROPE_INTERLEAVED = 0, 1
 DTYPES = {"f32": FTD_F32, "f16": FTD_F16, "bf16": FTD_BF16, "i8": FTD_I8}
 
 # Symbols include/ftd.h declares; the loader checks each one is exported.
 EXPORTS = ("ftd_init", "ftd_cache_ptrs", "ftd_decode_mha", "ftd_decode_mha_current", "ftd_decode_mha_paged",
            "ftd_decode_mha_host", "ftd_get_error", "ftd_destroy", "ftd_status_str", "ftd_last_error",
            "ftd_kernel_launches", "ftd_decode_mha_noalloc", "ftd_debug_stall_next",
-           "ftd_debug_late_lengths", "ftd_decode_mha_proj")
+           "ftd_debug_late_lengths", "ftd_decode_mha_proj", "ftd_set_rope", "ftd_rope_qkv", "ftd_enable_scores",
+           "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha")
 
 
 class FtdConfig(ctypes.Structure):
@@ -44,6 +47,12 @@ class FtdConfig(ctypes.Structure):
                 ("out_dtype", ctypes.c_int), ("window", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("num_pages", ctypes.c_int), ("q_len", ctypes.c_int), ("kernel", ctypes.c_int),
                 ("proj_dim", ctypes.c_int), ("wait_limit_us", ctypes.c_int)]
+
+
+class FtdRopeConfig(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("section", ctypes.c_int * 4),
+                ("pairing", ctypes.c_int), ("order", ctypes.c_int), ("theta", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
 
 
 class FtdError(RuntimeError):
@@ -96,6 +105,18 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ftd_decode_mha_noalloc.restype = I
     lib.ftd_debug_stall_next.argtypes = [P, I]
     lib.ftd_debug_stall_next.restype = I
+    lib.ftd_set_rope.argtypes = [P, ctypes.POINTER(FtdRopeConfig)]
+    lib.ftd_set_rope.restype = I
+    lib.ftd_rope_qkv.argtypes = [P] * 4 + [ctypes.c_int64] * 2 + [P] * 2 + [ctypes.c_int64] + [P] * 4
+    lib.ftd_rope_qkv.restype = I
+    lib.ftd_enable_scores.argtypes = [P, P]
+    lib.ftd_enable_scores.restype = I
+    lib.ftd_decode_mha_scored.argtypes = [P] * 16
+    lib.ftd_decode_mha_scored.restype = I
+    lib.ftd_cache_evict.argtypes = [P] * 12 + [I] * 3 + [P]
+    lib.ftd_cache_evict.restype = I
+    lib.ftd_cross_mha.argtypes = [P] * 9
+    lib.ftd_cross_mha.restype = I
     lib.ftd_debug_late_lengths.argtypes = [P, P, I, I, P]
     lib.ftd_debug_late_lengths.restype = I
     if path == LIB:
@@ -158,6 +179,38 @@ def ftd_decode_mha_proj(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, seq_le
                                                      scales, out, w_o, y, stream))
 
 
+def ftd_set_rope(ctx, cfg: Optional[FtdRopeConfig]) -> int:
+    return load_library().ftd_set_rope(ctx, ctypes.byref(cfg) if cfg is not None else None)
+
+
+def ftd_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out, k_out, v_out,
+                 stream) -> int:
+    return load_library().ftd_rope_qkv(*_ptrs(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens,
+                                              q_out, k_out, v_out, stream))
+
+
+def ftd_enable_scores(ctx, stream) -> int:
+    return load_library().ftd_enable_scores(ctx, stream)
+
+
+def ftd_decode_mha_scored(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, next_pos,
+                          acc, acc_out, positions, out, stream) -> int:
+    return load_library().ftd_decode_mha_scored(*_ptrs(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table,
+                                                       seq_lens, scales, next_pos, acc, acc_out, positions, out,
+                                                       stream))
+
+
+def ftd_cache_evict(ctx, k_cache, v_cache, scales, block_table, seq_lens, next_pos, acc, acc_out, positions,
+                    positions_out, new_lens, budget, recent, sinks, stream) -> int:
+    return load_library().ftd_cache_evict(*_ptrs(ctx, k_cache, v_cache, scales, block_table, seq_lens, next_pos, acc,
+                                                 acc_out, positions, positions_out, new_lens, budget, recent, sinks,
+                                                 stream))
+
+
+def ftd_cross_mha(ctx, q, q_bias, k_mem, v_mem, mem_lens, scales, out, stream) -> int:
+    return load_library().ftd_cross_mha(*_ptrs(ctx, q, q_bias, k_mem, v_mem, mem_lens, scales, out, stream))
+
+
 def ftd_decode_mha_host(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, seq_lens, scales, out,
                         stream) -> int:
     return load_library().ftd_decode_mha_host(*_ptrs(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache,
@@ -200,12 +253,33 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+def _row_stride(t, width: int, head_dim: int) -> int:
+    """Elements from one token's row of ``width`` elements (heads flattened, or [heads, head_dim]) to the next; 0: dense."""
+    if t.is_contiguous():
+        return 0
+    split = t.shape[-1] != width
+    lead = t.dim() - (2 if split else 1)
+    ok = lead >= 1 and t.stride(-1) == 1 and (not split or (t.shape[-1] == head_dim and t.stride(-2) == head_dim
+                                                            and t.shape[-2] * head_dim == width))
+    row, n = 0, 1  # the innermost token dimension's stride, and the tokens within the dimensions seen
+    for i in reversed(range(lead if ok else 0)):
+        if t.shape[i] == 1:
+            continue
+        row = row or t.stride(i)
+        ok = ok and t.stride(i) == row * n
+        n *= t.shape[i]
+    if not ok:
+        raise ValueError("rows of heads must be dense and a fixed number of elements apart")
+    return row
+
+
 class DecodeStep:
     """Owns one library context; calls take torch CUDA tensors (marshalling only)."""
 
     def __init__(self, max_batch, n_q_heads, n_kv_heads, head_dim, max_len, qkv_dtype="bf16",
                  cache_dtype="bf16", softmax_scale=0.0, stream: Optional[int] = None, out_dtype="f32",
-                 window=0, page_size=0, num_pages=0, q_len=1, kernel=FTD_KERNEL_AUTO, wait_limit_us=0, proj_dim=0):
+                 window=0, page_size=0, num_pages=0, q_len=1, kernel=FTD_KERNEL_AUTO, wait_limit_us=0, proj_dim=0,
+                 scored=False):
         import torch
         self.cfg = FtdConfig(max_batch, n_q_heads, n_kv_heads, head_dim, max_len, DTYPES[qkv_dtype],
                              DTYPES[cache_dtype], float(softmax_scale), DTYPES[out_dtype], int(window),
@@ -215,6 +289,8 @@ class DecodeStep:
         st, ctx = ftd_init(self.cfg, s)
         check(st)
         self.ctx = ctx
+        if scored:
+            self.enable_scores(s)
 
     def cache_ptrs(self):
         st, k, v, s = ftd_cache_ptrs(self.ctx)
@@ -245,6 +321,74 @@ class DecodeStep:
         check(ftd_decode_mha_paged(self.ctx, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(bias), _ptr(k_pages),
                                    _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(scales), _ptr(out),
                                    s))
+
+    def enable_scores(self, stream: Optional[int] = None):
+        """Allocate what ``scored`` and ``evict`` need (``scored=True`` does it at construction)."""
+        import torch
+        check(ftd_enable_scores(self.ctx, torch.cuda.current_stream().cuda_stream if stream is None else stream))
+
+    def scored(self, q, k_new, v_new, seq_lens, next_pos, acc, positions, out, acc_out=None, bias=None, k_cache=None,
+               v_cache=None, scales=None, block_table=None, stream: Optional[int] = None):
+        """The step, which also adds every position's attention weight to ``acc`` (into ``acc_out`` when
+        given); the new rows of ``positions`` (may be None, with next_pos) become next_pos, next_pos + 1, ..."""
+        import torch
+        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        check(ftd_decode_mha_scored(self.ctx, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(bias), _ptr(k_cache),
+                                    _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(scales), _ptr(next_pos),
+                                    _ptr(acc), _ptr(acc_out), _ptr(positions), _ptr(out), s))
+
+    def evict(self, acc, positions, seq_lens, next_pos, new_lens, budget, recent=0, sinks=0, acc_out=None,
+              positions_out=None, k_cache=None, v_cache=None, scales=None, block_table=None,
+              stream: Optional[int] = None):
+        """Bring every slot down to ``budget`` rows per kv head by accumulated weight (``new_lens`` may be
+        ``seq_lens``; planes change in place unless ``acc_out`` / ``positions_out`` are given)."""
+        import torch
+        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        check(ftd_cache_evict(self.ctx, _ptr(k_cache), _ptr(v_cache), _ptr(scales), _ptr(block_table),
+                              _ptr(seq_lens), _ptr(next_pos), _ptr(acc), _ptr(acc_out), _ptr(positions),
+                              _ptr(positions_out), _ptr(new_lens), int(budget), int(recent), int(sinks), s))
+
+    def cross(self, q, mem_lens, out, q_bias=None, k_mem=None, v_mem=None, scales=None,
+              stream: Optional[int] = None):
+        """Cross attention of the slots' tokens to memories of ``mem_lens`` rows (None: the context's pool)."""
+        import torch
+        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        check(ftd_cross_mha(self.ctx, _ptr(q), _ptr(q_bias), _ptr(k_mem), _ptr(v_mem), _ptr(mem_lens), _ptr(scales),
+                            _ptr(out), s))
+
+    def set_rope(self, n_axes=1, sections=None, rotary_dim=0, theta=0.0, pairing="halves", order="sections",
+                 inv_freq=None):
+        """The rotary positions of ``rope``: sections holds the pairs of each axis, inv_freq (host floats)
+        replaces theta^(-2i/R)."""
+        cfg = FtdRopeConfig(n_axes=int(n_axes), rotary_dim=int(rotary_dim), theta=float(theta))
+        sections = list(sections) if sections is not None else []
+        if len(sections) > 4:
+            raise ValueError("at most four axes")
+        for a, n in enumerate(sections):
+            cfg.section[a] = int(n)
+        cfg.pairing = {"halves": FTD_ROPE_HALVES, "adjacent": FTD_ROPE_ADJACENT}[pairing]
+        cfg.order = {"sections": FTD_ROPE_SECTIONS, "interleaved": FTD_ROPE_INTERLEAVED}[order]
+        if inv_freq is not None:
+            f = [float(x) for x in inv_freq]
+            if len(f) != (int(rotary_dim) or self.cfg.head_dim) // 2:
+                raise ValueError("inv_freq holds one value per pair")
+            cfg.inv_freq = (ctypes.c_double * len(f))(*f)
+        check(ftd_set_rope(self.ctx, cfg))
+
+    def rope(self, q, k, v, positions, q_out, k_out, v_out=None, bias=None, stream: Optional[int] = None):
+        """Bias and rotary positions for the tokens of q, k (and v, which only takes the bias; None with
+        v_out None): rows of heads a fixed stride apart, such as slices of a fused projection.  positions is
+        int32 [n_axes, tokens]; the outputs are dense and may be their own dense inputs."""
+        import torch
+        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
+        c = self.cfg
+        qw, kw = c.n_q_heads * c.head_dim, c.n_kv_heads * c.head_dim
+        n = q.numel() // qw
+        qs, ks = _row_stride(q, qw, c.head_dim), _row_stride(k, kw, c.head_dim)
+        if v is not None and (_row_stride(v, kw, c.head_dim) or kw) != (ks or kw) and n > 1:
+            raise ValueError("k and v must share one row stride")
+        check(ftd_rope_qkv(self.ctx, _ptr(q), _ptr(k), _ptr(v), qs, ks, _ptr(bias), _ptr(positions), n, _ptr(q_out),
+                           _ptr(k_out), _ptr(v_out), s))
 
     def get_error(self) -> int:
         return ftd_get_error(self.ctx)

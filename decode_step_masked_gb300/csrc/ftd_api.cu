@@ -23,6 +23,7 @@
 #include "ftd_decode_gqa_tc.cuh"
 #include "ftd_internal.cuh"
 #include "ftd_decode_wide_tc.cuh"
+#include "ftd_ops.cuh"
 #include "ftd_out_proj.cuh"
 
 namespace {
@@ -135,7 +136,7 @@ namespace ftd {
 // cfg.kernel == FTD_KERNEL_CUDA_CORE selects the CUDA-core kernel instead.
 // Internal to the library (hidden), shared by ftd_init and the no-allocation
 // entry point; tki.fn is null when the CUDA-core kernel runs.
-__attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c) {
+__attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, int mode) {
     TcChoice r{};
     r.nhb = 1;
     r.qblk = 8;
@@ -149,15 +150,30 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c) {
             // 32 or more query rows per kv head: the wide kernel, all rows of a block of
             // 32 or 64 in one pass per tile
             r.qblk = rows_q % 64 == 0 ? 64 : 32;
-            r.tki = select_wide(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1);
+            r.tki = mode == kScored  ? select_tc_scored(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1)
+                    : mode == kCross ? select_tc_cross(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1)
+                                     : select_wide(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1);
         } else {
             const int Gt = (rows_q % 16 == 0 && !want_tc_i8) ? 16 : 8;
             r.qblk = rows_q % 8 == 0 ? Gt : 4;
-            r.tki = want_tc_i8 ? select_tc_i8(c.q_len > 1) : select_tc(c.cache_dtype == FTD_BF16, Gt, c.q_len > 1);
+            const bool bf = c.cache_dtype == FTD_BF16, mt = c.q_len > 1;
+            if (mode == kScored) r.tki = want_tc_i8 ? select_tc_i8_scored(mt) : select_tc_scored(bf, Gt, mt);
+            else if (mode == kCross) r.tki = want_tc_i8 ? select_tc_i8_cross(mt) : select_tc_cross(bf, Gt, mt);
+            else r.tki = want_tc_i8 ? select_tc_i8(mt) : select_tc(bf, Gt, mt);
         }
         r.nhb = rows_q / r.qblk;
     }
     return r;
+}
+
+__attribute__((visibility("hidden"))) KernelInfo choose_cc(ftd_dtype dt, int D, int G, int mode) {
+    switch (dt) {
+        case FTD_F32: return mode == kScored ? select_f32_scored(D, G) : mode == kCross ? select_f32_cross(D, G) : select_f32(D, G);
+        case FTD_F16: return mode == kScored ? select_f16_scored(D, G) : mode == kCross ? select_f16_cross(D, G) : select_f16(D, G);
+        case FTD_BF16: return mode == kScored ? select_bf16_scored(D, G) : mode == kCross ? select_bf16_cross(D, G) : select_bf16(D, G);
+        case FTD_I8: return mode == kScored ? select_i8_scored(D, G) : mode == kCross ? select_i8_cross(D, G) : select_i8(D, G);
+    }
+    return KernelInfo{};
 }
 
 __attribute__((visibility("hidden"))) bool encode_tc_cache_map(CUtensorMap* map, void* base, ftd_dtype dt,
@@ -213,13 +229,7 @@ __attribute__((visibility("hidden"))) ftd_status plan_config(const ftd_config& c
     const int rows_q = nq * g;  // query rows per kv head: every new token's heads of the group
     int G = 8;
     while (rows_q % G) G >>= 1;
-    KernelInfo ki{};
-    switch (c.cache_dtype) {
-        case FTD_F32: ki = select_f32(c.head_dim, G); break;
-        case FTD_F16: ki = select_f16(c.head_dim, G); break;
-        case FTD_BF16: ki = select_bf16(c.head_dim, G); break;
-        case FTD_I8: ki = select_i8(c.head_dim, G); break;
-    }
+    const KernelInfo ki = choose_cc(c.cache_dtype, c.head_dim, G, kStep);
     if (!ki.fn) return bad(FTD_ERR_UNSUPPORTED, "no kernel for this configuration");
     const size_t Hkv = static_cast<size_t>(c.n_kv_heads);
     const size_t rows = paged ? static_cast<size_t>(c.num_pages) * Hkv * c.page_size
@@ -359,6 +369,21 @@ struct ftd_ctx {
     CUtensorMap tmpl;
     CUtensorMap tmw;
     const void* tm_w_base = nullptr;
+    // kernels of the step with scores and of cross attention, set up at their first use
+    struct ModeKernel {
+        bool ready = false;
+        ftd::KernelInfo ki{};
+        ftd::TcKernelInfo tki{};
+    } mode[3];
+    // ftd_enable_scores: workspace of ftd_decode_mha_scored and ftd_cache_evict
+    void* sc_pool = nullptr;
+    float* scores = nullptr;
+    float2* stats = nullptr;
+    int2* moves = nullptr;
+    uint32_t* evict_count = nullptr;
+    // ftd_set_rope
+    bool rope_set = false;
+    ftd::RopeParams rope{};
 };
 
 extern "C" {
@@ -555,7 +580,7 @@ static cudaError_t launch_overlapped(const void* fn, int grid, int threads, int 
 static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
                                 const void* bias, void* k_cache, void* v_cache, const int32_t* block_table,
                                 const int32_t* seq_lens, float* scales, void* out, cudaStream_t stream,
-                                bool proj = false) {
+                                bool proj = false, int mode = ftd::kStep) {
     if (!k_cache) k_cache = ctx->k_cache;
     if (!v_cache) v_cache = ctx->v_cache;
     const bool i8 = ctx->cfg.cache_dtype == FTD_I8;
@@ -603,6 +628,18 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     p.proj_hi = proj ? ctx->proj_hi : nullptr;
     p.proj_lo = proj ? ctx->proj_lo : nullptr;
     p.proj_dt = c.qkv_dtype == FTD_BF16 ? ftd::kBF16 : ftd::kF16;
+    ftd::KernelInfo ki = ctx->ki;
+    ftd::TcKernelInfo tki = ctx->tki;
+    if (mode != ftd::kStep) {
+        ki = ctx->mode[mode].ki;
+        tki = ctx->mode[mode].tki;
+    }
+    if (mode == ftd::kScored) {
+        p.scores = ctx->scores;
+        p.stats = ctx->stats;
+        p.sscale = ctx->qscale;
+        p.qscale = 1.f;
+    }
     p.stall = 0;
     if (ctx->stall_calls > 0) {
         p.stall = 1;
@@ -625,10 +662,10 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
         p.nhb = ctx->tc_nhb;
         p.qblk = ctx->tc_qblk;
         void* args[] = {&ctx->tmk, &ctx->tmv, &p};
-        e = launch_overlapped(ctx->tki.fn, ctx->grid, ctx->tki.threads, ctx->tki.smem, args, stream);
+        e = launch_overlapped(tki.fn, ctx->grid, tki.threads, tki.smem, args, stream);
     } else {
         void* args[] = {&p};
-        e = launch_overlapped(ctx->ki.fn, ctx->grid, ctx->ki.warps * 32, ctx->ki.smem, args, stream);
+        e = launch_overlapped(ki.fn, ctx->grid, ki.warps * 32, ki.smem, args, stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
     g_launches.fetch_add(1);
@@ -792,6 +829,7 @@ ftd_status ftd_get_error(ftd_ctx* ctx) {
     if (h & ftd::kErrTimeout) {
         // an abandoned launch may have left segment counters part-way; restart them
         e = cudaMemset(ctx->counters, 0, ctx->n_counters * sizeof(uint32_t));
+        if (e == cudaSuccess && ctx->evict_count) e = cudaMemset(ctx->evict_count, 0, 2 * sizeof(uint32_t));
         if (e == cudaSuccess && ctx->n_proj_counters)
             e = cudaMemset(ctx->proj_counters, 0, ctx->n_proj_counters * sizeof(uint32_t));
         if (e != cudaSuccess) return cuda_fail(e, "clearing the split-K counters");
@@ -821,8 +859,371 @@ void ftd_destroy(ftd_ctx* ctx) {
             }
     }
     cudaDeviceSynchronize();
+    cudaFree(ctx->sc_pool);
     cudaFree(ctx->pool);
     delete ctx;
+}
+
+// ------------------------------------------- operators around the step
+// The context's device, for calls that may come with another one current; restores it.
+namespace {
+struct DeviceScope {
+    int before = -1;
+    cudaError_t err;
+    explicit DeviceScope(int dev) {
+        err = cudaGetDevice(&before);
+        if (err == cudaSuccess && before != dev) err = cudaSetDevice(dev);
+        else before = -1;  // nothing to restore
+    }
+    ~DeviceScope() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+};
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// The kernels of `mode` for the context's configuration, with their shared-memory limits raised
+// (the same tiles, blocks and partial slots as the step's, so its workspace serves them too).
+ftd_status ready_mode(ftd_ctx* ctx, int mode) {
+    ftd_ctx::ModeKernel& m = ctx->mode[mode];
+    if (m.ready) return FTD_OK;
+    const ftd_config& c = ctx->cfg;
+    m.ki = ftd::choose_cc(c.cache_dtype, c.head_dim, ctx->G, mode);
+    cudaError_t e = cudaSuccess;
+    if (ctx->use_tc) {
+        m.tki = ftd::choose_tc(c, mode).tki;
+        e = cudaFuncSetAttribute(m.tki.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, m.tki.smem);
+    } else {
+        e = cudaFuncSetAttribute(m.ki.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, m.ki.smem);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    m.ready = true;
+    return FTD_OK;
+}
+
+int page_shift_of(const ftd_ctx* ctx) {
+    int s = 0;
+    while (ctx->paged && (1 << s) < ctx->cfg.page_size) ++s;
+    return s;
+}
+
+// The block table a call needs: given for a paged context, absent for a contiguous one.
+ftd_status check_table(const ftd_ctx* ctx, const int32_t* table, const char* what) {
+    if (ctx->paged && (!table || !aligned(table, 4)))
+        return fail(FTD_ERR_INVALID_ARG, "%s: a paged context needs a 4-byte aligned block table", what);
+    if (!ctx->paged && table) return fail(FTD_ERR_INVALID_ARG, "%s: a contiguous context takes no block table", what);
+    return FTD_OK;
+}
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+}  // namespace
+
+ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_enable_scores: ctx is NULL");
+    if (ctx->sc_pool) return FTD_OK;
+    const ftd_config& c = ctx->cfg;
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    cudaError_t e = ftd::setup_evict();
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (eviction)");
+    const ftd_status st = ready_mode(ctx, ftd::kScored);
+    if (st != FTD_OK) return st;
+    const size_t segs = static_cast<size_t>(c.max_batch) * c.n_kv_heads;
+    const size_t rows_q = static_cast<size_t>(ctx->nq) * (c.n_q_heads / c.n_kv_heads);
+    const size_t n_scores = segs * rows_q * c.max_len, n_moves = segs * (c.max_len / 2);
+    // The weights kernel's grid: one block per 512 positions of a kv head.
+    if (segs * ((c.max_len + 511) / 512) >= (static_cast<size_t>(1) << 31))
+        return fail(FTD_ERR_UNSUPPORTED, "ftd_enable_scores: cache too large for the weights kernel's grid");
+    size_t off = 0;
+    auto carve = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    };
+    const size_t o_cnt = carve(2 * sizeof(uint32_t)), o_sc = carve(n_scores * sizeof(float));
+    const size_t o_st = carve(segs * rows_q * sizeof(float2)), o_mv = carve(n_moves * sizeof(int2));
+    void* pool = nullptr;
+    e = cudaMalloc(&pool, off);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "cudaMalloc of the score workspace");
+    }
+    e = cudaMemsetAsync(pool, 0, o_sc, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        cudaFree(pool);
+        return cuda_fail(e, "cudaMemsetAsync of the score workspace");
+    }
+    unsigned char* base = static_cast<unsigned char*>(pool);
+    ctx->sc_pool = pool;
+    ctx->evict_count = reinterpret_cast<uint32_t*>(base + o_cnt);
+    ctx->scores = reinterpret_cast<float*>(base + o_sc);
+    ctx->stats = reinterpret_cast<float2*>(base + o_st);
+    ctx->moves = reinterpret_cast<int2*>(base + o_mv);
+    return FTD_OK;
+}
+
+ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
+                                 const void* qkv_bias, void* k_cache, void* v_cache, const int32_t* block_table,
+                                 const int32_t* seq_lens, float* scales, const int32_t* next_pos, const float* acc,
+                                 float* acc_out, int32_t* positions, void* out, void* stream) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: ctx is NULL");
+    if (!ctx->sc_pool) return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: ftd_enable_scores first");
+    if (!acc || !aligned(acc, 16) || !aligned(acc_out, 16))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: acc must be non-NULL, acc and acc_out 16-byte aligned");
+    if (positions && (!next_pos || !aligned(next_pos, 4) || !aligned(positions, 4)))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: positions needs next_pos, both 4-byte aligned");
+    ftd_status st = check_table(ctx, block_table, "ftd_decode_mha_scored");
+    if (st != FTD_OK) return st;
+    const ftd_config& c = ctx->cfg;
+    if (!acc_out) acc_out = const_cast<float*>(acc);
+    const size_t plane = ctx->rows * sizeof(float);
+    if (acc_out != acc && overlaps(acc, plane, acc_out, plane))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: acc_out must be acc or a plane apart from it");
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, out, s, false,
+                       ftd::kScored);
+    if (st != FTD_OK) return st;
+    ftd::WeightsParams w{};
+    w.scores = ctx->scores;
+    w.stats = ctx->stats;
+    w.seq_lens = seq_lens;
+    w.next_pos = next_pos;
+    w.block_table = ctx->paged ? block_table : nullptr;
+    w.acc = acc;
+    w.acc_out = acc_out;
+    w.positions = positions;
+    w.B = c.max_batch;
+    w.Hkv = c.n_kv_heads;
+    w.Lmax = c.max_len;
+    w.nq = ctx->nq;
+    w.group = c.n_q_heads / c.n_kv_heads;
+    w.window = c.window;
+    w.pages_per_seq = ctx->pages_per_seq;
+    w.page_shift = page_shift_of(ctx);
+    w.num_pages = c.num_pages;
+    const cudaError_t e = ftd::launch_weights(w, s);
+    if (e != cudaSuccess) return cuda_fail(e, "weights kernel launch");
+    g_launches.fetch_add(1);
+    return FTD_OK;
+}
+
+ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* scales, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* next_pos, const float* acc, float* acc_out,
+                           const int32_t* positions, int32_t* positions_out, int32_t* new_lens, int budget, int recent,
+                           int sinks, void* stream) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: ctx is NULL");
+    if (!ctx->sc_pool) return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: ftd_enable_scores first");
+    const ftd_config& c = ctx->cfg;
+    if (c.window > 0)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: rows change places, which a sliding window cannot follow");
+    if (c.max_len > ftd::kMaxEvictLen)
+        return fail(FTD_ERR_UNSUPPORTED, "ftd_cache_evict: max_len %d above %d", c.max_len, ftd::kMaxEvictLen);
+    if (!seq_lens || !next_pos || !acc || !positions || !new_lens)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: seq_lens, next_pos, acc, positions and new_lens must be non-NULL");
+    if (!aligned(seq_lens, 4) || !aligned(next_pos, 4) || !aligned(acc, 4) || !aligned(acc_out, 4) ||
+        !aligned(positions, 4) || !aligned(positions_out, 4) || !aligned(new_lens, 4))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: lengths and planes must be 4-byte aligned");
+    if (budget < 1 || budget > c.max_len)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: budget %d outside 1..%d", budget, c.max_len);
+    if (recent < 0 || sinks < 0 || static_cast<long long>(recent) + sinks > budget)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: recent %d and sinks %d must be >= 0 and fit the budget %d",
+                    recent, sinks, budget);
+    if (!k_cache) k_cache = ctx->k_cache;
+    if (!v_cache) v_cache = ctx->v_cache;
+    const bool i8 = c.cache_dtype == FTD_I8;
+    if (i8 && !scales) scales = ctx->scales;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || (i8 && !aligned16(scales)))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: caches and scales must be 16-byte aligned");
+    ftd_status st = check_table(ctx, block_table, "ftd_cache_evict");
+    if (st != FTD_OK) return st;
+    if (!acc_out) acc_out = const_cast<float*>(acc);
+    if (!positions_out) positions_out = const_cast<int32_t*>(positions);
+    const size_t plane = ctx->rows * 4;
+    if ((acc_out != acc && overlaps(acc, plane, acc_out, plane)) ||
+        (positions_out != positions && overlaps(positions, plane, positions_out, plane)))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: an output plane must be its input plane or apart from it");
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    ftd::EvictParams p{};
+    p.k_cache = static_cast<unsigned char*>(k_cache);
+    p.v_cache = static_cast<unsigned char*>(v_cache);
+    p.k_scales = i8 ? scales : nullptr;
+    p.v_scales = i8 ? scales + ctx->rows : nullptr;
+    p.seq_lens = seq_lens;
+    p.new_lens = new_lens;
+    p.next_pos = next_pos;
+    p.block_table = ctx->paged ? block_table : nullptr;
+    p.acc = acc;
+    p.acc_out = acc_out;
+    p.positions = positions;
+    p.positions_out = positions_out;
+    p.keys = reinterpret_cast<uint32_t*>(ctx->scores);  // (at least one score row per kv head)
+    p.moves = ctx->moves;
+    p.count = ctx->evict_count;
+    p.err = ctx->err;
+    p.B = c.max_batch;
+    p.Hkv = c.n_kv_heads;
+    p.Lmax = c.max_len;
+    p.row_bytes = c.head_dim * elem_bytes(c.cache_dtype);
+    p.budget = budget;
+    p.recent = recent;
+    p.sinks = sinks;
+    p.pages_per_seq = ctx->pages_per_seq;
+    p.page_shift = page_shift_of(ctx);
+    p.num_pages = c.num_pages;
+    const cudaError_t e = ftd::launch_evict(p, ctx->grid, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "eviction kernel launch");
+    g_launches.fetch_add(2);
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return FTD_OK;
+}
+
+ftd_status ftd_cross_mha(ftd_ctx* ctx, const void* q, const void* q_bias, const void* k_mem, const void* v_mem,
+                         const int32_t* mem_lens, const float* scales, void* out, void* stream) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_cross_mha: ctx is NULL");
+    if (ctx->paged) return fail(FTD_ERR_INVALID_ARG, "ftd_cross_mha serves contiguous memories only");
+    if (ctx->cfg.window > 0) return fail(FTD_ERR_INVALID_ARG, "ftd_cross_mha: a memory has no sliding window");
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    const ftd_status st = ready_mode(ctx, ftd::kCross);
+    if (st != FTD_OK) return st;
+    // The memory is only read, and there are no new rows: q stands in for k_new and v_new,
+    // which the cross-attention kernels do not touch.
+    return launch_decode(ctx, q, q, q, q_bias, const_cast<void*>(k_mem), const_cast<void*>(v_mem), nullptr, mem_lens,
+                         const_cast<float*>(scales), out, static_cast<cudaStream_t>(stream), false, ftd::kCross);
+}
+
+ftd_status ftd_set_rope(ftd_ctx* ctx, const ftd_rope_config* cfg) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: ctx is NULL");
+    if (!cfg) return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: cfg is NULL");
+    const int D = ctx->cfg.head_dim;
+    const int R = cfg->rotary_dim ? cfg->rotary_dim : D;
+    if (R < 2 || R > D || R % 2 != 0)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: rotary_dim %d must be even, 2..%d (0: head_dim)", cfg->rotary_dim, D);
+    if (cfg->n_axes < 1 || cfg->n_axes > 4)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: n_axes %d outside 1..4", cfg->n_axes);
+    if (cfg->pairing != FTD_ROPE_HALVES && cfg->pairing != FTD_ROPE_ADJACENT)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: pairing %d", cfg->pairing);
+    if (cfg->order != FTD_ROPE_SECTIONS && cfg->order != FTD_ROPE_INTERLEAVED)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: order %d", cfg->order);
+    int left[4] = {};
+    long long sum = 0;
+    for (int a = 0; a < cfg->n_axes; ++a) {
+        if (cfg->section[a] < 0) return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: section %d is negative", a);
+        left[a] = cfg->section[a];
+        sum += left[a];
+    }
+    if (cfg->n_axes == 1 && sum == 0) sum = left[0] = R / 2;
+    if (sum != R / 2)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: the sections hold %lld pairs, rotary_dim %d has %d", sum, R, R / 2);
+    if (!cfg->inv_freq && !(cfg->theta == 0.0 || (cfg->theta > 0.0 && std::isfinite(cfg->theta))))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: theta must be finite and > 0 (0: 10000)");
+    ftd::RopeParams r{};
+    r.R = R;
+    r.D = D;
+    r.adjacent = cfg->pairing == FTD_ROPE_ADJACENT;
+    const double theta = cfg->theta > 0.0 ? cfg->theta : 10000.0;
+    int axis = 0;
+    for (int i = 0; i < R / 2; ++i) {
+        while (!left[axis]) axis = (axis + 1) % cfg->n_axes;
+        r.axis[i] = static_cast<unsigned char>(axis);
+        --left[axis];
+        if (cfg->order == FTD_ROPE_INTERLEAVED) axis = (axis + 1) % cfg->n_axes;
+        const double f = cfg->inv_freq ? cfg->inv_freq[i] : std::pow(theta, -2.0 * i / R);
+        if (!std::isfinite(f)) return fail(FTD_ERR_INVALID_ARG, "ftd_set_rope: inv_freq[%d] is not finite", i);
+        double turns = f / 6.283185307179586476925286766559;
+        turns -= std::floor(turns);  // [0, 1); rounding can give 1, a whole turn
+        r.step[i] = turns >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(turns, 64));
+    }
+    ctx->rope = r;
+    ctx->rope_set = true;
+    return FTD_OK;
+}
+
+ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride, int64_t kv_stride,
+                        const void* qkv_bias, const int32_t* positions, int64_t n_tokens, void* q_out, void* k_out,
+                        void* v_out, void* stream) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: ctx is NULL");
+    if (!ctx->rope_set) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: ftd_set_rope first");
+    const ftd_config& c = ctx->cfg;
+    if (n_tokens < 0 || n_tokens > (static_cast<int64_t>(1) << 31) - 1)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: n_tokens %lld", static_cast<long long>(n_tokens));
+    if (n_tokens == 0) return FTD_OK;
+    if (!q || !k || !positions || !q_out || !k_out || (v == nullptr) != (v_out == nullptr))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: q, k, positions, q_out and k_out must be non-NULL, v and v_out both or neither");
+    const int64_t qw = static_cast<int64_t>(c.n_q_heads) * c.head_dim, kw = static_cast<int64_t>(c.n_kv_heads) * c.head_dim;
+    if (q_stride == 0) q_stride = qw;
+    if (kv_stride == 0) kv_stride = kw;
+    if (q_stride < qw || kv_stride < kw || q_stride > (static_cast<int64_t>(1) << 31) || kv_stride > (static_cast<int64_t>(1) << 31))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: strides %lld, %lld below a row of %lld, %lld elements (or above 2^31)",
+                    static_cast<long long>(q_stride), static_cast<long long>(kv_stride), static_cast<long long>(qw),
+                    static_cast<long long>(kw));
+    const int eb = elem_bytes(c.qkv_dtype);
+    const void* ptrs[] = {q, k, v, qkv_bias, q_out, k_out, v_out};
+    bool vec = (q_stride * eb) % 16 == 0 && (kv_stride * eb) % 16 == 0 && (ctx->rope.R / 2) % (16 / eb) == 0;
+    for (const void* p : ptrs) {
+        if (!aligned(p, eb)) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: pointers must be aligned to their element");
+        vec = vec && aligned16(p);
+    }
+    if (!aligned(positions, 4)) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: positions must be 4-byte aligned");
+    // An output may be its own input (same rows); any other overlap would be read after it was written.
+    const size_t n = static_cast<size_t>(n_tokens);
+    struct Span { const void* p; size_t bytes; int64_t stride, width; };
+    const Span in[3] = {{q, ((n - 1) * q_stride + qw) * eb, q_stride, qw},
+                        {k, ((n - 1) * kv_stride + kw) * eb, kv_stride, kw},
+                        {v, ((n - 1) * kv_stride + kw) * eb, kv_stride, kw}};
+    const Span out[3] = {{q_out, n * qw * eb, qw, qw}, {k_out, n * kw * eb, kw, kw}, {v_out, n * kw * eb, kw, kw}};
+    for (int o = 0; o < 3; ++o) {
+        if (!out[o].p) continue;
+        for (int i = 0; i < 3; ++i) {
+            if (!in[i].p || !overlaps(in[i].p, in[i].bytes, out[o].p, out[o].bytes)) continue;
+            if (!(i == o && in[i].p == out[o].p && in[i].stride == in[i].width))
+                return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: an output may only be its own dense input, or apart from every input");
+        }
+        for (int i = 0; i < o; ++i)
+            if (out[i].p && overlaps(out[i].p, out[i].bytes, out[o].p, out[o].bytes))
+                return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: outputs overlap");
+        if (overlaps(positions, n * 4, out[o].p, out[o].bytes) ||
+            (qkv_bias && overlaps(qkv_bias, static_cast<size_t>(qw + 2 * kw) * eb, out[o].p, out[o].bytes)))
+            return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: an output overlaps positions or the bias");
+    }
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    ftd::RopeParams r = ctx->rope;
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.bias = qkv_bias;
+    r.qo = q_out;
+    r.ko = k_out;
+    r.vo = v_out;
+    r.pos = positions;
+    r.n = n_tokens;
+    r.q_stride = q_stride;
+    r.kv_stride = kv_stride;
+    r.Hq = c.n_q_heads;
+    r.Hkv = c.n_kv_heads;
+    r.dt = static_cast<int>(c.qkv_dtype);
+    // values in place and without a bias are done already
+    const bool move_v = v && (v != v_out || qkv_bias);
+    r.heads = c.n_q_heads + c.n_kv_heads * (move_v ? 2 : 1);
+    const cudaError_t e = ftd::launch_rope(r, vec, ctx->grid, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rotary kernel launch");
+    g_launches.fetch_add(1);
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return FTD_OK;
 }
 
 }  // extern "C"

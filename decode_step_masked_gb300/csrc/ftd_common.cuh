@@ -34,6 +34,11 @@ constexpr int kThreads = kWarps * 32;
 
 enum QkvType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
+// What a decode kernel is compiled for: the step; the step that also keeps every visible
+// score and each query row's softmax statistics, for the accumulated weights; or cross
+// attention to a memory of M rows (no append, every query row sees all of them).
+enum StepMode : int { kStep = 0, kScored = 1, kCross = 2 };
+
 // Arguments of one decode step, resolved by the host entry point.
 struct DecodeParams {
     const void* q;        // [B][Hq][D]  qkv dtype
@@ -68,7 +73,39 @@ struct DecodeParams {
     void* proj_hi;          // nullptr: no projection
     void* proj_lo;
     int proj_dt;
+    // kScored: the scores of query row qi of (b, kv head) at [((b * Hkv + kvh) * nq * group + qi) * Lmax + position],
+    // in the log2 domain, and the row's (reference m, 1 / sum of 2^(s - m)).  There q is staged
+    // unscaled (qscale 1) and the scores are multiplied by sscale: a 16-bit q, alone or with a
+    // bias, then splits into its hi and lo parts (almost) without rounding, which keeps the fp32
+    // weights as exact as fp32 products.
+    float* scores;
+    float2* stats;
+    float sscale;
 };
+
+// Cached length the kernels work with, from the caller's entry: L tokens before the new ones,
+// or, for cross attention, the memory's last row M - 1.
+template <int MODE>
+__device__ __forceinline__ int step_len(int raw) {
+    if constexpr (MODE == kCross) return max(raw, 0) - 1;
+    return raw;
+}
+// New rows a segment holds past its cached length: nq, or the memory's own last row.
+template <int MODE>
+__device__ __forceinline__ int step_nq(const DecodeParams& p) {
+    if constexpr (MODE == kCross) return 1;
+    return p.nq;
+}
+// Rows that come from the cache.
+template <int MODE>
+__device__ __forceinline__ int cached_rows(int L) {
+    if constexpr (MODE == kCross) return L + 1;
+    return L;
+}
+// kScored: index of the score and statistics row of query row qi of (b, kvh).
+__device__ __forceinline__ size_t score_row(const DecodeParams& p, int b, int kvh, int qi) {
+    return (static_cast<size_t>(b) * p.Hkv + kvh) * (p.nq * p.group) + qi;
+}
 
 // First visible position of a slot with L cached tokens (the window start).
 __device__ __forceinline__ int window_start(int L, int window) {

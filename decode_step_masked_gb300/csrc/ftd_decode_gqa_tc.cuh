@@ -432,7 +432,7 @@ static __device__ __noinline__ void tc_drain_copies(uint32_t full0, int stages, 
 
 // MQ: several new tokens per slot (q_len > 1), so the columns of S carry
 // their own causal limits; without it every column shares one row range.
-template <typename CT, int G, bool MQ>
+template <typename CT, int G, bool MQ, int MODE = kStep>
 __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>), 1)
     decode_gqa_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                          const DecodeParams p) {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     const int np = kPasses ? p.nhb : 1;
     const int spp = kPasses ? p.Hkv : p.Hkv * p.nhb;
     bool ovf = false;
-    if (warp == 0) ovf = build_prefix(p, TM, spp, LY::ALPHA, P, VP, Ls, lane);
+    if (warp == 0) ovf = build_prefix<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, lane);
     fence_mbar_init();
     tc::tc_fence_before();
     __syncthreads();
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
         for (int k = 0; k < min(NS, n_my); ++k) {
             const int L = Ls[c.b];
             const int t0 = (window_start(L, p.window) / TM + c.tile) * TM;
-            const int n_cache = min(TM, max(0, L - t0));
+            const int n_cache = min(TM, max(0, cached_rows<MODE>(L) - t0));
             if (n_cache > 0) {
                 const size_t rb = static_cast<size_t>(cache_row(p, c.b, c.seg / p.nhb, t0, 0));
                 bulk_prefetch_l2(p.k_cache + rb * D * EBC, static_cast<uint32_t>(n_cache) * D * EBC);
@@ -525,12 +525,12 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     }
     grid_dep_wait();    // inputs, caches and outputs may be in use by the previous launch
     grid_dep_launch();  // the next step may take SMs as this grid's blocks finish
-    if (lengths_changed(p, Ls, lane)) {
+    if (lengths_changed<MODE>(p, Ls, lane)) {
         // (rare) the lengths changed after this block read them: the warps meet, warp 0
         // rebuilds the split from the lengths now visible, they meet again.  If the
         // warps disagree (the lengths changed while the step ran) the meeting gives up:
         // the warp then skips its role, and the others' bounded waits run out.
-        const int r = replan(p, TM, spp, LY::ALPHA, P, VP, Ls, rv);
+        const int r = replan<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, rv);
         const bool ok = r >= 0;
         ovf = r > 0;
         t_begin = split.begin(wid);
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         if (k >= 2 && !tc::wait_or_abort(bar(kBarEmpty8 + s8), ((k >> 1) - 1) & 1, p.err, abort_flag,
                                                          p.wait_cycles))
                             break;
-                        const int n_cache = min(TM, max(0, Ls[cu.b] - t0));
+                        const int n_cache = min(TM, max(0, cached_rows<MODE>(Ls[cu.b]) - t0));
                         const uint32_t sb = static_cast<uint32_t>((n_cache * 4 + 15) & ~15);
                         unsigned char* st8 = stages8 + s8 * round_up(tc::STAGE8, 1024);
                         const uint32_t fb = bar(kBarFull8 + s8);
@@ -666,13 +666,13 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 }
                 // a single new token sits in the last tile; several may start a tile earlier
                 bool has_new = cu.tile == cu.nt - 1;
-                if constexpr (MQ)
+                if constexpr (MQ && MODE != kCross)
                     has_new = Ls[cu.b] < (window_start(Ls[cu.b], p.window) / TM + cu.tile + 1) * TM;
                 if (!I8 && has_new) {
                     // ---- append the new tokens (rows L - t0 ..) and zero staged V rows past the end ----
                     const int L = Ls[cu.b];
                     const int t0 = (window_start(L, p.window) / TM + cu.tile) * TM;
-                    const int n_total = min(TM, L + p.nq - t0);  // rows holding data
+                    const int n_total = min(TM, L + step_nq<MODE>(p) - t0);  // rows holding data
                     const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
                     unsigned char* st = stages + s * tc::STAGE;
                     const int nz = (TM - n_total) * 8;
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         *reinterpret_cast<uint4*>(st + 2 * KB + box * KB + r * 128 + (rem & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
-                    for (int nr = max(0, L - t0); nr < n_total; ++nr) {
+                    for (int nr = MODE == kCross ? n_total : max(0, L - t0); nr < n_total; ++nr) {
                         const int tok = t0 + nr - L, pos = t0 + nr;
                         const bool isv = lane >= 16;  // lanes 0-15: K row, 16-31: V row, 8 elements each
                         const int d0 = (lane & 15) * 8;
@@ -767,8 +767,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 float* ssc = reinterpret_cast<float*>(st8 + 2 * TM * D);  // [K | V][TM]
                 const int L = Ls[cu.b];
                 const int t0 = (window_start(L, p.window) / TM + cu.tile) * TM;
-                bool has_new = cu.tile == cu.nt - 1;
-                if constexpr (MQ) has_new = L < t0 + TM;
+                bool has_new = MODE != kCross && cu.tile == cu.nt - 1;
+                if constexpr (MQ && MODE != kCross) has_new = L < t0 + TM;
                 if (has_new && warp < 4) {  // warp 2 appends K rows, warp 3 V rows
                     const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
                     const int n_total = min(TM, L + p.nq - t0);
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     q_staged = false;
 #pragma unroll
                     for (int jj = 0; jj < GH; ++jj) {
-                        tk[jj] = tkn[jj];
+                        tk[jj] = MODE == kCross ? 0 : tkn[jj];  // (a memory is seen whole by every token)
                         m[jj] = -INFINITY;
                         l[jj] = 0.f;
                         o[jj] = 0.f;
@@ -1011,6 +1011,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 float sc[GH];
                 float vf[GH];  // INT8: the row's V scale, folded into the weight (0 for rows not seen)
                 bool need = false;  // a visible score above the column's reference by more than the margin
+                float* srow = nullptr;  // kScored: this thread's place in its first column's scores
+                if constexpr (MODE == kScored) srow = p.scores + score_row(p, cu.b, kvh, hb * QB + c0) * p.Lmax + t0 + r;
                 float ksr = 1.f, vsr = 1.f;
                 if constexpr (I8) {
                     ksr = scl[(k & 3) * 2 * TM + r];
@@ -1020,6 +1022,10 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 for (int jj = 0; jj < GH; ++jj) {
                     const bool valid = MQ ? (r >= lo0 + tk[jj] && r < hi0 + tk[jj]) : valid0;
                     sc[jj] = valid ? (I8 ? (sh[jj] + sl_[jj]) * ksr : sh[jj] + sl_[jj]) : -INFINITY;
+                    if constexpr (MODE == kScored) {
+                        sc[jj] *= p.sscale;  // (-inf stays -inf: the scale is positive)
+                        if (valid && c0 + jj < QB) srow[static_cast<size_t>(jj) * p.Lmax] = sc[jj];
+                    }
                     vf[jj] = valid ? vsr : 0.f;
                     need |= sc[jj] > m[jj] + tc::kRescaleLog2;  // always when m = -inf and the score is visible
                 }
@@ -1117,8 +1123,12 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     if (piece_first == 0 && last) {
 #pragma unroll
                         for (int jj = 0; jj < GH; ++jj)
-                            if (c0 + jj < QB)
+                            if (c0 + jj < QB) {
                                 store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r, o[jj] / lt[jj]);
+                                if constexpr (MODE == kScored)
+                                    if (r == 0)
+                                        p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] = make_float2(m[jj], 1.f / lt[jj]);
+                            }
                     } else {
                         float* slot = p.ws + static_cast<size_t>(segg + wid) * LY::SLOT;
                         if (r == 0) {
@@ -1173,9 +1183,14 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             }
 #pragma unroll
                             for (int jj = 0; jj < GH; ++jj)
-                                if (c0 + jj < QB)
+                                if (c0 + jj < QB) {
                                     store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r,
                                                Ac[jj] / Ls_[jj]);
+                                    if constexpr (MODE == kScored)
+                                        if (r == 0)
+                                            p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] =
+                                                make_float2(Mx[jj], 1.f / Ls_[jj]);
+                                }
                             if (leader) p.counters[segg] = 0u;
                         }
                         tc::named_bar_sync(1, SMX);
@@ -1214,14 +1229,19 @@ struct TcKernelInfo {
     int threads;  // threads per CTA (tc::threads_for)
 };
 
-template <typename CT, int G, bool MQ>
+template <typename CT, int G, bool MQ, int MODE = kStep>
 TcKernelInfo tc_kernel_info() {
     using LY = tc::Layout<G, std::is_same_v<CT, int8_t>>;
-    return TcKernelInfo{reinterpret_cast<const void*>(&decode_gqa_tc_kernel<CT, G, MQ>), LY::SMEM, LY::SLOT, G,
+    return TcKernelInfo{reinterpret_cast<const void*>(&decode_gqa_tc_kernel<CT, G, MQ, MODE>), LY::SMEM, LY::SLOT, G,
                         tc::threads_for(G, std::is_same_v<CT, int8_t>)};
 }
 
 TcKernelInfo select_tc(bool bf16, int G, bool multi_token);
 TcKernelInfo select_tc_i8(bool multi_token);
+// the same for kScored and kCross, blocks of 8, 16, 32 and 64 query rows
+TcKernelInfo select_tc_scored(bool bf16, int G, bool multi_token);
+TcKernelInfo select_tc_i8_scored(bool multi_token);
+TcKernelInfo select_tc_cross(bool bf16, int G, bool multi_token);
+TcKernelInfo select_tc_i8_cross(bool multi_token);
 
 }  // namespace ftd

@@ -243,6 +243,7 @@ __device__ __forceinline__ void advance(Cursor& cu, const int* P, int segs) {
 // to the tile of position L + nq - 1, times segs), VP[b] the same plus ALPHA per
 // segment, Ls[b] the cached length (-1 for slots without work).  Returns, in every
 // lane, whether some slot has L + nq > Lmax (the caller raises the overflow flag).
+template <int MODE = kStep>
 __device__ __forceinline__ bool build_prefix(const DecodeParams& p, int T, int segs, int alpha, int* P, int* VP,
                                              int* Ls, int lane) {
     constexpr unsigned FULL = 0xffffffffu;
@@ -250,10 +251,12 @@ __device__ __forceinline__ bool build_prefix(const DecodeParams& p, int T, int s
     bool ovf = false;
     for (int base = 0; base < p.B; base += 32) {
         const int b = base + lane;
-        const int L = b < p.B ? __ldcg(p.seq_lens + b) : -1;  // L2: may run before the wait on the previous launch
-        const bool valid = L >= 0 && L <= p.Lmax - p.nq;
-        ovf |= (b < p.B) && (L > p.Lmax - p.nq);
-        int v = valid ? ((L + p.nq - 1) / T + 1 - window_start(L, p.window) / T) * segs : 0;
+        // L2: may run before the wait on the previous launch
+        const int L = b < p.B ? step_len<MODE>(__ldcg(p.seq_lens + b)) : -1;
+        const int nq = step_nq<MODE>(p);
+        const bool valid = L >= 0 && L <= p.Lmax - nq;
+        ovf |= (b < p.B) && (L > p.Lmax - nq);
+        int v = valid ? ((L + nq - 1) / T + 1 - window_start(L, p.window) / T) * segs : 0;
         int vw = v + (valid ? alpha * segs : 0);
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -287,11 +290,12 @@ __device__ __forceinline__ bool build_prefix(const DecodeParams& p, int T, int s
 // may still be writing seq_lens).  So after the wait every warp reads all the
 // lengths again, through L2, and votes.  All warps read the same final values,
 // so they reach the same answer without waiting for one another.
+template <int MODE = kStep>
 __device__ __forceinline__ bool lengths_changed(const DecodeParams& p, const int* Ls, int lane) {
     bool changed = false;
     for (int b = lane; b < p.B; b += 32) {
-        const int L = __ldcg(p.seq_lens + b);
-        changed |= ((L >= 0 && L <= p.Lmax - p.nq) ? L : -1) != Ls[b];
+        const int L = step_len<MODE>(__ldcg(p.seq_lens + b));
+        changed |= ((L >= 0 && L <= p.Lmax - step_nq<MODE>(p)) ? L : -1) != Ls[b];
     }
     return __any_sync(0xffffffffu, changed);
 }
@@ -329,12 +333,13 @@ __device__ __forceinline__ bool warp_rendezvous(int* ctr, int target, long long 
 // disagreed), else whether some slot overflows (meaningful in warp 0).  The
 // tensor-core kernel calls it out of line, which keeps its streaming loops' code
 // as it was; the CUDA-core kernel measured faster with the same steps inline.
+template <int MODE = kStep>
 static __device__ __noinline__ int replan(const DecodeParams& p, int T, int segs, int alpha, int* P, int* VP, int* Ls,
                                           int* rv) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = static_cast<int>(blockDim.x) / 32;
     if (!warp_rendezvous(rv, nw, p.wait_cycles, p.err, lane)) return -1;
     bool ovf = false;
-    if (warp == 0) ovf = build_prefix(p, T, segs, alpha, P, VP, Ls, lane);
+    if (warp == 0) ovf = build_prefix<MODE>(p, T, segs, alpha, P, VP, Ls, lane);
     if (!warp_rendezvous(rv, 2 * nw, p.wait_cycles, p.err, lane)) return -1;
     return ovf ? 1 : 0;
 }
@@ -391,7 +396,7 @@ struct WeightedSplit {
 };
 
 // ================================================================ kernel
-template <typename CT, int D, int G>
+template <typename CT, int D, int G, int MODE = kStep>
 __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk_kernel(const DecodeParams p) {
     using TL = Tiling<CT, D, G>;
     constexpr int T = TL::T, R = TL::R, EPL = TL::EPL, ROW = TL::ROW, SPW = TL::SPW, RB = TL::RB;
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     // After the wait the lengths are checked again (lengths_changed).  Everything
     // that reads the caches' contents or writes memory comes after the wait.
     bool ovf = false;
-    if (warp == 0) ovf = build_prefix(p, T, segs, TL::ALPHA, P, VP, Ls, lane);
+    if (warp == 0) ovf = build_prefix<MODE>(p, T, segs, TL::ALPHA, P, VP, Ls, lane);
     fence_mbar_init();
     __syncthreads();
 
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         for (int k = 0; k < min(NPF, n_my); ++k) {
             const int L = Ls[c.b];
             const int t0 = (window_start(L, p.window) / T + c.tile) * T;
-            const int n_cache = min(T, max(0, L - t0));
+            const int n_cache = min(T, max(0, cached_rows<MODE>(L) - t0));
             if (n_cache > 0) {
                 const size_t rb = static_cast<size_t>(cache_row(p, c.b, c.seg / p.nhb, t0, 0));
                 bulk_prefetch_l2(p.k_cache + rb * ROW, static_cast<uint32_t>(n_cache) * ROW);
@@ -455,11 +460,11 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     }
     grid_dep_wait();    // inputs, caches and outputs may be in use by the previous launch
     grid_dep_launch();  // the next step may take SMs as this grid's blocks finish
-    if (lengths_changed(p, Ls, lane)) {
+    if (lengths_changed<MODE>(p, Ls, lane)) {
         // (rare) the lengths changed after this block read them: the warps meet, warp 0
         // rebuilds the split from the lengths now visible, they meet again
         if (!warp_rendezvous(rv, TL::WARPS, p.wait_cycles, p.err, lane)) return;
-        if (warp == 0) ovf = build_prefix(p, T, segs, TL::ALPHA, P, VP, Ls, lane);
+        if (warp == 0) ovf = build_prefix<MODE>(p, T, segs, TL::ALPHA, P, VP, Ls, lane);
         if (!warp_rendezvous(rv, 2 * TL::WARPS, p.wait_cycles, p.err, lane)) return;
         t_begin = split.begin(wid);
         n_my = split.begin(wid + 1) - t_begin;
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     auto issue = [&](int s, const Cursor& cu) {
         const int L = Ls[cu.b];
         const int t0 = (window_start(L, p.window) / T + cu.tile) * T;
-        const int n_cache = min(T, max(0, L - t0));  // rows before the new tokens come from the cache
+        const int n_cache = min(T, max(0, cached_rows<MODE>(L) - t0));  // rows before the new tokens come from the cache
         const int kvh = cu.seg / p.nhb;
         const long long rb = cache_row(p, cu.b, kvh, t0, pages.page(p, cu.b, t0));
         if (rb < 0) atomicOr(p.err, kErrBadPage);
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     auto prefetch_segment = [&](const Cursor& cu) {
         const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
         const int lines = D * qeb / 128;  // 128-byte lines per row
-        const int nlines = (G + 2 * p.nq) * lines;
+        const int nlines = (MODE == kCross ? G : G + 2 * p.nq) * lines;
         for (int i = lane; i < nlines; i += 32) {
             const int row = i / lines, part = i - row * lines;
             const unsigned char* base;
@@ -550,7 +555,8 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     // q . k runs as dp4a integer dot products with the int8 codes (four products per
     // instruction) and needs no per-byte conversion; relative error about 1.5e-5 of max |q|,
     // the same budget as the tensor-core kernel's hi/lo split.  qsc = s1 / 254.
-    uint32_t qh[G][I8 ? EPL / 4 : 1], ql[G][I8 ? EPL / 4 : 1];
+    // (kScored adds a third level, s1 / 254^2: the weights are kept in fp32.)
+    uint32_t qh[G][I8 ? EPL / 4 : 1], ql[G][I8 ? EPL / 4 : 1], qx[G][I8 && MODE == kScored ? EPL / 4 : 1];
     float qsc[G];
     auto begin_segment = [&](const Cursor& cu) {
         const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
@@ -559,6 +565,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
             const size_t qrow = q_row(p, cu.b, kvh, hb * G + j);
             tk[j] = q_token(p, hb * G + j);
             const int h = kvh * p.group + (hb * G + j - tk[j] * p.group);
+            if constexpr (MODE == kCross) tk[j] = 0;  // every token sees the whole memory
 #pragma unroll
             for (int e = 0; e < EPL; ++e) {
                 const int d = c * EPL + e;
@@ -579,17 +586,24 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
                 const float inv1 = 1.f / s1, inv2 = 254.f / s1;
 #pragma unroll
                 for (int w = 0; w < EPL / 4; ++w) {
-                    uint32_t hw = 0u, lw = 0u;
+                    uint32_t hw = 0u, lw = 0u, xw = 0u;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float x = qr[j][4 * w + k];
                         const int hi = max(-127, min(127, __float2int_rn(x * inv1)));
                         const int lo = max(-127, min(127, __float2int_rn((x - static_cast<float>(hi) * s1) * inv2)));
+                        if constexpr (MODE == kScored) {
+                            const float rem = fmaf(-static_cast<float>(lo), s1 * (1.f / 254.f),
+                                                   fmaf(-static_cast<float>(hi), s1, x));
+                            const int x3 = max(-127, min(127, __float2int_rn(rem * (254.f * inv2))));
+                            xw |= (static_cast<uint32_t>(x3) & 0xffu) << (8 * k);
+                        }
                         hw |= (static_cast<uint32_t>(hi) & 0xffu) << (8 * k);
                         lw |= (static_cast<uint32_t>(lo) & 0xffu) << (8 * k);
                     }
                     qh[j][w] = hw;
                     ql[j][w] = lw;
+                    if constexpr (MODE == kScored) qx[j][w] = xw;
                 }
                 qsc[j] = s1 / 254.f;
             }
@@ -693,6 +707,8 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         for (int j = 0; j < G; ++j) {
             const size_t dst = q_row(p, mc.b, kvh, hb * G + j) * D + lane * DL;
             const float inv = 1.f / Ls_[j];
+            if constexpr (MODE == kScored)
+                if (lane == 0) p.stats[score_row(p, mc.b, kvh, hb * G + j)] = make_float2(Mx[j], inv);
             if constexpr (DL == 4) {
                 store_out4(p, dst, Ac[j][0] * inv, Ac[j][1] * inv, Ac[j][2] * inv, Ac[j][3] * inv);
             } else {
@@ -728,13 +744,13 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         const int L = Ls[cc.b];
         const int pos0 = window_start(L, p.window);  // window start of the first new token
         const int t0 = (pos0 / T + cc.tile) * T;
-        const int n_total = min(T, L + p.nq - t0);   // rows holding data (history or new tokens)
+        const int n_total = min(T, L + step_nq<MODE>(p) - t0);   // rows holding data (history or new tokens)
         const int r_lo = max(0, pos0 - t0);          // rows before the window start are masked
         const bool last_tile = cc.tile == cc.nt - 1;
         const int kvh = cc.seg / p.nhb, hb = cc.seg % p.nhb;
 
         // ---- append: rows at positions L .. L + nq - 1 are the new tokens ----
-        for (int nr = max(0, L - t0); nr < n_total; ++nr) {
+        for (int nr = MODE == kCross ? n_total : max(0, L - t0); nr < n_total; ++nr) {
             const int tok = t0 + nr - L;  // token of this row
             const int pos = t0 + nr;
             const bool isv = hr != 0;   // half-warp 0 writes K, half-warp 1 writes V
@@ -792,7 +808,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         for (int ib = 0; ib < R / RB; ++ib) {
             if constexpr (I8) {
                 // integer partial sums 254 * (hi . k) + (lo . k): |value| < 2^31 for D <= 128
-                int part[G * RB];
+                int part[G * RB], part3[MODE == kScored ? G * RB : 1];
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
                     const int row = 2 * (ib * RB + i) + hr;
@@ -806,19 +822,28 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
                     }
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
-                        int ah = 0, al = 0;
+                        int ah = 0, al = 0, ax = 0;
 #pragma unroll
                         for (int w = 0; w < EPL / 4; ++w) {
                             ah = __dp4a(static_cast<int>(kw[w]), static_cast<int>(qh[j][w]), ah);
                             al = __dp4a(static_cast<int>(kw[w]), static_cast<int>(ql[j][w]), al);
+                            if constexpr (MODE == kScored)
+                                ax = __dp4a(static_cast<int>(kw[w]), static_cast<int>(qx[j][w]), ax);
                         }
                         part[j * RB + i] = ah * 254 + al;
+                        if constexpr (MODE == kScored) part3[j * RB + i] = ax;
                     }
                 }
                 int idx = 0;
                 ReduceScatter<G * RB, 8, int>::run(part, c, idx);
                 const int j = idx / RB, i = idx % RB;
-                sc[j * T + 2 * (ib * RB + i) + hr] = static_cast<float>(part[0]) * qsc[j];
+                float s8 = static_cast<float>(part[0]);
+                if constexpr (MODE == kScored) {
+                    int idx3 = 0;
+                    ReduceScatter<G * RB, 8, int>::run(part3, c, idx3);
+                    s8 = fmaf(static_cast<float>(part3[0]), 1.f / 254.f, s8);
+                }
+                sc[j * T + 2 * (ib * RB + i) + hr] = s8 * qsc[j];
             } else {
                 float part[G * RB];
 #pragma unroll
@@ -850,12 +875,18 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         // its own window start on
         const int hi0 = L + 1 - t0, lo0 = p.window > 0 ? L + 1 - p.window - t0 : -(1 << 30);
         const bool full = hi0 + tk[0] >= T && lo0 + tk[G - 1] <= 0;  // every query row sees every row
+        float* srow = nullptr;  // kScored: this lane's place in the first query row's scores
+        if constexpr (MODE == kScored) srow = p.scores + score_row(p, cc.b, kvh, hb * G) * p.Lmax + t0 + r;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
             float sv = -INFINITY;
             if (full || (r >= lo0 + tk[j] && r < hi0 + tk[j])) {
                 sv = sc[j * T + r];
                 if constexpr (I8) sv *= reinterpret_cast<const float*>(st + 2 * TILE)[r];
+                if constexpr (MODE == kScored) {
+                    sv *= p.sscale;
+                    if (lane < T) srow[static_cast<size_t>(j) * p.Lmax] = sv;
+                }
             }
             float tmax = sv;
 #pragma unroll
@@ -995,6 +1026,8 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
                         const float inv = 1.f / l[j];
+                        if constexpr (MODE == kScored)
+                            if (c == 0) p.stats[score_row(p, cc.b, kvh, hb * G + j)] = make_float2(m[j], inv);
                         const size_t dst = q_row(p, cc.b, kvh, hb * G + j) * D + c * EPL;
 #pragma unroll
                         for (int e4 = 0; e4 < EPL / 4; ++e4)
@@ -1070,28 +1103,28 @@ struct KernelInfo {
     int warps;  // workers (warps) per CTA; the launch uses warps * 32 threads
 };
 
-template <typename CT, int D, int G>
+template <typename CT, int D, int G, int MODE = kStep>
 KernelInfo kernel_info() {
     using TL = Tiling<CT, D, G>;
-    return KernelInfo{reinterpret_cast<const void*>(&decode_splitk_kernel<CT, D, G>), TL::SMEM, TL::T, TL::SLOT, G,
+    return KernelInfo{reinterpret_cast<const void*>(&decode_splitk_kernel<CT, D, G, MODE>), TL::SMEM, TL::T, TL::SLOT, G,
                       TL::WARPS};
 }
 
-template <typename CT>
+template <typename CT, int MODE = kStep>
 KernelInfo select_kernel(int D, int G) {
     if (D == 64) {
         switch (G) {
-            case 1: return kernel_info<CT, 64, 1>();
-            case 2: return kernel_info<CT, 64, 2>();
-            case 4: return kernel_info<CT, 64, 4>();
-            case 8: return kernel_info<CT, 64, 8>();
+            case 1: return kernel_info<CT, 64, 1, MODE>();
+            case 2: return kernel_info<CT, 64, 2, MODE>();
+            case 4: return kernel_info<CT, 64, 4, MODE>();
+            case 8: return kernel_info<CT, 64, 8, MODE>();
         }
     } else if (D == 128) {
         switch (G) {
-            case 1: return kernel_info<CT, 128, 1>();
-            case 2: return kernel_info<CT, 128, 2>();
-            case 4: return kernel_info<CT, 128, 4>();
-            case 8: return kernel_info<CT, 128, 8>();
+            case 1: return kernel_info<CT, 128, 1, MODE>();
+            case 2: return kernel_info<CT, 128, 2, MODE>();
+            case 4: return kernel_info<CT, 128, 4, MODE>();
+            case 8: return kernel_info<CT, 128, 8, MODE>();
         }
     }
     return KernelInfo{nullptr, 0, 0, 0, 0};
@@ -1104,5 +1137,14 @@ KernelInfo select_f32(int D, int G);
 KernelInfo select_f16(int D, int G);
 KernelInfo select_bf16(int D, int G);
 KernelInfo select_i8(int D, int G);
+// the same for the step with scores (kScored) and for cross attention (kCross)
+KernelInfo select_f32_scored(int D, int G);
+KernelInfo select_f16_scored(int D, int G);
+KernelInfo select_bf16_scored(int D, int G);
+KernelInfo select_i8_scored(int D, int G);
+KernelInfo select_f32_cross(int D, int G);
+KernelInfo select_f16_cross(int D, int G);
+KernelInfo select_bf16_cross(int D, int G);
+KernelInfo select_i8_cross(int D, int G);
 
 }  // namespace ftd

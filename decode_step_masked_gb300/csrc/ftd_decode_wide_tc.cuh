@@ -347,7 +347,7 @@ __device__ __forceinline__ void with_qkv_type(int dt, F&& f) {
 // lengths are read again (lengths_changed) while the q loads are in flight, and q is
 // written only when they are unchanged; returns whether they changed.  Out of line:
 // it runs once per piece, and one copy serves every call site.
-template <typename CT, int G, bool MQ>
+template <typename CT, int G, bool MQ, int MODE = kStep>
 static __device__ __noinline__ bool stage_q_fn(const DecodeParams& p, const Cursor c, int st, unsigned char* Qs,
                                                const int* Ls, bool check) {
     bool changed = false;
@@ -357,7 +357,7 @@ static __device__ __noinline__ bool stage_q_fn(const DecodeParams& p, const Curs
         fetch_q<T, G, MQ>(p, c, st, x);
         // the first piece's q loads go out before the producer's first copies (named barrier 3)
         if (check) asm volatile("bar.arrive 3, %0;" ::"r"(wide::kThreads - 32) : "memory");
-        if (check) changed = lengths_changed(p, Ls, threadIdx.x & 31);
+        if (check) changed = lengths_changed<MODE>(p, Ls, threadIdx.x & 31);
         if (!changed) put_q<CT, T, G>(Qs, x, p, st);
     });
     return changed;
@@ -368,12 +368,12 @@ static __device__ __noinline__ bool stage_q_fn(const DecodeParams& p, const Curs
 // rows (rows L - t0 .. of the staged K and V slots, and of the cache when the block is
 // the kv head's first) and zeros in the staged V rows past the end.  Out of line: it
 // runs once per segment.
-template <typename CT>
+template <typename CT, int MODE = kStep>
 static __device__ __noinline__ void append_rows(const DecodeParams& p, unsigned char* kst, unsigned char* vst, int b,
                                                 int seg, int tile, int L, int lane) {
     constexpr int TM = tc::TM, D = tc::D, KB = tc::KB;
     const int t0 = (window_start(L, p.window) / TM + tile) * TM;
-    const int n_total = min(TM, L + p.nq - t0);
+    const int n_total = min(TM, L + step_nq<MODE>(p) - t0);
     const int kvh = seg / p.nhb, hb = seg % p.nhb;
     const int nz = (TM - n_total) * 8;
     for (int c = lane; c < 2 * nz; c += 32) {
@@ -381,7 +381,7 @@ static __device__ __noinline__ void append_rows(const DecodeParams& p, unsigned 
         const int r = n_total + (rem >> 3);
         *reinterpret_cast<uint4*>(vst + box * KB + r * 128 + (rem & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int nr = max(0, L - t0); nr < n_total; ++nr) {
+    for (int nr = MODE == kCross ? n_total : max(0, L - t0); nr < n_total; ++nr) {
         const int tok = t0 + nr - L, pos = t0 + nr;
         const bool isv = lane >= 16;
         const int d0 = (lane & 15) * 8;
@@ -423,7 +423,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
 
 }  // namespace wide
 
-template <typename CT, int G, bool MQ>
+template <typename CT, int G, bool MQ, int MODE = kStep>
 __global__ void __launch_bounds__(wide::kThreads, 1)
     decode_wide_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                           const DecodeParams p) {
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
     const int np = kPasses ? p.nhb : 1;
     const int spp = kPasses ? p.Hkv : p.Hkv * p.nhb;
     bool ovf = false;
-    if (warp == 0) ovf = build_prefix(p, TM, spp, LY::ALPHA, P, VP, Ls, lane);
+    if (warp == 0) ovf = build_prefix<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, lane);
     fence_mbar_init();
     tc::tc_fence_before();
     __syncthreads();
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
         for (int k = 0; k < min(NS, n_my); ++k) {
             const int L = Ls[c.b];
             const int t0 = (window_start(L, p.window) / TM + c.tile) * TM;
-            const int n_cache = min(TM, max(0, L - t0));
+            const int n_cache = min(TM, max(0, cached_rows<MODE>(L) - t0));
             if (n_cache > 0) {
                 const size_t rb = static_cast<size_t>(cache_row(p, c.b, c.seg / p.nhb, t0, 0));
                 bulk_prefetch_l2(p.k_cache + rb * D * 2, static_cast<uint32_t>(n_cache) * D * 2);
@@ -510,22 +510,22 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
         if (leader) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(kQReady)) : "memory");
     };
     auto stage_q = [&](const Cursor& c) {
-        wide::stage_q_fn<CT, G, MQ>(p, c, st, Qs, Ls, false);
+        wide::stage_q_fn<CT, G, MQ, MODE>(p, c, st, Qs, Ls, false);
         publish_q();
     };
     // the softmax warps fetch the first piece's q (as planned) while the lengths are checked
     bool changed;
     if (warp >= 2 && n_my > 0) {
-        changed = wide::stage_q_fn<CT, G, MQ>(p, locate_pass(t_begin, P, p.B, spp, np), st, Qs, Ls, true);
+        changed = wide::stage_q_fn<CT, G, MQ, MODE>(p, locate_pass(t_begin, P, p.B, spp, np), st, Qs, Ls, true);
         if (!changed) publish_q();
     } else {
-        changed = lengths_changed(p, Ls, lane);
+        changed = lengths_changed<MODE>(p, Ls, lane);
         // the producer issues its first copies once the softmax warps' q loads are out
         if (warp == 0 && n_my > 0) tc::named_bar_sync(3, wide::kThreads - 32);
     }
     if (changed) {
         // (rare) the lengths changed after this block read them: re-plan, as in the narrow kernel
-        const int pr = replan(p, TM, spp, LY::ALPHA, P, VP, Ls, rv);
+        const int pr = replan<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, rv);
         const bool ok = pr >= 0;
         ovf = pr > 0;
         t_begin = split.begin(wid);
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                 if (ks < n_my) {
                     const bool new_piece = (ks == 0) || (cu.tile == 0);
                     bool has_new = cu.tile == cu.nt - 1;
-                    if constexpr (MQ)
+                    if constexpr (MQ && MODE != kCross)
                         has_new = Ls[cu.b] < (window_start(Ls[cu.b], p.window) / TM + cu.tile + 1) * TM;
                     const bool patch_v = has_new || (cu.tile == 0 && p.window > 0);  // the V tile is written here
                     const int s = ks % NS;
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                             __syncwarp();
                         }
                         if (has_new) {
-                            wide::append_rows<CT>(p, stages + s * 2 * KB, stages + LY::OFF_V + (ks % NSV) * 2 * KB, cu.b,
+                            wide::append_rows<CT, MODE>(p, stages + s * 2 * KB, stages + LY::OFF_V + (ks % NSV) * 2 * KB, cu.b,
                                                   cu.seg, cu.tile, Ls[cu.b], lane);
                             fence_proxy_async_smem();
                             __syncwarp();
@@ -772,8 +772,8 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
             Cursor cu = locate_pass(t_begin, P, p.B, spp, np);
             // token of owned query row jj of head block hb (0 unless several new tokens per step)
             auto tok_of = [&](int hb, int jj) -> int {
-                if constexpr (MQ) return c0 + jj < QB ? q_token(p, hb * QB + c0 + jj) : 0;
-                return 0;
+                if constexpr (MQ && MODE != kCross) return c0 + jj < QB ? q_token(p, hb * QB + c0 + jj) : 0;
+                return 0;  // (a memory is seen whole by every token)
             };
             auto orow = [&](int b, int kvh, int qi) -> size_t {
                 if constexpr (MQ) return q_row(p, b, kvh, qi);
@@ -836,6 +836,14 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                     const uint32_t scol = static_cast<uint32_t>((k & 1) * G);
                     float pq[GH];  // weights against the current references, kept until the vote
                     ld_rows(scol, pq);
+                    if constexpr (MODE == kScored) {
+                        float* srow = p.scores + score_row(p, cu.b, kvh, hb * QB + c0) * p.Lmax + t0 + r;
+#pragma unroll
+                        for (int jj = 0; jj < GH; ++jj) {
+                            pq[jj] *= p.sscale;
+                            if (full || visible(jj)) srow[static_cast<size_t>(jj) * p.Lmax] = pq[jj];
+                        }
+                    }
                     if (!full) {
 #pragma unroll
                         for (int jj = 0; jj < GH; ++jj)
@@ -870,6 +878,10 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                         {
                             float sc[GH];
                             ld_rows(scol, sc);
+                            if constexpr (MODE == kScored) {
+#pragma unroll
+                                for (int jj = 0; jj < GH; ++jj) sc[jj] *= p.sscale;
+                            }
                             if (!full) {
 #pragma unroll
                                 for (int jj = 0; jj < GH; ++jj)
@@ -886,6 +898,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
 #pragma unroll
                             for (int i8 = 0; i8 < 8; ++i8) {
                                 const int jj = j8 + i8, j = c0 + jj;
+                                if constexpr (MODE == kScored) sc[i8] *= p.sscale;
                                 if (!full && !visible(jj)) sc[i8] = -INFINITY;
                                 const float tmax = fmaxf(fmaxf(red_max[j], red_max[G + j]),
                                                          fmaxf(red_max[2 * G + j], red_max[3 * G + j]));
@@ -1038,6 +1051,8 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                     }
                 }
                 if (fin) {
+                    if constexpr (MODE == kScored)
+                        if (st < QB) p.stats[score_row(p, cu.b, kvh, hb * QB + st)] = make_float2(mrg[st], 1.f / mrg[G + st]);
                     // the block's rows: O / l, one 16-byte store per 4 dimensions
 #pragma unroll 1
                     for (int idx = st; idx < QB * (D / 4); idx += SMX) {
@@ -1073,10 +1088,10 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
     }
 }
 
-template <typename CT, int G, bool MQ>
+template <typename CT, int G, bool MQ, int MODE = kStep>
 TcKernelInfo wide_kernel_info() {
     using LY = wide::Layout<G>;
-    return TcKernelInfo{reinterpret_cast<const void*>(&decode_wide_tc_kernel<CT, G, MQ>), LY::SMEM, LY::SLOT, G,
+    return TcKernelInfo{reinterpret_cast<const void*>(&decode_wide_tc_kernel<CT, G, MQ, MODE>), LY::SMEM, LY::SLOT, G,
                         wide::kThreads};
 }
 

@@ -15,7 +15,10 @@ struct TcChoice {
     int nhb;
     int qblk;
 };
-TcChoice choose_tc(const ftd_config& c);
+TcChoice choose_tc(const ftd_config& c, int mode = kStep);
+
+// The CUDA-core kernel for blocks of G query rows of head_dim D on cache type dt.
+KernelInfo choose_cc(ftd_dtype dt, int D, int G, int mode);
 
 // What a valid configuration runs: the CUDA-core kernel's block of G query rows
 // (nhb blocks per kv head) and its instantiation, the tensor-core choice, and

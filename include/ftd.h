@@ -320,6 +320,140 @@ ftd_status ftd_debug_stall_next(ftd_ctx* ctx, int calls);
  */
 ftd_status ftd_debug_late_lengths(const int32_t* src, int32_t* dst, int n, int delay_us, void* stream);
 
+/*
+ * Operators around the step: rotary positions before it, the step that also
+ * accumulates attention weights, the eviction by those weights, and cross
+ * attention.  They take the context's shapes, types and caches, follow the
+ * conventions above, launch on the caller's stream without allocating or
+ * synchronising, and may be captured into a graph (after one call of
+ * ftd_enable_scores, and of ftd_cross_mha, outside the capture).  Calls on one
+ * context must not overlap in time, whichever entry points they are: graphs
+ * captured from one context share its workspace too.
+ */
+
+enum { FTD_ROPE_HALVES = 0, FTD_ROPE_ADJACENT = 1 };
+enum { FTD_ROPE_SECTIONS = 0, FTD_ROPE_INTERLEAVED = 1 };
+
+typedef struct {
+    int n_axes;       /* position axes (time, height, width, ...): 1 .. 4 */
+    int rotary_dim;   /* R: the first R elements of a head turn, the others pass; even, 0 = head_dim */
+    int section[4];   /* pairs that follow each axis; together R / 2 (one axis: 0 stands for R / 2) */
+    int pairing;      /* FTD_ROPE_HALVES: pair i is elements (i, i + R/2); FTD_ROPE_ADJACENT: (2i, 2i + 1) */
+    int order;        /* FTD_ROPE_SECTIONS: the first section[0] pairs follow axis 0, the next section[1] axis 1, ...;
+                         FTD_ROPE_INTERLEAVED: pairs go to the axes in turn, an axis whose section is full is passed over */
+    double theta;     /* pair i turns theta^(-2i/R) radians per position; 0 = 10000 */
+    const double* inv_freq;  /* host, R / 2 radians per position that replace theta's; NULL: theta */
+} ftd_rope_config;
+
+/*
+ * ftd_set_rope -- the rotary positions that ftd_rope_qkv applies on this context.
+ * Copies what cfg holds (host work only); may be called again.  INVALID_ARG for
+ * sizes that do not fit, leaving the previous setting.
+ */
+ftd_status ftd_set_rope(ftd_ctx* ctx, const ftd_rope_config* cfg);
+
+/*
+ * ftd_rope_qkv -- bias and rotary positions for n_tokens tokens, those of a step
+ * (B * T in the order of q) or of a prompt, ahead of ftd_decode_mha (which is then
+ * called without a bias) or of a cache fill:
+ *   x = in + bias (one fp32 add);  for pair i, (a, b) of a query or key head, with
+ *   w = positions[axis(i)][token] * inv_freq[i]:
+ *   out_a = a cos w - b sin w,  out_b = b cos w + a sin w,
+ * in fp32, rounded once to the qkv type.  Angles are wrapped exactly, so far
+ * positions keep their full accuracy; positions may be negative.  Value heads only
+ * take the bias.
+ *   q, k, v   : device, qkv dtype; token t's heads at q + t * q_stride and k, v +
+ *               t * kv_stride elements (0: dense rows), so a fused projection's
+ *               [n][(Hq + 2 Hkv) * D] output is passed as three pointers into it.
+ *               v and v_out may both be NULL.
+ *   qkv_bias  : device [(Hq + 2 Hkv) * D] or NULL.
+ *   positions : device int32 [n_axes][n_tokens].
+ *   q_out, k_out, v_out : device, dense [n_tokens][Hq][D] and [n_tokens][Hkv][D]; each
+ *               may be its own dense input.  Other overlaps are refused.
+ * Pointers need the alignment of their elements; with 16-byte aligned pointers and
+ * strides, and R / 2 a multiple of 8 (fp32: 4), the kernel moves 16 bytes at a time.
+ * n_tokens 0 launches nothing.
+ */
+ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,
+                        int64_t kv_stride, const void* qkv_bias, const int32_t* positions, int64_t n_tokens,
+                        void* q_out, void* k_out, void* v_out, void* stream);
+
+/*
+ * ftd_enable_scores -- allocate the workspace of ftd_decode_mha_scored and
+ * ftd_cache_evict: 4 bytes per (query row, cache position) of the context, 4 more
+ * per (kv head, position) and some constants.  One cudaMalloc, freed by
+ * ftd_destroy; clearing runs on `stream`.  A second call does nothing.
+ */
+ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream);
+
+/*
+ * ftd_decode_mha_scored -- the step of ftd_decode_mha (of ftd_decode_mha_paged on a
+ * paged context), which also adds each position's attention weight to a plane:
+ *   acc_out[b][h][t] = (t < L_b ? acc[b][h][t] : 0) + sum of p_t over the T * Hq / Hkv
+ *   query rows of kv head h, for t = 0 .. L_b + T - 1,
+ * in fp32 and in a fixed order.  A row whose window or causal limit hides t adds
+ * nothing there.  With T > 1 every token's row counts, also of tokens that the
+ * caller then rejects.
+ *   block_table : as in ftd_decode_mha_paged; NULL on a contiguous context.
+ *   acc       : device fp32 plane laid out like one INT8 scale plane: [B][Hkv][Lmax],
+ *               paged [num_pages][Hkv][page_size]; 16-byte aligned.
+ *   acc_out   : the same, NULL or acc: in place.  Entries past L_b + T - 1, and
+ *               slots without work, keep what they hold.
+ *   positions : device int32 plane of the same layout, or NULL: the new rows' entries
+ *               become next_pos[b] + j (every kv head's).  Older entries are kept.
+ *   next_pos  : device int32 [B], the sequence position of the slot's first new token
+ *               (L_b as long as nothing was evicted); needed with positions.
+ * Other arguments, out and the sticky errors as in ftd_decode_mha.  Launches two kernels.
+ */
+ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
+                                 const void* qkv_bias, void* k_cache, void* v_cache, const int32_t* block_table,
+                                 const int32_t* seq_lens, float* scales, const int32_t* next_pos, const float* acc,
+                                 float* acc_out, int32_t* positions, void* out, void* stream);
+
+/*
+ * ftd_cache_evict -- bring every slot with more than `budget` cached rows down to
+ * budget, each kv head by its own weights.  Of its L_b = seq_lens[b] rows a head keeps
+ *   first those whose position is below `sinks` or at least next_pos[b] - `recent`,
+ *   then the largest acc (NaN below all), equal ones by the lower row.
+ * Rows are not kept in order: the j-th kept row at index >= budget moves into the
+ * j-th row below budget that is not kept, K and V (INT8: and their scales), weight
+ * and position; no other row moves, and rows from budget on keep their old content.
+ * Attention does not depend on the order (positions are in K), so ftd_decode_mha runs
+ * on from new_lens; on a paged context the pages past them are free to reuse.
+ *   k_cache, v_cache, scales, block_table : as in ftd_decode_mha / _paged (NULL caches
+ *               and scales: the pool).
+ *   acc, positions : planes as in ftd_decode_mha_scored, 4-byte aligned.
+ *   acc_out, positions_out : planes that take the kept rows' entries 0 .. new length - 1;
+ *               NULL or the input plane: in place.
+ *   new_lens  : device int32 [B], may be seq_lens: budget, or L_b where that is no more.
+ * Inactive slots (L_b < 0) are left alone; L_b > Lmax raises FTD_ERR_SEQ_OVERFLOW, a
+ * bad table entry FTD_ERR_BAD_PAGE (that slot's rows stay where they are, its length
+ * and planes are undefined).  Needs 1 <= budget <= Lmax and recent + sinks <= budget, a
+ * context without a window, and Lmax up to 2^20 (UNSUPPORTED above).  Launches two kernels.
+ */
+ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* scales, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* next_pos, const float* acc, float* acc_out,
+                           const int32_t* positions, int32_t* positions_out, int32_t* new_lens, int budget,
+                           int recent, int sinks, void* stream);
+
+/*
+ * ftd_cross_mha -- cross attention of the T = q_len tokens (or beams) of every slot to
+ * an encoder's states, kept as K and V rows in the layout of a cache:
+ *   out[b][j][h] = softmax(scale * (q[b][j][h] + q_bias[h]) . K_mem[b][h'][0 .. M_b - 1]) V_mem,
+ * M_b = mem_lens[b], h' the kv head of h.  Nothing is appended, every token sees the
+ * whole memory, and the tokens of a slot share one pass over it.
+ *   q        : device [B][T][Hq][D], out [B][T][Hq][D] of out_dtype.
+ *   q_bias   : device [Hq * D] or NULL.
+ *   k_mem, v_mem : device [B][Hkv][Lmax][D] of the cache dtype, read only (INT8: with
+ *              scales [2][B][Hkv][Lmax]); NULL: the context's pool.  Rows from M_b on
+ *              may hold anything.
+ *   mem_lens : device int32 [B].  M_b <= 0 gives zeros; M_b > Lmax gives zeros and
+ *              raises FTD_ERR_SEQ_OVERFLOW.
+ * Runs on any context without pages and without a window.  Launches one kernel.
+ */
+ftd_status ftd_cross_mha(ftd_ctx* ctx, const void* q, const void* q_bias, const void* k_mem, const void* v_mem,
+                         const int32_t* mem_lens, const float* scales, void* out, void* stream);
+
 /* Size of the fixed device array that ftd_decode_mha_noalloc uses as scratch. */
 #define FTD_NOALLOC_SCRATCH_BYTES (8u << 20)
 
