@@ -102,6 +102,14 @@ __device__ __forceinline__ int cached_rows(int L) {
     if constexpr (MODE == kCross) return L + 1;
     return L;
 }
+// Scale of an INT8 row from its largest magnitude (0: 1).  The step divides by 127; the scored
+// step multiplies by the fp32 value of 1 / 127, within an ulp of that.
+template <int MODE>
+__device__ __forceinline__ float i8_row_scale(float amax) {
+    if (amax == 0.f) return 1.f;
+    if constexpr (MODE == kScored) return amax * (1.f / 127.f);
+    return __fdiv_rn(amax, 127.f);
+}
 // kScored: index of the score and statistics row of query row qi of (b, kvh).
 __device__ __forceinline__ size_t score_row(const DecodeParams& p, int b, int kvh, int qi) {
     return (static_cast<size_t>(b) * p.Hkv + kvh) * (p.nq * p.group) + qi;

@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             amax = fmaxf(amax, fabsf(x[e]));
                         }
                         amax = warp_max(amax);
-                        const float qs = amax == 0.f ? 1.f : __fdiv_rn(amax, 127.f);
+                        const float qs = i8_row_scale<MODE>(amax);
                         uint32_t w = 0u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {

@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
                 for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
                 for (int mm = 8; mm >= 1; mm >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, mm));
-                const float qs = amax == 0.f ? 1.f : __fdiv_rn(amax, 127.f);
+                const float qs = i8_row_scale<MODE>(amax);
                 uint32_t w[EPL / 4];
 #pragma unroll
                 for (int k4 = 0; k4 < EPL / 4; ++k4) w[k4] = 0u;

@@ -403,7 +403,10 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream);
  *               become next_pos[b] + j (every kv head's).  Older entries are kept.
  *   next_pos  : device int32 [B], the sequence position of the slot's first new token
  *               (L_b as long as nothing was evicted); needed with positions.
- * Other arguments, out and the sticky errors as in ftd_decode_mha.  Launches two kernels.
+ * Other arguments, out and the sticky errors as in ftd_decode_mha, and so are the
+ * appended rows, but for an INT8 row's scale: absmax * (1 / 127) in fp32 here, at most an
+ * ulp from ftd_decode_mha's absmax / 127 (codes are round(k' / scale) in both, so one that
+ * lies on a rounding border can differ by 1).  Launches two kernels.
  */
 ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
                                  const void* qkv_bias, void* k_cache, void* v_cache, const int32_t* block_table,
@@ -429,7 +432,7 @@ ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new,
  * Inactive slots (L_b < 0) are left alone; L_b > Lmax raises FTD_ERR_SEQ_OVERFLOW, a
  * bad table entry FTD_ERR_BAD_PAGE (that slot's rows stay where they are, its length
  * and planes are undefined).  Needs 1 <= budget <= Lmax and recent + sinks <= budget, a
- * context without a window, and Lmax up to 2^20 (UNSUPPORTED above).  Launches two kernels.
+ * context without a window, and Lmax up to 2^30 (UNSUPPORTED above).  Launches two kernels.
  */
 ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* scales, const int32_t* block_table,
                            const int32_t* seq_lens, const int32_t* next_pos, const float* acc, float* acc_out,

@@ -78,6 +78,18 @@ def weights(w, q, k, lo, hi):
     return p / p.sum(axis=1, keepdims=True), mass
 
 
+def appended_i8(w, inp, b, which):
+    """Codes [Hkv][T][D] and scales [Hkv][T] of slot b's new rows: the scored step's quantiser in fp32."""
+    x = np.asarray(widen(inp[which + "_new"][b], w.qkv_dtype), np.float32).reshape(-1, w.Hkv, w.D)
+    if inp.get("bias") is not None:
+        o = (w.Hq + (w.Hkv if which == "v" else 0)) * w.D
+        x = x + np.asarray(widen(inp["bias"], w.qkv_dtype), np.float32)[o:o + w.Hkv * w.D].reshape(w.Hkv, w.D)
+    x = x.transpose(1, 0, 2)
+    top = np.abs(x).max(axis=-1)
+    s = np.where(top == 0, np.float32(1), top * (np.float32(1) / np.float32(127))).astype(np.float32)
+    return np.clip(np.rint(x / s[..., None]), -127, 127).astype(np.int8), s
+
+
 def added_weights(w, inp, k_after, scales_after, b, window=0):
     """Sum over the query rows of each kv head of slot b's weights, [Hkv][L + T], and the largest mass."""
     L, T, g = int(inp["seq_lens"][b]), w.q_len, w.Hq // w.Hkv

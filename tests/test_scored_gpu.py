@@ -9,7 +9,7 @@ import decode_step_masked_gb300 as ftd
 import oracle
 from tests import operators_ref as ref
 from tests.gpu_util import (assert_close, assert_same_bytes, dev, from_pages, host, make_step, page_layout, rising_scores,
-                            to_pages)
+                            to_pages, valid_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -122,9 +122,18 @@ def check(w, inp, window=0, cc=False, page=0, **kw):
     r = oracle.load().decode_step(w, inp, nthreads=8, window=window)
     out, kv, scg, status = run(w, inp, window=window, cc=cc, page=page, **kw)
     assert status == (ftd.FTD_ERR_SEQ_OVERFLOW if r["overflow"] else ftd.FTD_OK)
-    if not page:
-        assert_same_bytes(kv["k"], r["k_cache"], "K after append")
-        assert_same_bytes(kv["v"], r["v_cache"], "V after append")
+    want = dict(k=r["k_cache"].copy(), v=r["v_cache"].copy())
+    if w.cache_dtype == "i8":  # this step's row scale is its own
+        scales = inp["scales"].copy()
+        for b, L in enumerate(inp["seq_lens"]):
+            if 0 <= L <= w.Lmax - w.q_len:
+                for i, n in enumerate("kv"):
+                    want[n][b, :, L:L + w.q_len], scales[i, b, :, L:L + w.q_len] = ref.appended_i8(w, inp, b, n)
+                    assert_same_bytes(scg[i, b, :, :L + w.q_len], scales[i, b, :, :L + w.q_len], f"{n} scales after append")
+    if page:
+        want = {n: valid_rows(w, a, inp["seq_lens"], q_len=w.q_len) for n, a in want.items()}
+    for n in "kv":
+        assert_same_bytes(kv[n], want[n], f"{n} after append")
     assert_close(out.double().cpu().numpy().reshape(r["out"].shape), r["out"], i8=w.cache_dtype == "i8")
 
 
