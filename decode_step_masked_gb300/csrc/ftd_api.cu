@@ -1025,8 +1025,7 @@ ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* sc
     const ftd_config& c = ctx->cfg;
     if (c.window > 0)
         return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: rows change places, which a sliding window cannot follow");
-    if (c.max_len > ftd::kMaxEvictLen)
-        return fail(FTD_ERR_UNSUPPORTED, "ftd_cache_evict: max_len %d above %d", c.max_len, ftd::kMaxEvictLen);
+    if (c.max_len > 1 << 30) return fail(FTD_ERR_UNSUPPORTED, "ftd_cache_evict: max_len %d above 2^30", c.max_len);
     if (!seq_lens || !next_pos || !acc || !positions || !new_lens)
         return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: seq_lens, next_pos, acc, positions and new_lens must be non-NULL");
     if (!aligned(seq_lens, 4) || !aligned(next_pos, 4) || !aligned(acc, 4) || !aligned(acc_out, 4) ||

@@ -8,27 +8,33 @@
 // Rows move from [budget, L) to [0, budget), so no row is read and written, every move
 // can run at the same time, and only rows that must move do.
 //
-// select_kernel, one block per (slot, kv head): the weights become 32-bit keys whose
-// unsigned order is theirs; the budget-th largest key is found two bits at a time, by
-// counting, over keys held in shared memory, the four values of the next two bits among
-// the keys that match the bits found so far (counts are sums: no atomics, any order gives
-// the same result), at most 16 rounds of one block barrier each.  Then two more
-// sweeps rank ties and list the moves.  A block reserves its part of the call's one move
-// list with an atomic add; the list's order varies, but its moves are independent.
-// move_kernel splits the list evenly over all warps and copies rows and their planes.
+// select_kernel, one cluster of 1 to 8 blocks per (slot, kv head), each block with a
+// contiguous part of the rows: the weights become 32-bit keys whose unsigned order is
+// theirs, held in shared memory; the budget-th largest is found eight bits at a time
+// (histograms of the next byte among the keys that match so far, added up over the
+// cluster through distributed shared memory: sums, so any order of the atomics gives the
+// same result), in at most four rounds.  Then the moves are listed in row order
+// (ranks by ballots, warp and block prefixes).  The cluster reserves its part of the
+// call's one move list with an atomic add; the list's order varies, its moves are independent.
+// move_kernel deals the list out to all warps in chunks of rows and copies rows and planes.
 //
 // Bound: 8 bytes per position for the selection, then the moved rows, read and written.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "ftd_ops.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace ftd {
 namespace {
 
-constexpr int kThreadsE = 1024;
+constexpr int kThreadsE = 512;
 constexpr int kWarpsE = kThreadsE / 32;
-constexpr int kSmemKeys = 48 * 1024;  // keys that fit shared memory (192 KB)
+constexpr int kMaxCluster = 8;
+constexpr int kSmemKeys = 48 * 1024;  // keys of a block that fit shared memory (192 KB)
 constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 8;  // rows a warp copies at a time
 
 __device__ __forceinline__ long long evict_row(const EvictParams& p, int b, int kvh, int t) {
     if (!p.block_table) return (static_cast<long long>(b) * p.Hkv + kvh) * p.Lmax + t;
@@ -44,26 +50,43 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+// What the blocks of a cluster read of each other.
+struct alignas(16) Shared {
+    uint32_t hist[2][256];
+    int ties, holes, movers;  // of this block
+    uint32_t list_base;       // of the cluster (block 0's)
+    int bad;
+};
+
 __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) {
     extern __shared__ __align__(16) uint32_t skeys[];
-    __shared__ uint2 cnt[2][kWarpsE];
+    __shared__ Shared sh;
     __shared__ int wsum[kWarpsE], wsum2[kWarpsE];
-    __shared__ uint32_t list_base;
+    __shared__ int found[3];  // digit, rows needed of it, keys with it
     constexpr unsigned FULL = 0xffffffffu;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int cl = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seg = blockIdx.x, b = seg / p.Hkv, kvh = seg - b * p.Hkv;
+    const int seg = blockIdx.x / cl, b = seg / p.Hkv, kvh = seg - b * p.Hkv;
+    // every thread of the cluster (or, alone, of the block) has written what it shares
+    auto meet = [&]() {
+        if (cl > 1) cluster.sync();
+        else __syncthreads();
+    };
+    if (tid < 256) sh.hist[0][tid] = 0u;
+    if (tid == 0) sh.bad = 0;
     grid_dep_wait();
     grid_dep_launch();
     const int L = __ldcg(p.seq_lens + b);
     if (L <= 0) return;
     if (L > p.Lmax) {
-        if (tid == 0) atomicOr(p.err, kErrSeqOverflow);
+        if (tid == 0 && rank == 0) atomicOr(p.err, kErrSeqOverflow);
         return;
     }
     const bool apart = p.acc_out != p.acc, papart = p.positions_out != p.positions;
     if (L <= p.budget) {  // everything stays
         if (apart || papart)
-            for (int t = tid; t < L; t += kThreadsE) {
+            for (int t = rank * kThreadsE + tid; t < L; t += cl * kThreadsE) {
                 const long long row = evict_row(p, b, kvh, t);
                 if (row < 0) {
                     atomicOr(p.err, kErrBadPage);
@@ -74,69 +97,117 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
             }
         return;
     }
-    // ---- keys; a warp owns a contiguous run of positions ----
-    uint32_t* keys = L <= kSmemKeys ? skeys : p.keys + static_cast<size_t>(seg) * p.Lmax;
-    const int S = ((L + kWarpsE - 1) / kWarpsE + 31) & ~31;
-    const int w0 = min(L, warp * S), w1 = min(L, w0 + S);
+    // ---- keys; a warp owns a contiguous run of S rows, a block the runs of its warps ----
+    const int S = ((L + cl * kWarpsE - 1) / (cl * kWarpsE) + 31) & ~31;
+    const int c0 = rank * kWarpsE * S;  // the block's first row (may lie past L)
+    const int w0 = min(L, c0 + warp * S), w1 = min(L, w0 + S);
+    // keys[t] for row t of this block
+    uint32_t* keys = (S * kWarpsE <= p.smem_keys ? skeys : p.keys + static_cast<size_t>(seg) * p.Lmax + min(c0, L)) - min(c0, L);
     const long long fresh = static_cast<long long>(__ldcg(p.next_pos + b)) - p.recent;
     bool bad = false;
-    for (int t = w0 + lane; t < w1; t += 32) {
-        const long long row = evict_row(p, b, kvh, t);
-        uint32_t key = 0u;
-        if (row < 0) {
-            bad = true;
-        } else {
-            const int pos = p.positions[row];
-            key = ((pos >= 0 && pos < p.sinks) || (p.recent > 0 && pos >= fresh)) ? 0xffffffffu : weight_key(p.acc[row]);
-        }
-        keys[t] = key;
-    }
-    if (__syncthreads_or(bad)) {  // a page of this slot is bad: it is left as it is
-        if (tid == 0) atomicOr(p.err, kErrBadPage);
-        return;
-    }
-    // ---- the budget-th largest key ----
-    uint32_t prefix = 0u;     // bits found so far (from the top)
-    int need = p.budget;      // kept rows still to be found among the keys with this prefix
-    int shift = 30;
-    bool whole = false;       // every key with the prefix is kept
-    for (;;) {
-        // counts of the next two bits' values, 16 bits each: a warp's run is at most
-        // kMaxEvictLen / 32 = 32768 keys
-        uint32_t c01 = 0u, c23 = 0u;
-        const bool first = shift == 30;
-        for (int t = w0 + lane; t < w1; t += 32) {
-            const uint32_t k = keys[t];
-            if (first || (k >> (shift + 2)) == prefix) {
-                const uint32_t d = (k >> shift) & 3u;
-                const uint32_t one = (d & 1u) ? 0x10000u : 1u;
-                if (d & 2u) c23 += one;
-                else c01 += one;
+    constexpr int U = 4;  // rows a lane has in flight
+    for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
+        float a[U];
+        int ps[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 32 * u;
+            a[u] = 0.f;
+            ps[u] = 0;
+            if (t < w1) {
+                const long long row = evict_row(p, b, kvh, t);
+                if (row < 0) {
+                    bad = true;
+                } else {
+                    a[u] = p.acc[row];
+                    ps[u] = p.positions[row];
+                }
             }
         }
-        c01 = __reduce_add_sync(FULL, c01);
-        c23 = __reduce_add_sync(FULL, c23);
-        const int buf = (shift >> 1) & 1;
-        if (lane == 0) cnt[buf][warp] = make_uint2(c01, c23);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 32 * u;
+            if (t < w1)
+                keys[t] = ((ps[u] >= 0 && ps[u] < p.sinks) || (p.recent > 0 && ps[u] >= fresh)) ? 0xffffffffu : weight_key(a[u]);
+        }
+    }
+    if (bad) sh.bad = 1;
+    __syncthreads();
+    // ---- the budget-th largest key, a byte at a time from the top ----
+    uint32_t prefix = 0u;  // bytes found so far
+    int need = p.budget;   // kept rows still to be found among the keys with this prefix
+    int shift = 24;
+    bool whole = false;    // every key with the prefix is kept
+    for (int round = 0;; ++round) {
+        uint32_t* hist = sh.hist[round & 1];
+        for (int t = w0 + lane; t < w1; t += 32) {
+            const uint32_t k = keys[t];
+            if (round == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        }
+        meet();
+        if (round == 0) {
+            int any = 0;
+            for (int r = 0; r < cl; ++r) any |= cl > 1 ? *cluster.map_shared_rank(&sh.bad, r) : sh.bad;
+            if (any) {  // a page of this slot is bad: it is left as it is
+                if (tid == 0 && rank == 0) atomicOr(p.err, kErrBadPage);
+                meet();  // no block leaves while another reads its flag
+                return;
+            }
+        }
+        if (tid < 256) sh.hist[(round + 1) & 1][tid] = 0u;  // (read last before this meeting)
+        if (warp == 0) {
+            // lane owns bytes 8 lane .. 8 lane + 7; keys above them: those of the later lanes
+            uint32_t h[8] = {};
+            for (int r = 0; r < cl; ++r) {
+                const uint32_t* rh = cl > 1 ? cluster.map_shared_rank(hist, r) : hist;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(rh + 8 * lane + 4 * i);
+                    h[4 * i] += x.x;
+                    h[4 * i + 1] += x.y;
+                    h[4 * i + 2] += x.z;
+                    h[4 * i + 3] += x.w;
+                }
+            }
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += static_cast<int>(h[i]);
+            int incl = sum;  // of this lane and the later ones
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int y = __shfl_down_sync(FULL, incl, m);
+                if (lane + m < 32) incl += y;
+            }
+            int left = need - (incl - sum);  // still needed when this lane's bytes are reached
+            if (left > 0 && left <= sum) {
+#pragma unroll
+                for (int i = 7; i >= 0; --i) {
+                    const int n = static_cast<int>(h[i]);
+                    if (left > 0 && left <= n) {
+                        found[0] = 8 * lane + i;
+                        found[1] = left;
+                        found[2] = n;
+                    }
+                    left -= n;
+                }
+            }
+        }
         __syncthreads();
-        const uint2 x = cnt[buf][lane];
-        const int n1 = static_cast<int>(__reduce_add_sync(FULL, x.x >> 16));
-        const int n2 = static_cast<int>(__reduce_add_sync(FULL, x.y & 0xffffu));
-        const int n3 = static_cast<int>(__reduce_add_sync(FULL, x.y >> 16));
-        const int n0 = static_cast<int>(__reduce_add_sync(FULL, x.x & 0xffffu));
-        int d, n;
-        if (need <= n3) { d = 3; n = n3; }
-        else if (need <= n3 + n2) { d = 2; n = n2; need -= n3; }
-        else if (need <= n3 + n2 + n1) { d = 1; n = n1; need -= n3 + n2; }
-        else { d = 0; n = n0; need -= n3 + n2 + n1; }
-        prefix = (prefix << 2) | static_cast<uint32_t>(d);
-        whole = need == n;
+        prefix = (prefix << 8) | static_cast<uint32_t>(found[0]);
+        need = found[1];
+        whole = need == found[2];
         if (whole || shift == 0) break;
-        shift -= 2;
+        shift -= 8;
     }
     const uint32_t lo = prefix << shift;  // the smallest key with the prefix
-    // ---- ties: the first `need` keys equal to lo, by row index ----
-    int ties_before = 0;  // in earlier warps
+    // exclusive prefix of v over the block's warps, and the block's sum (after a barrier)
+    auto over_warps = [&](const int* w, int& before, int& sum) {
+        const int v = lane < kWarpsE ? w[lane] : 0;
+        before = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < warp ? v : 0)));
+        sum = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(v)));
+    };
+    // ---- ties: the first `need` keys equal to lo, by row ----
+    int ties_before = 0, sum;
     if (!whole) {
         int n = 0;
         for (int t0 = w0; t0 < w1; t0 += 32) {
@@ -145,9 +216,14 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
         }
         if (lane == 0) wsum[warp] = n;
         __syncthreads();
-        const int v = wsum[lane];
-        ties_before = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < warp ? v : 0)));
-        __syncthreads();
+        over_warps(wsum, ties_before, sum);
+        if (cl > 1) {
+            if (tid == 0) sh.ties = sum;
+            meet();
+            for (int r = 0; r < rank; ++r) ties_before += *cluster.map_shared_rank(&sh.ties, r);
+        } else {
+            __syncthreads();  // wsum is written again below
+        }
     }
     auto kept_at = [&](int t, int& ties) {  // whole warp, consecutive groups in order
         const uint32_t k = t < w1 ? keys[t] : 0u;
@@ -174,14 +250,31 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
     }
     __syncthreads();
     {
-        const int h = wsum[lane], m = wsum2[lane];
-        holes = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < warp ? h : 0)));
-        movers = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < warp ? m : 0)));
-        const uint32_t total = __reduce_add_sync(FULL, static_cast<unsigned>(h));
-        if (tid == 0) list_base = total ? atomicAdd(p.count, total) : 0u;
+        int total, sum2;
+        over_warps(wsum, holes, sum);
+        over_warps(wsum2, movers, sum2);
+        total = sum;
+        if (cl > 1) {
+            if (tid == 0) {
+                sh.holes = sum;
+                sh.movers = sum2;
+            }
+            meet();
+            total = 0;
+            for (int r = 0; r < cl; ++r) {
+                const int h = *cluster.map_shared_rank(&sh.holes, r), m = *cluster.map_shared_rank(&sh.movers, r);
+                total += h;
+                if (r < rank) {
+                    holes += h;
+                    movers += m;
+                }
+            }
+        }
+        if (rank == 0 && tid == 0) sh.list_base = total ? atomicAdd(p.count, static_cast<uint32_t>(total)) : 0u;
+        meet();
     }
-    __syncthreads();
-    int2* list = p.moves + list_base;
+    int2* list = p.moves + (cl > 1 ? *cluster.map_shared_rank(&sh.list_base, 0) : sh.list_base);
+    if (cl > 1) cluster.barrier_arrive();  // (no block's shared memory is read past this point)
     ties = ties_before;
     for (int t0 = w0; t0 < w1; t0 += 32) {
         const int t = t0 + lane;
@@ -199,6 +292,7 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
             if (papart) p.positions_out[row] = p.positions[row];
         }
     }
+    if (cl > 1) cluster.barrier_wait();
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
@@ -206,41 +300,45 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31;
-    const long long W = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
-    const long long w = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
-    const long long M = __ldcg(p.count);
-    const int m0 = static_cast<int>(M * w / W), m1 = static_cast<int>(M * (w + 1) / W);
+    const int W = gridDim.x * (kMoveThreads / 32), w = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    const int M = static_cast<int>(__ldcg(p.count));
     // a row's K and V as 16-byte words, consecutive lanes along one row
-    const int words = p.row_bytes >> 4;             // a power of two
+    const int words = p.row_bytes >> 4;  // a power of two
     const int shift = 31 - __clz(2 * words);
-    const long long i1 = static_cast<long long>(m1) << shift;
-    for (long long i = (static_cast<long long>(m0) << shift) + lane; i < i1; i += 32 * U) {
-        uint4 x[U];
-        unsigned char* dst[U];
+    // chunks of neighbouring rows in turn, so that all warps work in the same part of the cache;
+    // a call with few moves deals out single rows
+    const int rows = M >= W * kMoveRows ? kMoveRows : 1;
+    for (long long m0 = static_cast<long long>(w) * rows; m0 < M; m0 += static_cast<long long>(W) * rows) {
+        const int n = static_cast<int>(min(static_cast<long long>(rows), M - m0));
+        const int2* list = p.moves + m0;
+        for (int i = lane; i < n << shift; i += 32 * U) {
+            uint4 x[U];
+            unsigned char* dst[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long j = i + 32 * u;
-            dst[u] = nullptr;
-            if (j < i1) {
-                const int2 mv = __ldcg(p.moves + (j >> shift));
-                const int c = static_cast<int>(j) & (2 * words - 1);
-                unsigned char* base = c < words ? p.k_cache : p.v_cache;
-                const int off = (c & (words - 1)) * 16;
-                x[u] = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<long long>(mv.x) * p.row_bytes + off));
-                dst[u] = base + static_cast<long long>(mv.y) * p.row_bytes + off;
+            for (int u = 0; u < U; ++u) {
+                const int j = i + 32 * u;
+                dst[u] = nullptr;
+                if (j < n << shift) {
+                    const int2 mv = __ldcg(list + (j >> shift));
+                    const int c = j & (2 * words - 1);
+                    unsigned char* base = c < words ? p.k_cache : p.v_cache;
+                    const int off = (c & (words - 1)) * 16;
+                    x[u] = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<long long>(mv.x) * p.row_bytes + off));
+                    dst[u] = base + static_cast<long long>(mv.y) * p.row_bytes + off;
+                }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
-    }
-    for (int m = m0 + lane; m < m1; m += 32) {
-        const int2 mv = __ldcg(p.moves + m);
-        p.acc_out[mv.y] = p.acc[mv.x];
-        p.positions_out[mv.y] = p.positions[mv.x];
-        if (p.k_scales) {
-            p.k_scales[mv.y] = p.k_scales[mv.x];
-            p.v_scales[mv.y] = p.v_scales[mv.x];
+            for (int u = 0; u < U; ++u)
+                if (dst[u]) __stcs(reinterpret_cast<uint4*>(dst[u]), x[u]);
+        }
+        if (lane < n) {
+            const int2 mv = __ldcg(list + lane);
+            p.acc_out[mv.y] = p.acc[mv.x];
+            p.positions_out[mv.y] = p.positions[mv.x];
+            if (p.k_scales) {
+                p.k_scales[mv.y] = p.k_scales[mv.x];
+                p.v_scales[mv.y] = p.v_scales[mv.x];
+            }
         }
     }
     // new lengths after every selection has read the old ones (new_lens may be seq_lens)
@@ -267,11 +365,16 @@ cudaError_t setup_evict() {
                                 kSmemKeys * 4);
 }
 
-cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream) {
-    void* args[] = {const_cast<EvictParams*>(&p)};
-    const int nk = p.Lmax < kSmemKeys ? p.Lmax : kSmemKeys;
-    const cudaError_t e = launch_pdl(reinterpret_cast<const void*>(&select_kernel),
-                                     dim3(static_cast<unsigned>(p.B) * p.Hkv), kThreadsE, nk * 4, args, stream);
+cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream) {
+    // Blocks per selection: more while the blocks stay within two per SM and each keeps 2048 rows.
+    const long long segs = static_cast<long long>(p.B) * p.Hkv;
+    int cl = 1;
+    while (cl < kMaxCluster && segs * cl * 2 <= 2LL * sms && p.Lmax / (cl * 2) >= 2048) cl *= 2;
+    const int per = (p.Lmax + cl - 1) / cl + 32 * kWarpsE;  // a block's rows, its warps' runs rounded up
+    p.smem_keys = per < kSmemKeys ? per : kSmemKeys;
+    void* args[] = {&p};
+    const cudaError_t e = launch_pdl(reinterpret_cast<const void*>(&select_kernel), dim3(static_cast<unsigned>(segs * cl)),
+                                     kThreadsE, p.smem_keys * 4, args, stream, cl);
     if (e != cudaSuccess) return e;
     return launch_pdl(reinterpret_cast<const void*>(&move_kernel), dim3(static_cast<unsigned>(sms) * 4), kMoveThreads, 0,
                       args, stream);

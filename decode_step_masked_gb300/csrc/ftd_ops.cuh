@@ -85,11 +85,10 @@ struct EvictParams {
     int B, Hkv, Lmax;
     int row_bytes;  // D elements
     int budget, recent, sinks;
+    int smem_keys;  // set by the launcher: keys of a block that its shared memory holds
     int pages_per_seq, page_shift, num_pages;
 };
-// Longest cache the selection counts in 16 bits per warp.
-constexpr int kMaxEvictLen = 1 << 20;
-cudaError_t launch_evict(const EvictParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream);
 // One-time set-up on the current device (shared-memory limits).
 cudaError_t setup_evict();
 
