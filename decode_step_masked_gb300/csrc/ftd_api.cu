@@ -380,6 +380,7 @@ struct ftd_ctx {
     float* scores = nullptr;
     float2* stats = nullptr;
     int2* moves = nullptr;
+    int2* local_moves = nullptr;
     uint32_t* evict_count = nullptr;
     // ftd_set_rope
     bool rope_set = false;
@@ -947,6 +948,7 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream) {
     };
     const size_t o_cnt = carve(2 * sizeof(uint32_t)), o_sc = carve(n_scores * sizeof(float));
     const size_t o_st = carve(segs * rows_q * sizeof(float2)), o_mv = carve(n_moves * sizeof(int2));
+    const size_t o_lm = carve(segs * ftd::kMaxLocalMoves * sizeof(int2));
     void* pool = nullptr;
     e = cudaMalloc(&pool, off);
     if (e != cudaSuccess) {
@@ -964,6 +966,7 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream) {
     ctx->scores = reinterpret_cast<float*>(base + o_sc);
     ctx->stats = reinterpret_cast<float2*>(base + o_st);
     ctx->moves = reinterpret_cast<int2*>(base + o_mv);
+    ctx->local_moves = reinterpret_cast<int2*>(base + o_lm);
     return FTD_OK;
 }
 
@@ -1067,6 +1070,7 @@ ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* sc
     p.positions_out = positions_out;
     p.keys = reinterpret_cast<uint32_t*>(ctx->scores);  // (at least one score row per kv head)
     p.moves = ctx->moves;
+    p.local_moves = ctx->local_moves;
     p.count = ctx->evict_count;
     p.err = ctx->err;
     p.B = c.max_batch;

@@ -1,5 +1,5 @@
 // ftd_evict.cu -- eviction from the cache by accumulated attention weight
-// (ftd_cache_evict): two kernels.
+// (ftd_cache_evict): a selection and a move kernel.
 //
 // Each (slot, kv head) keeps `budget` of its L rows, in the order of the key
 //   protected (position < sinks, or >= next_pos - recent)  >  weight  >  row index (lower first).
@@ -14,9 +14,13 @@
 // (histograms of the next byte among the keys that match so far, added up over the
 // cluster through distributed shared memory: sums, so any order of the atomics gives the
 // same result), in at most four rounds.  Then the moves are listed in row order
-// (ranks by ballots, warp and block prefixes).  The cluster reserves its part of the
-// call's one move list with an atomic add; the list's order varies, its moves are independent.
-// move_kernel deals the list out to all warps in chunks of rows and copies rows and planes.
+// (ranks by ballots, warp, block and cluster prefixes).  A cluster with few moves, as when
+// a cache is kept at its budget from step to step, makes them itself; else it appends them
+// to the call's list (one atomic add reserves its part; the list's order varies, its
+// moves are independent).
+// move_kernel deals the list out to all warps in chunks of 4 KB, so that ragged slots
+// do not leave SMs idle, and writes the new lengths, which may overwrite the old ones: every
+// cluster has read them by then.
 //
 // Bound: 8 bytes per position for the selection, then the moved rows, read and written.
 #include <cooperative_groups.h>
@@ -33,14 +37,16 @@ constexpr int kThreadsE = 512;
 constexpr int kWarpsE = kThreadsE / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSmemKeys = 48 * 1024;  // keys of a block that fit shared memory (192 KB)
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;  // rows a warp copies at a time
+constexpr int kLocalMoves = kMaxLocalMoves / kMaxCluster;  // moves per block that a cluster makes itself
+constexpr int kMoveThreads = 512;
+constexpr int kMoveU = 8;                 // 16-byte words a lane has in flight: 4 KB a warp
 
-__device__ __forceinline__ long long evict_row(const EvictParams& p, int b, int kvh, int t) {
-    if (!p.block_table) return (static_cast<long long>(b) * p.Hkv + kvh) * p.Lmax + t;
-    const int page = __ldcg(p.block_table + static_cast<size_t>(b) * p.pages_per_seq + (t >> p.page_shift));
+// Cache row of position index t, -1 behind a bad page (rows are below 2^31).
+__device__ __forceinline__ int evict_row(const EvictParams& p, int b, int kvh, int t) {
+    if (!p.block_table) return (b * p.Hkv + kvh) * p.Lmax + t;
+    const int page = p.block_table[static_cast<size_t>(b) * p.pages_per_seq + (t >> p.page_shift)];
     if (page < 0 || page >= p.num_pages) return -1;
-    return ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+    return ((page * p.Hkv + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
 }
 
 // Unsigned key in the order of the weights (NaN below every number), all below ~0u.
@@ -50,33 +56,81 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+// Copies n rows (n * the words of a row at most 32 * kMoveU) of K and V and their plane entries, by
+// one warp; lane m < n holds the m-th move.
+__device__ __forceinline__ void copy_rows(const EvictParams& p, int2 mv, int n, int lane) {
+    const int words = p.row_bytes >> 4;  // 16-byte words of a row, a power of two
+    const int shift = 31 - __clz(2 * words);
+    uint4 x[kMoveU];
+    float a = 0.f, ks = 0.f, vs = 0.f;
+    int ps = 0;
+    if (lane < n) {
+        a = p.acc[mv.x];
+        ps = p.positions[mv.x];
+        if (p.k_scales) {
+            ks = p.k_scales[mv.x];
+            vs = p.v_scales[mv.x];
+        }
+    }
+    // word j of the chunk: K then V of row j >> shift, consecutive lanes along one row
+    auto place = [&](int j, int row) {
+        const int c = j & (2 * words - 1);
+        return (c < words ? p.k_cache : p.v_cache) + static_cast<long long>(row) * p.row_bytes + (c & (words - 1)) * 16;
+    };
+#pragma unroll
+    for (int u = 0; u < kMoveU; ++u) {
+        const int j = lane + 32 * u;
+        const int src = __shfl_sync(0xffffffffu, mv.x, min(j >> shift, 31));
+        if (j >> shift < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(place(j, src)));
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveU; ++u) {
+        const int j = lane + 32 * u;
+        const int dst = __shfl_sync(0xffffffffu, mv.y, min(j >> shift, 31));
+        if (j >> shift < n) __stcs(reinterpret_cast<uint4*>(place(j, dst)), x[u]);
+    }
+    if (lane < n) {
+        p.acc_out[mv.y] = a;
+        p.positions_out[mv.y] = ps;
+        if (p.k_scales) {
+            p.k_scales[mv.y] = ks;
+            p.v_scales[mv.y] = vs;
+        }
+    }
+}
+
 // What the blocks of a cluster read of each other.
 struct alignas(16) Shared {
     uint32_t hist[2][256];
     int ties, holes, movers;  // of this block
-    uint32_t list_base;       // of the cluster (block 0's)
     int bad;
+    uint32_t list_base;       // of the cluster (block 0's)
 };
 
-__global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) {
-    extern __shared__ __align__(16) uint32_t skeys[];
+// MULTI: clusters of several blocks.
+template <bool MULTI>
+__device__ __forceinline__ void evict_segment(const EvictParams& p, uint32_t* skeys, int seg, int rank, int cl) {
     __shared__ Shared sh;
+    __shared__ __align__(16) uint32_t tot[256];
     __shared__ int wsum[kWarpsE], wsum2[kWarpsE];
     __shared__ int found[3];  // digit, rows needed of it, keys with it
     constexpr unsigned FULL = 0xffffffffu;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int cl = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seg = blockIdx.x / cl, b = seg / p.Hkv, kvh = seg - b * p.Hkv;
+    const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
     // every thread of the cluster (or, alone, of the block) has written what it shares
     auto meet = [&]() {
-        if (cl > 1) cluster.sync();
+        if constexpr (MULTI) cluster.sync();
         else __syncthreads();
     };
+    auto peer = [&](auto* x, int r) {
+        if constexpr (MULTI) return cluster.map_shared_rank(x, r);
+        return x;
+    };
+    // lane r < cl: block r's x (every lane loads at once; the others get 0)
+    auto of_peers = [&](int* x) { return lane < cl ? *peer(x, lane) : 0; };
     if (tid < 256) sh.hist[0][tid] = 0u;
     if (tid == 0) sh.bad = 0;
-    grid_dep_wait();
-    grid_dep_launch();
     const int L = __ldcg(p.seq_lens + b);
     if (L <= 0) return;
     if (L > p.Lmax) {
@@ -87,7 +141,7 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
     if (L <= p.budget) {  // everything stays
         if (apart || papart)
             for (int t = rank * kThreadsE + tid; t < L; t += cl * kThreadsE) {
-                const long long row = evict_row(p, b, kvh, t);
+                const int row = evict_row(p, b, kvh, t);
                 if (row < 0) {
                     atomicOr(p.err, kErrBadPage);
                     continue;
@@ -99,36 +153,35 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
     }
     // ---- keys; a warp owns a contiguous run of S rows, a block the runs of its warps ----
     const int S = ((L + cl * kWarpsE - 1) / (cl * kWarpsE) + 31) & ~31;
-    const int c0 = rank * kWarpsE * S;  // the block's first row (may lie past L)
+    const int c0 = min(L, rank * kWarpsE * S);  // the block's first row
     const int w0 = min(L, c0 + warp * S), w1 = min(L, w0 + S);
-    // keys[t] for row t of this block
-    uint32_t* keys = (S * kWarpsE <= p.smem_keys ? skeys : p.keys + static_cast<size_t>(seg) * p.Lmax + min(c0, L)) - min(c0, L);
+    // keys[t - c0] for row t
+    uint32_t* keys = S * kWarpsE <= p.smem_keys ? skeys : p.keys + static_cast<size_t>(seg) * p.Lmax + c0;
     const long long fresh = static_cast<long long>(__ldcg(p.next_pos + b)) - p.recent;
     bool bad = false;
     constexpr int U = 4;  // rows a lane has in flight
     for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
         float a[U];
-        int ps[U];
+        int ps[U], row[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) row[u] = t0 + 32 * u < w1 ? evict_row(p, b, kvh, t0 + 32 * u) : -2;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = t0 + 32 * u;
-            a[u] = 0.f;
-            ps[u] = 0;
-            if (t < w1) {
-                const long long row = evict_row(p, b, kvh, t);
-                if (row < 0) {
-                    bad = true;
-                } else {
-                    a[u] = p.acc[row];
-                    ps[u] = p.positions[row];
-                }
-            }
+            bad |= row[u] == -1;
+            a[u] = row[u] >= 0 ? p.acc[row[u]] : 0.f;
+            ps[u] = row[u] >= 0 ? p.positions[row[u]] : 0;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int t = t0 + 32 * u;
-            if (t < w1)
-                keys[t] = ((ps[u] >= 0 && ps[u] < p.sinks) || (p.recent > 0 && ps[u] >= fresh)) ? 0xffffffffu : weight_key(a[u]);
+            if (row[u] == -2) continue;
+            keys[t - c0] = ((ps[u] >= 0 && ps[u] < p.sinks) || (p.recent > 0 && ps[u] >= fresh)) ? 0xffffffffu : weight_key(a[u]);
+            // planes apart: entries below the budget go over as they are, and the moves then
+            // overwrite those of the rows that go
+            if (row[u] >= 0 && t < p.budget) {
+                if (apart) p.acc_out[row[u]] = a[u];
+                if (papart) p.positions_out[row[u]] = ps[u];
+            }
         }
     }
     if (bad) sh.bad = 1;
@@ -140,35 +193,34 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
     bool whole = false;    // every key with the prefix is kept
     for (int round = 0;; ++round) {
         uint32_t* hist = sh.hist[round & 1];
+#pragma unroll 4
         for (int t = w0 + lane; t < w1; t += 32) {
-            const uint32_t k = keys[t];
+            const uint32_t k = keys[t - c0];
             if (round == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
         }
         meet();
         if (round == 0) {
-            int any = 0;
-            for (int r = 0; r < cl; ++r) any |= cl > 1 ? *cluster.map_shared_rank(&sh.bad, r) : sh.bad;
-            if (any) {  // a page of this slot is bad: it is left as it is
+            if (__any_sync(FULL, of_peers(&sh.bad) != 0)) {  // a page of this slot is bad: its rows are left where they are
                 if (tid == 0 && rank == 0) atomicOr(p.err, kErrBadPage);
                 meet();  // no block leaves while another reads its flag
                 return;
             }
         }
-        if (tid < 256) sh.hist[(round + 1) & 1][tid] = 0u;  // (read last before this meeting)
+        if (tid < 256) {
+            sh.hist[(round + 1) & 1][tid] = 0u;  // (read last before this meeting)
+            if constexpr (MULTI) {
+                uint32_t n = 0u;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) n += r < cl ? *peer(hist + tid, r) : 0u;
+                tot[tid] = n;
+            }
+        }
+        if constexpr (MULTI) __syncthreads();
         if (warp == 0) {
             // lane owns bytes 8 lane .. 8 lane + 7; keys above them: those of the later lanes
-            uint32_t h[8] = {};
-            for (int r = 0; r < cl; ++r) {
-                const uint32_t* rh = cl > 1 ? cluster.map_shared_rank(hist, r) : hist;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(rh + 8 * lane + 4 * i);
-                    h[4 * i] += x.x;
-                    h[4 * i + 1] += x.y;
-                    h[4 * i + 2] += x.z;
-                    h[4 * i + 3] += x.w;
-                }
-            }
+            const uint4* ht = reinterpret_cast<const uint4*>((MULTI ? tot : hist) + 8 * lane);
+            const uint4 h0 = ht[0], h1 = ht[1];
+            const uint32_t h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
             int sum = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += static_cast<int>(h[i]);
@@ -200,7 +252,7 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
         shift -= 8;
     }
     const uint32_t lo = prefix << shift;  // the smallest key with the prefix
-    // exclusive prefix of v over the block's warps, and the block's sum (after a barrier)
+    // exclusive prefix of w over the block's warps, and the block's sum (after a barrier)
     auto over_warps = [&](const int* w, int& before, int& sum) {
         const int v = lane < kWarpsE ? w[lane] : 0;
         before = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < warp ? v : 0)));
@@ -212,21 +264,20 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
         int n = 0;
         for (int t0 = w0; t0 < w1; t0 += 32) {
             const int t = t0 + lane;
-            n += __popc(__ballot_sync(FULL, t < w1 && keys[t] == lo));
+            n += __popc(__ballot_sync(FULL, t < w1 && keys[t - c0] == lo));
         }
         if (lane == 0) wsum[warp] = n;
         __syncthreads();
         over_warps(wsum, ties_before, sum);
-        if (cl > 1) {
-            if (tid == 0) sh.ties = sum;
-            meet();
-            for (int r = 0; r < rank; ++r) ties_before += *cluster.map_shared_rank(&sh.ties, r);
-        } else {
-            __syncthreads();  // wsum is written again below
+        if (MULTI && tid == 0) sh.ties = sum;
+        meet();  // (and wsum may be written again)
+        if constexpr (MULTI) {
+            const int v = of_peers(&sh.ties);
+            ties_before += static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < rank ? v : 0)));
         }
     }
     auto kept_at = [&](int t, int& ties) {  // whole warp, consecutive groups in order
-        const uint32_t k = t < w1 ? keys[t] : 0u;
+        const uint32_t k = t < w1 ? keys[t - c0] : 0u;
         bool kept = t < w1 && (whole ? k >= lo : k > lo);
         if (!whole) {
             const bool tie = t < w1 && k == lo;
@@ -238,6 +289,7 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
     };
     // ---- holes below the budget and kept rows from it on: counted, then listed ----
     int holes = 0, movers = 0, ties = ties_before;
+#pragma unroll 2
     for (int t0 = w0; t0 < w1; t0 += 32) {
         const int t = t0 + lane;
         const bool kept = kept_at(t, ties);
@@ -249,120 +301,105 @@ __global__ void __launch_bounds__(kThreadsE) select_kernel(const EvictParams p) 
         wsum2[warp] = movers;
     }
     __syncthreads();
-    {
-        int total, sum2;
-        over_warps(wsum, holes, sum);
-        over_warps(wsum2, movers, sum2);
-        total = sum;
-        if (cl > 1) {
-            if (tid == 0) {
-                sh.holes = sum;
-                sh.movers = sum2;
-            }
-            meet();
-            total = 0;
-            for (int r = 0; r < cl; ++r) {
-                const int h = *cluster.map_shared_rank(&sh.holes, r), m = *cluster.map_shared_rank(&sh.movers, r);
-                total += h;
-                if (r < rank) {
-                    holes += h;
-                    movers += m;
-                }
-            }
+    int total, sum2;
+    over_warps(wsum, holes, total);
+    over_warps(wsum2, movers, sum2);
+    if constexpr (MULTI) {
+        if (tid == 0) {
+            sh.holes = total;
+            sh.movers = sum2;
         }
-        if (rank == 0 && tid == 0) sh.list_base = total ? atomicAdd(p.count, static_cast<uint32_t>(total)) : 0u;
-        meet();
+        cluster.sync();
+        const int h = of_peers(&sh.holes), m = of_peers(&sh.movers);
+        total = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(h)));
+        holes += static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < rank ? h : 0)));
+        movers += static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < rank ? m : 0)));
     }
-    int2* list = p.moves + (cl > 1 ? *cluster.map_shared_rank(&sh.list_base, 0) : sh.list_base);
-    if (cl > 1) cluster.barrier_arrive();  // (no block's shared memory is read past this point)
+    // the moves' place: shared by the whole call, or, for few, this cluster's own
+    const bool local = total <= kLocalMoves * cl;
+    int2* list = p.local_moves + static_cast<size_t>(seg) * kMaxLocalMoves;
+    if (!local) {
+        if (rank == 0 && tid == 0) sh.list_base = atomicAdd(p.count, static_cast<uint32_t>(total));
+        meet();
+        list = p.moves + *peer(&sh.list_base, 0);
+    }
     ties = ties_before;
+#pragma unroll 2
     for (int t0 = w0; t0 < w1; t0 += 32) {
         const int t = t0 + lane;
         const bool kept = kept_at(t, ties);
         const bool hole = t < w1 && t < p.budget && !kept, mover = t >= p.budget && kept;
         const unsigned hm = __ballot_sync(FULL, hole), mm = __ballot_sync(FULL, mover);
         const unsigned below = (1u << lane) - 1u;
-        if (hole) list[holes + __popc(hm & below)].y = static_cast<int>(evict_row(p, b, kvh, t));
-        if (mover) list[movers + __popc(mm & below)].x = static_cast<int>(evict_row(p, b, kvh, t));
+        if (hole || mover) {
+            const int row = evict_row(p, b, kvh, t);
+            if (hole) list[holes + __popc(hm & below)].y = row;
+            else list[movers + __popc(mm & below)].x = row;
+        }
         holes += __popc(hm);
         movers += __popc(mm);
-        if ((apart || papart) && kept && t < p.budget) {
-            const long long row = evict_row(p, b, kvh, t);
-            if (apart) p.acc_out[row] = p.acc[row];
-            if (papart) p.positions_out[row] = p.positions[row];
-        }
     }
-    if (cl > 1) cluster.barrier_wait();
+    meet();  // the list is complete (and no block's shared memory is read past this point)
+    if (local)
+        for (int m = rank * kWarpsE + warp; m < total; m += cl * kWarpsE) copy_rows(p, __ldcg(list + m), 1, lane);
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
-    constexpr int U = 4;
+template <bool MULTI>
+__global__ void __launch_bounds__(kThreadsE, 2) select_kernel(const EvictParams p) {
+    extern __shared__ __align__(16) uint32_t skeys[];
+    int cl = 1, rank = 0;
+    if constexpr (MULTI) {
+        const cg::cluster_group cluster = cg::this_cluster();
+        cl = static_cast<int>(cluster.num_blocks());
+        rank = static_cast<int>(cluster.block_rank());
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    evict_segment<MULTI>(p, skeys, static_cast<int>(blockIdx.x) / cl, rank, cl);
+}
+
+__global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const EvictParams p) {
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31;
     const int W = gridDim.x * (kMoveThreads / 32), w = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
     const int M = static_cast<int>(__ldcg(p.count));
-    // a row's K and V as 16-byte words, consecutive lanes along one row
-    const int words = p.row_bytes >> 4;  // a power of two
-    const int shift = 31 - __clz(2 * words);
-    // chunks of neighbouring rows in turn, so that all warps work in the same part of the cache;
-    // a call with few moves deals out single rows
-    const int rows = M >= W * kMoveRows ? kMoveRows : 1;
-    for (long long m0 = static_cast<long long>(w) * rows; m0 < M; m0 += static_cast<long long>(W) * rows) {
-        const int n = static_cast<int>(min(static_cast<long long>(rows), M - m0));
-        const int2* list = p.moves + m0;
-        for (int i = lane; i < n << shift; i += 32 * U) {
-            uint4 x[U];
-            unsigned char* dst[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = i + 32 * u;
-                dst[u] = nullptr;
-                if (j < n << shift) {
-                    const int2 mv = __ldcg(list + (j >> shift));
-                    const int c = j & (2 * words - 1);
-                    unsigned char* base = c < words ? p.k_cache : p.v_cache;
-                    const int off = (c & (words - 1)) * 16;
-                    x[u] = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<long long>(mv.x) * p.row_bytes + off));
-                    dst[u] = base + static_cast<long long>(mv.y) * p.row_bytes + off;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (dst[u]) __stcs(reinterpret_cast<uint4*>(dst[u]), x[u]);
-        }
-        if (lane < n) {
-            const int2 mv = __ldcg(list + lane);
-            p.acc_out[mv.y] = p.acc[mv.x];
-            p.positions_out[mv.y] = p.positions[mv.x];
-            if (p.k_scales) {
-                p.k_scales[mv.y] = p.k_scales[mv.x];
-                p.v_scales[mv.y] = p.v_scales[mv.x];
-            }
-        }
-    }
-    // new lengths after every selection has read the old ones (new_lens may be seq_lens)
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < p.B; b += kMoveThreads) {
-            const int L = p.seq_lens[b];
+            const int L = __ldcg(p.seq_lens + b);
             p.new_lens[b] = (L > p.budget && L <= p.Lmax) ? p.budget : L;
         }
+    if (M == 0) return;
+    // Chunks of neighbouring rows in turn, so that all warps work in the same part of the cache; the
+    // next chunk's moves are loaded while this one's rows are copied.
+    const int rows = 32 * kMoveU * 8 / p.row_bytes;  // 4 KB of K and V (4 to 32 rows)
+    const long long step = static_cast<long long>(W) * rows;
+    long long m0 = static_cast<long long>(w) * rows;
+    int2 mv = make_int2(0, 0);
+    if (m0 + lane < M && lane < rows) mv = __ldcg(p.moves + m0 + lane);
+    for (; m0 < M; m0 += step) {
+        int2 next = make_int2(0, 0);
+        if (m0 + step + lane < M && lane < rows) next = __ldcg(p.moves + m0 + step + lane);
+        copy_rows(p, mv, static_cast<int>(min(static_cast<long long>(rows), M - m0)), lane);
+        mv = next;
+    }
     // the last block to finish leaves the counters at zero for the next call
     __syncthreads();
-    if (threadIdx.x == 0) {
-        const uint32_t done = arrive_acq_rel(p.count + 1, 1u);
-        if (done == gridDim.x - 1) {
-            p.count[0] = 0u;
-            p.count[1] = 0u;
-        }
+    if (threadIdx.x == 0 && arrive_acq_rel(p.count + 1, 1u) == gridDim.x - 1) {
+        p.count[0] = 0u;
+        p.count[1] = 0u;
     }
 }
 
 }  // namespace
 
 cudaError_t setup_evict() {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmemKeys * 4);
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<false>),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<true>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
+    return e;
 }
 
 cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream) {
@@ -372,11 +409,12 @@ cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream) {
     while (cl < kMaxCluster && segs * cl * 2 <= 2LL * sms && p.Lmax / (cl * 2) >= 2048) cl *= 2;
     const int per = (p.Lmax + cl - 1) / cl + 32 * kWarpsE;  // a block's rows, its warps' runs rounded up
     p.smem_keys = per < kSmemKeys ? per : kSmemKeys;
+    const void* fn = cl > 1 ? reinterpret_cast<const void*>(&select_kernel<true>)
+                            : reinterpret_cast<const void*>(&select_kernel<false>);
     void* args[] = {&p};
-    const cudaError_t e = launch_pdl(reinterpret_cast<const void*>(&select_kernel), dim3(static_cast<unsigned>(segs * cl)),
-                                     kThreadsE, p.smem_keys * 4, args, stream, cl);
+    const cudaError_t e = launch_pdl(fn, dim3(static_cast<unsigned>(segs * cl)), kThreadsE, p.smem_keys * 4, args, stream, cl);
     if (e != cudaSuccess) return e;
-    return launch_pdl(reinterpret_cast<const void*>(&move_kernel), dim3(static_cast<unsigned>(sms) * 4), kMoveThreads, 0,
+    return launch_pdl(reinterpret_cast<const void*>(&move_kernel), dim3(static_cast<unsigned>(sms) * 2), kMoveThreads, 0,
                       args, stream);
 }
 

@@ -79,8 +79,9 @@ struct EvictParams {
     const int32_t* positions;
     int32_t* positions_out;
     uint32_t* keys;   // workspace [B * Hkv][Lmax], for segments whose keys do not fit shared memory
-    int2* moves;      // workspace [B * Hkv * (Lmax / 2)]: source and destination cache rows
-    uint32_t* count;  // [2]: moves listed, blocks done; zero between calls
+    int2* moves;        // workspace [B * Hkv * (Lmax / 2)]: source and destination cache rows
+    int2* local_moves;  // workspace [B * Hkv][kMaxLocalMoves]
+    uint32_t* count;    // [2]: moves listed, blocks done; zero between calls
     uint32_t* err;
     int B, Hkv, Lmax;
     int row_bytes;  // D elements
@@ -88,6 +89,8 @@ struct EvictParams {
     int smem_keys;  // set by the launcher: keys of a block that its shared memory holds
     int pages_per_seq, page_shift, num_pages;
 };
+// Most moves of one kv head that its selection makes itself, in place of the move kernel.
+constexpr int kMaxLocalMoves = 256;
 cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream);
 // One-time set-up on the current device (shared-memory limits).
 cudaError_t setup_evict();
