@@ -136,14 +136,32 @@ namespace ftd {
 // cfg.kernel == FTD_KERNEL_CUDA_CORE selects the CUDA-core kernel instead.
 // Internal to the library (hidden), shared by ftd_init and the no-allocation
 // entry point; tki.fn is null when the CUDA-core kernel runs.
+// Smallest blocks of query rows for which the scored step and cross attention take the tensor cores.
+constexpr int kMinTcBlock = 3, kMinTcBlockI8 = 4;
 __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, int mode) {
     TcChoice r{};
     r.nhb = 1;
     r.qblk = 8;
     const int rows_q = (c.q_len > 1 ? c.q_len : 1) * (c.n_q_heads / c.n_kv_heads);
     const bool forced = c.kernel == FTD_KERNEL_CUDA_CORE;
-    const bool want_tc = (c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16) && c.head_dim == 128 &&
-                         rows_q % 4 == 0 && !forced;
+    const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
+    if (mode != kStep && c.head_dim == 128 && !forced && encode_tiled() && (half || c.cache_dtype == FTD_I8) &&
+        !(half && rows_q % 32 == 0)) {
+        // The scored step and cross attention: blocks of any size up to 16 rows (INT8: 8), the
+        // columns past them zero; the largest block that divides the rows, the CUDA cores when
+        // that is too small to pay for the tensor cores.
+        int blk = half ? 16 : 8;
+        while (rows_q % blk) --blk;
+        if (blk < (half ? kMinTcBlock : kMinTcBlockI8)) return r;
+        const bool bf = c.cache_dtype == FTD_BF16, mt = c.q_len > 1;
+        const int Gt = blk > 8 ? 16 : 8;
+        r.qblk = blk;
+        r.nhb = rows_q / blk;
+        r.tki = mode == kScored ? (half ? select_tc_scored(bf, Gt, mt) : select_tc_i8_scored(mt))
+                                : (half ? select_tc_cross(bf, Gt, mt) : select_tc_i8_cross(mt));
+        return r;
+    }
+    const bool want_tc = half && c.head_dim == 128 && rows_q % 4 == 0 && !forced;
     const bool want_tc_i8 = c.cache_dtype == FTD_I8 && c.head_dim == 128 && rows_q % 8 == 0 && !forced;
     if ((want_tc || want_tc_i8) && encode_tiled()) {
         if (want_tc && rows_q % 32 == 0) {
@@ -156,10 +174,7 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
         } else {
             const int Gt = (rows_q % 16 == 0 && !want_tc_i8) ? 16 : 8;
             r.qblk = rows_q % 8 == 0 ? Gt : 4;
-            const bool bf = c.cache_dtype == FTD_BF16, mt = c.q_len > 1;
-            if (mode == kScored) r.tki = want_tc_i8 ? select_tc_i8_scored(mt) : select_tc_scored(bf, Gt, mt);
-            else if (mode == kCross) r.tki = want_tc_i8 ? select_tc_i8_cross(mt) : select_tc_cross(bf, Gt, mt);
-            else r.tki = want_tc_i8 ? select_tc_i8(mt) : select_tc(bf, Gt, mt);
+            r.tki = want_tc_i8 ? select_tc_i8(c.q_len > 1) : select_tc(c.cache_dtype == FTD_BF16, Gt, c.q_len > 1);
         }
         r.nhb = rows_q / r.qblk;
     }
@@ -373,7 +388,7 @@ struct ftd_ctx {
     struct ModeKernel {
         bool ready = false;
         ftd::KernelInfo ki{};
-        ftd::TcKernelInfo tki{};
+        ftd::TcChoice tcc{};
     } mode[3];
     // ftd_enable_scores: workspace of ftd_decode_mha_scored and ftd_cache_evict
     void* sc_pool = nullptr;
@@ -445,9 +460,17 @@ ftd_status ftd_init(const ftd_config* cfg, void* stream, ftd_ctx** out) {
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (tensor-core kernel)");
     }
     const bool use_tc = tki.fn != nullptr;
-    const size_t n_seg = use_tc ? B * Hkv * tc_nhb : B * Hkv * nhb;
+    size_t n_seg = use_tc ? B * Hkv * tc_nhb : B * Hkv * nhb;
     const size_t n_slots = n_seg + static_cast<size_t>(grid) * (use_tc ? 1 : ki.warps);
-    const size_t ws_bytes = n_slots * (use_tc ? tki.slot_floats : ki.slot_floats) * sizeof(float);
+    size_t ws_bytes = n_slots * (use_tc ? tki.slot_floats : ki.slot_floats) * sizeof(float);
+    // the scored step and cross attention cut query rows into blocks of their own (alike for both);
+    // where they run on the CUDA cores so does the step, with the same blocks
+    const ftd::TcChoice tcm = ftd::choose_tc(c, ftd::kCross);
+    if (tcm.tki.fn) {
+        const size_t segs = B * Hkv * tcm.nhb, bytes = (segs + grid) * tcm.tki.slot_floats * sizeof(float);
+        if (segs > n_seg) n_seg = segs;
+        if (bytes > ws_bytes) ws_bytes = bytes;
+    }
     const int qeb = elem_bytes(c.qkv_dtype);
 
     ftd_ctx* ctx = new (std::nothrow) ftd_ctx();
@@ -630,11 +653,12 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     p.proj_lo = proj ? ctx->proj_lo : nullptr;
     p.proj_dt = c.qkv_dtype == FTD_BF16 ? ftd::kBF16 : ftd::kF16;
     ftd::KernelInfo ki = ctx->ki;
-    ftd::TcKernelInfo tki = ctx->tki;
+    ftd::TcChoice tcc{ctx->tki, ctx->tc_nhb, ctx->tc_qblk};
     if (mode != ftd::kStep) {
         ki = ctx->mode[mode].ki;
-        tki = ctx->mode[mode].tki;
+        tcc = ctx->mode[mode].tcc;
     }
+    const ftd::TcKernelInfo& tki = tcc.tki;
     if (mode == ftd::kScored) {
         p.scores = ctx->scores;
         p.stats = ctx->stats;
@@ -648,7 +672,7 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     }
 
     cudaError_t e;
-    if (ctx->use_tc) {
+    if (tki.fn) {
         const size_t rows = ctx->rows;
         if (ctx->tm_k_base != k_cache) {
             if (!encode_cache_map(&ctx->tmk, k_cache, c.cache_dtype, rows))
@@ -660,8 +684,8 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
                 return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for v_cache");
             ctx->tm_v_base = v_cache;
         }
-        p.nhb = ctx->tc_nhb;
-        p.qblk = ctx->tc_qblk;
+        p.nhb = tcc.nhb;
+        p.qblk = tcc.qblk;
         void* args[] = {&ctx->tmk, &ctx->tmv, &p};
         e = launch_overlapped(tki.fn, ctx->grid, tki.threads, tki.smem, args, stream);
     } else {
@@ -884,16 +908,16 @@ struct DeviceScope {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The kernels of `mode` for the context's configuration, with their shared-memory limits raised
-// (the same tiles, blocks and partial slots as the step's, so its workspace serves them too).
+// (ftd_init sized the workspace for them).
 ftd_status ready_mode(ftd_ctx* ctx, int mode) {
     ftd_ctx::ModeKernel& m = ctx->mode[mode];
     if (m.ready) return FTD_OK;
     const ftd_config& c = ctx->cfg;
     m.ki = ftd::choose_cc(c.cache_dtype, c.head_dim, ctx->G, mode);
+    m.tcc = ftd::choose_tc(c, mode);
     cudaError_t e = cudaSuccess;
-    if (ctx->use_tc) {
-        m.tki = ftd::choose_tc(c, mode).tki;
-        e = cudaFuncSetAttribute(m.tki.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, m.tki.smem);
+    if (m.tcc.tki.fn) {
+        e = cudaFuncSetAttribute(m.tcc.tki.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, m.tcc.tki.smem);
     } else {
         e = cudaFuncSetAttribute(m.ki.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, m.ki.smem);
     }
@@ -937,8 +961,8 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream) {
     const size_t segs = static_cast<size_t>(c.max_batch) * c.n_kv_heads;
     const size_t rows_q = static_cast<size_t>(ctx->nq) * (c.n_q_heads / c.n_kv_heads);
     const size_t n_scores = segs * rows_q * c.max_len, n_moves = segs * (c.max_len / 2);
-    // The weights kernel's grid: one block per 512 positions of a kv head.
-    if (segs * ((c.max_len + 511) / 512) >= (static_cast<size_t>(1) << 31))
+    // The weights kernels' grids: at most one block per 128 positions of a kv head.
+    if (segs * ((c.max_len + 127) / 128) >= (static_cast<size_t>(1) << 31))
         return fail(FTD_ERR_UNSUPPORTED, "ftd_enable_scores: cache too large for the weights kernel's grid");
     size_t off = 0;
     auto carve = [&](size_t bytes) {

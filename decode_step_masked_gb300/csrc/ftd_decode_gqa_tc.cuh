@@ -60,6 +60,9 @@ constexpr int softmax_groups(int G) { return G >= 16 ? 4 : (G >= 8 ? 2 : 1); }
 
 // Weight of a segment boundary in the static split (in 128-row tiles; see WeightedSplit).
 constexpr int kAlpha = 1;
+// Of the scored step and of cross attention: ragged memories of four beams (B16 H32 D128, 33 to
+// 2047 rows) took 93 / 70 / 60 / 57 / 60 us at 1 / 2 / 3 / 4 / 6, a 70B-shaped memory 85 at each.
+constexpr int kModeAlpha = 4;
 
 // Margin (log2 units) by which a score may pass a column's running reference
 // before the softmax moves the reference: weights then stay below 2^8, well
@@ -104,6 +107,7 @@ struct Layout {
     // P, Ls and, where shared memory has room, the weighted prefix VP (else the split is unweighted)
     static constexpr bool HAVE_VP = OFF_PREFIX + round_up((3 * kMaxBatch + 2) * 4, 128) + 1024 <= 232448;
     static constexpr int ALPHA = HAVE_VP ? kAlpha : 0;
+    static constexpr int MODE_PREFIX = 232448 - 1024 - OFF_PREFIX;  // bytes left for the prefixes of the other modes
     static constexpr int PREFIX_BYTES = ((HAVE_VP ? 3 : 2) * kMaxBatch + 2) * 4;
     static constexpr int SMEM = OFF_PREFIX + round_up(PREFIX_BYTES, 128) + 1024;  // + alignment slack
     // S (2 x N columns) and O (2 x N); INT8 adds the score MMAs' K operand, widened from
@@ -362,11 +366,14 @@ __device__ __forceinline__ int seg_ordinal(int B, int spp, int b, int s, int h) 
 // h V1 + VP[b] + s (nt + ALPHA) + i, V1 = VP[B] the weighted length of a pass, and
 // worker w takes the tiles whose position lies in [ceil(w V / W), ceil((w+1) V / W)),
 // V = np V1.
+// ALPHA < 0: the weight is the member alpha.
 template <int ALPHA>
 struct PassSplit {
     const int* P;
     const int* VP;
-    int B, spp, np, W;
+    int B, spp, np, W, alpha;
+
+    __device__ int boundary() const { return ALPHA >= 0 ? ALPHA : alpha; }
 
     __device__ long long V() const { return static_cast<long long>(np) * VP[B]; }
 
@@ -387,14 +394,14 @@ struct PassSplit {
         if (VP[lo + 1] <= v1) return h * P[B] + P[lo + 1];
         const int nt = (P[lo + 1] - P[lo]) / spp;
         const long long o = v1 - VP[lo];
-        const long long sg = o / (nt + ALPHA);
-        const long long r = o - sg * (nt + ALPHA);
+        const long long sg = o / (nt + boundary());
+        const long long r = o - sg * (nt + boundary());
         return h * P[B] + P[lo] + static_cast<int>(sg * nt + (r < nt ? r : nt));
     }
 
     // worker holding tile i of segment s of slot b in pass h (nt tiles)
     __device__ int worker_at(int b, int s, int h, int nt, int i) const {
-        const long long v = static_cast<long long>(h) * VP[B] + VP[b] + static_cast<long long>(s) * (nt + ALPHA) + i;
+        const long long v = static_cast<long long>(h) * VP[B] + VP[b] + static_cast<long long>(s) * (nt + boundary()) + i;
         const long long vv = V();
         if (vv * W < (1ll << 32))  // the product fits 32 bits: a cheaper division
             return static_cast<int>(static_cast<uint32_t>(v * W) / static_cast<uint32_t>(vv));
@@ -466,8 +473,15 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     int* bcast = reinterpret_cast<int*>(smem + LY::OFF_MISC + kNumBars * 8 + 8);
     int* rv = reinterpret_cast<int*>(smem + LY::OFF_MISC + kNumBars * 8 + 12);  // re-planning meeting counter
     int* P = reinterpret_cast<int*>(smem + LY::OFF_PREFIX);
-    int* Ls = P + (kMaxBatch + 1);
-    int* VP = LY::HAVE_VP ? Ls + kMaxBatch : P;
+    // kScored, kCross: the three arrays as large as the batch, so that the weighted prefix fits
+    // beside 16-row blocks too (up to 788 slots; beyond, the split is unweighted there)
+    const int cap = MODE == kStep ? kMaxBatch : p.B;
+    const bool have_vp = MODE == kStep ? LY::HAVE_VP : (3 * cap + 2) * 4 <= LY::MODE_PREFIX;
+    int* Ls = P + (cap + 1);
+    int* VP = have_vp ? Ls + cap : P;
+    // weight of a segment boundary: fixed for the step, else by whether the prefix fits
+    constexpr int ALPHA = MODE == kStep ? LY::ALPHA : -1;
+    const int alpha = MODE == kStep ? LY::ALPHA : (have_vp ? tc::kModeAlpha : 0);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
@@ -491,7 +505,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     const int np = kPasses ? p.nhb : 1;
     const int spp = kPasses ? p.Hkv : p.Hkv * p.nhb;
     bool ovf = false;
-    if (warp == 0) ovf = build_prefix<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, lane);
+    if (warp == 0) ovf = build_prefix<MODE>(p, TM, spp, alpha, P, VP, Ls, lane);
     fence_mbar_init();
     tc::tc_fence_before();
     __syncthreads();
@@ -504,9 +518,15 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     // variant measured faster without it, back to back and after a GEMM).  After
     // the wait the lengths are checked again (lengths_changed).  Reads of the
     // caches and writes of shared outputs come after the wait.
-    const long long W = gridDim.x;
     const int wid = blockIdx.x;
-    const PassSplit<LY::ALPHA> split{P, VP, p.B, spp, np, static_cast<int>(W)};
+    PassSplit<ALPHA> split{P, VP, p.B, spp, np, static_cast<int>(gridDim.x), alpha};
+    // kScored, kCross: a short tile space is cut into fewer pieces (see the CUDA-core kernel); a
+    // piece costs the merge about a quarter of a tile's time
+    auto limit_workers = [&]() {
+        if constexpr (MODE != kStep)
+            split.W = limited_workers(np * VP[p.B], p.B * spp * np, 4.f, static_cast<int>(gridDim.x));
+    };
+    limit_workers();
     int t_begin = split.begin(wid);
     int n_my = split.begin(wid + 1) - t_begin;
     if (!I8 && n_my > 0 && tid == 0 && !p.block_table) {
@@ -530,9 +550,10 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
         // rebuilds the split from the lengths now visible, they meet again.  If the
         // warps disagree (the lengths changed while the step ran) the meeting gives up:
         // the warp then skips its role, and the others' bounded waits run out.
-        const int r = replan<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, rv);
+        const int r = replan<MODE>(p, TM, spp, alpha, P, VP, Ls, rv);
         const bool ok = r >= 0;
         ovf = r > 0;
+        if (ok) limit_workers();
         t_begin = split.begin(wid);
         n_my = ok ? split.begin(wid + 1) - t_begin : 0;
         if (!ok) *abort_flag = 1;
@@ -1011,8 +1032,6 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 float sc[GH];
                 float vf[GH];  // INT8: the row's V scale, folded into the weight (0 for rows not seen)
                 bool need = false;  // a visible score above the column's reference by more than the margin
-                float* srow = nullptr;  // kScored: this thread's place in its first column's scores
-                if constexpr (MODE == kScored) srow = p.scores + score_row(p, cu.b, kvh, hb * QB + c0) * p.Lmax + t0 + r;
                 float ksr = 1.f, vsr = 1.f;
                 if constexpr (I8) {
                     ksr = scl[(k & 3) * 2 * TM + r];
@@ -1020,12 +1039,9 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 }
 #pragma unroll
                 for (int jj = 0; jj < GH; ++jj) {
-                    const bool valid = MQ ? (r >= lo0 + tk[jj] && r < hi0 + tk[jj]) : valid0;
+                    const bool valid = MQ && MODE != kCross ? (r >= lo0 + tk[jj] && r < hi0 + tk[jj]) : valid0;
                     sc[jj] = valid ? (I8 ? (sh[jj] + sl_[jj]) * ksr : sh[jj] + sl_[jj]) : -INFINITY;
-                    if constexpr (MODE == kScored) {
-                        sc[jj] *= p.sscale;  // (-inf stays -inf: the scale is positive)
-                        if (valid && c0 + jj < QB) srow[static_cast<size_t>(jj) * p.Lmax] = sc[jj];
-                    }
+                    if constexpr (MODE == kScored) sc[jj] *= p.sscale;  // (-inf stays -inf: the scale is positive)
                     vf[jj] = valid ? vsr : 0.f;
                     need |= sc[jj] > m[jj] + tc::kRescaleLog2;  // always when m = -inf and the score is visible
                 }
@@ -1073,7 +1089,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         const float tmax = fmaxf(fmaxf(red_max[j], red_max[G + j]), fmaxf(red_max[2 * G + j], red_max[3 * G + j]));
                         const float mnew = fmaxf(m[jj], tmax);
                         float pj;
-                        if constexpr (MQ) {
+                        if constexpr (MQ && MODE != kCross) {
                             const float mref = mnew == -INFINITY ? 0.f : mnew;
                             alpha[jj] = exp2f(m[jj] - mref);
                             pj = exp2f(sc[jj] - mref);
@@ -1090,6 +1106,16 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     tc::named_bar_sync(1, SMX);
                 }
                 if (leader) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(kBarPFull + (k & 1))) : "memory");
+                if constexpr (MODE == kScored) {
+                    // the scores, once the weights are on their way to the MMAs (stored before, they
+                    // lengthened the chain of a tile by half: 990 against 660 cycles)
+                    float* srow = p.scores + score_row(p, cu.b, kvh, hb * QB + c0) * p.Lmax + t0 + r;
+#pragma unroll
+                    for (int jj = 0; jj < GH; ++jj) {
+                        const bool valid = MQ ? (r >= lo0 + tk[jj] && r < hi0 + tk[jj]) : valid0;
+                        if (valid && c0 + jj < QB) srow[static_cast<size_t>(jj) * p.Lmax] = sc[jj];
+                    }
+                }
                 if (stage_next) {
                     store_q();
                     q_staged = true;
@@ -1161,7 +1187,41 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                 Ls_[jj] = 0.f;
                                 Ac[jj] = 0.f;
                             }
-                            for (int w = wf; w <= wl; ++w) {
+                            int w0 = wf;
+                            if constexpr (MODE != kStep) {
+                                // four pieces' loads in flight (every worker from wf to wl holds one)
+                                for (; w0 + 3 <= wl; w0 += 4) {
+                                    float mw[4][GH], lw[4][GH], ow[4][GH];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float* sl = p.ws + static_cast<size_t>(segg + w0 + i) * LY::SLOT;
+#pragma unroll
+                                        for (int jj = 0; jj < GH; ++jj) {
+                                            mw[i][jj] = __ldcg(sl + c0 + jj);
+                                            lw[i][jj] = __ldcg(sl + G + c0 + jj);
+                                            ow[i][jj] = __ldcg(sl + LY::OOFF + (c0 + jj) * D + r);
+                                        }
+                                    }
+#pragma unroll
+                                    for (int jj = 0; jj < GH; ++jj) {
+                                        float mn = Mx[jj];
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) mn = fmaxf(mn, mw[i][jj]);
+                                        const float mref = mn == -INFINITY ? 0.f : mn;
+                                        const float a = exp2f(Mx[jj] - mref);
+                                        Ls_[jj] *= a;
+                                        Ac[jj] *= a;
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const float f = exp2f(mw[i][jj] - mref);
+                                            Ls_[jj] += lw[i][jj] * f;
+                                            Ac[jj] += ow[i][jj] * f;
+                                        }
+                                        Mx[jj] = mn;
+                                    }
+                                }
+                            }
+                            for (int w = w0; w <= wl; ++w) {
                                 if (!split.has_piece(w, wf, wl)) continue;
                                 const float* sl = p.ws + static_cast<size_t>(segg + w) * LY::SLOT;
                                 float mw[GH], lw[GH], ow[GH];
@@ -1232,7 +1292,8 @@ struct TcKernelInfo {
 template <typename CT, int G, bool MQ, int MODE = kStep>
 TcKernelInfo tc_kernel_info() {
     using LY = tc::Layout<G, std::is_same_v<CT, int8_t>>;
-    return TcKernelInfo{reinterpret_cast<const void*>(&decode_gqa_tc_kernel<CT, G, MQ, MODE>), LY::SMEM, LY::SLOT, G,
+    return TcKernelInfo{reinterpret_cast<const void*>(&decode_gqa_tc_kernel<CT, G, MQ, MODE>),
+                        MODE == kStep ? LY::SMEM : 232448, LY::SLOT, G,
                         tc::threads_for(G, std::is_same_v<CT, int8_t>)};
 }
 

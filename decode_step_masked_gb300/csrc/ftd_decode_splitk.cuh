@@ -395,6 +395,14 @@ struct WeightedSplit {
     }
 };
 
+// Workers for a tile space of weighted length V over segs segments (some may be empty), at most
+// Wmax: each gets at least sqrt(V / segs / cost) tiles.  Never more workers than tiles, so
+// every worker between a segment's first and last holds a piece of it.
+__device__ __forceinline__ int limited_workers(int V, int segs, float cost, int Wmax) {
+    const int m = static_cast<int>(sqrtf(static_cast<float>(V) / (cost * static_cast<float>(segs))) + 0.5f);
+    return max(1, min(Wmax, V / max(1, m)));
+}
+
 // ================================================================ kernel
 template <typename CT, int D, int G, int MODE = kStep>
 __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk_kernel(const DecodeParams p) {
@@ -438,9 +446,22 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     fence_mbar_init();
     __syncthreads();
 
-    const long long W = static_cast<long long>(gridDim.x) * TL::WARPS;
-    const int wid = blockIdx.x * TL::WARPS + warp;
-    const WeightedSplit<TL::ALPHA> split{P, VP, p.B, segs, static_cast<int>(W)};
+    const int Wmax = static_cast<int>(gridDim.x) * TL::WARPS;
+    int wid = blockIdx.x * TL::WARPS + warp;
+    WeightedSplit<TL::ALPHA> split{P, VP, p.B, segs, Wmax};
+    // kScored and kCross: a short tile space is not cut as fine as it goes, since every piece
+    // more costs its segment's merge a partial.  A worker's time grows with its tiles m, the
+    // merge's with the segment's pieces n / m, so m goes with sqrt(n); measured best (cross attention, one
+    // slot): m = 3 for n = 47 (16 heads of 64, 1500 rows: 62 us cut finest, 10.9 us), 4 for 125,
+    // 8 for 512 (27.8 -> 21.8 us), which sqrt(n / 6) follows.  The workers left are spread over the SMs.
+    auto limit_workers = [&]() {
+        if constexpr (MODE != kStep) {
+            split.W = limited_workers(VP[p.B], p.B * segs, 6.f, Wmax);
+            wid = split.W < Wmax ? warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)
+                                 : static_cast<int>(blockIdx.x) * TL::WARPS + warp;
+        }
+    };
+    limit_workers();
     int t_begin = split.begin(wid);
     int n_my = split.begin(wid + 1) - t_begin;
     if (n_my > 0 && lane == 0 && !p.block_table) {
@@ -466,6 +487,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         if (!warp_rendezvous(rv, TL::WARPS, p.wait_cycles, p.err, lane)) return;
         if (warp == 0) ovf = build_prefix<MODE>(p, T, segs, TL::ALPHA, P, VP, Ls, lane);
         if (!warp_rendezvous(rv, 2 * TL::WARPS, p.wait_cycles, p.err, lane)) return;
+        limit_workers();
         t_begin = split.begin(wid);
         n_my = split.begin(wid + 1) - t_begin;
     }

@@ -478,9 +478,15 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const long long W = gridDim.x;
     const int wid = blockIdx.x;
-    const PassSplit<LY::ALPHA> split{P, VP, p.B, spp, np, static_cast<int>(W)};
+    PassSplit<LY::ALPHA> split{P, VP, p.B, spp, np, static_cast<int>(gridDim.x), LY::ALPHA};
+    // kScored, kCross: a short tile space is cut into fewer pieces (see the CUDA-core kernel); a
+    // piece, with its G x D partial, costs the merge about half a tile's time
+    auto limit_workers = [&]() {
+        if constexpr (MODE != kStep)
+            split.W = limited_workers(np * VP[p.B], p.B * spp * np, 2.f, static_cast<int>(gridDim.x));
+    };
+    limit_workers();
     int t_begin = split.begin(wid);
     int n_my = split.begin(wid + 1) - t_begin;
     if (n_my > 0 && tid == 0 && !p.block_table) {
@@ -528,6 +534,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
         const int pr = replan<MODE>(p, TM, spp, LY::ALPHA, P, VP, Ls, rv);
         const bool ok = pr >= 0;
         ovf = pr > 0;
+        if (ok) limit_workers();
         t_begin = split.begin(wid);
         n_my = ok ? split.begin(wid + 1) - t_begin : 0;
         if (!ok) *abort_flag = 1;
@@ -837,12 +844,8 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                     float pq[GH];  // weights against the current references, kept until the vote
                     ld_rows(scol, pq);
                     if constexpr (MODE == kScored) {
-                        float* srow = p.scores + score_row(p, cu.b, kvh, hb * QB + c0) * p.Lmax + t0 + r;
 #pragma unroll
-                        for (int jj = 0; jj < GH; ++jj) {
-                            pq[jj] *= p.sscale;
-                            if (full || visible(jj)) srow[static_cast<size_t>(jj) * p.Lmax] = pq[jj];
-                        }
+                        for (int jj = 0; jj < GH; ++jj) pq[jj] *= p.sscale;
                     }
                     if (!full) {
 #pragma unroll
@@ -930,7 +933,21 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                     if (leader) {
                         // the weights are in place and S buffer k & 1 is read
                         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(kPFull)) : "memory");
-                        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(kSFree + (k & 1))) : "memory");
+                        if constexpr (MODE != kScored)
+                            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(kSFree + (k & 1))) : "memory");
+                    }
+                    if constexpr (MODE == kScored) {
+                        // the scores, read from TMEM once more while the weights go through the MMAs;
+                        // the S buffer is free after that
+                        float* srow = p.scores + score_row(p, cu.b, kvh, hb * QB + c0) * p.Lmax + t0 + r;
+                        ld_rows(scol, pq);
+#pragma unroll
+                        for (int jj = 0; jj < GH; ++jj)
+                            if (full || visible(jj)) srow[static_cast<size_t>(jj) * p.Lmax] = pq[jj] * p.sscale;
+                        tc::tc_fence_before();
+                        tc::named_bar_sync(1, SMX);
+                        if (leader)
+                            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(kSFree + (k & 1))) : "memory");
                     }
                     if (i + 1 < ntl) advance_pass(cu, P, p.B, spp, np);
                 }

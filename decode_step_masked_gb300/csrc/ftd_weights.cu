@@ -20,7 +20,7 @@ namespace ftd {
 namespace {
 
 constexpr int kThreadsW = 128;
-constexpr int kPosW = 4 * kThreadsW;  // positions per block
+constexpr int kMaxRowsPerThread = 12;
 
 // Cache-plane row of position t (a multiple of 4 and the three after it: pages are multiples of 128)
 __device__ __forceinline__ long long plane_row(const WeightsParams& p, int b, int kvh, int t) {
@@ -30,76 +30,186 @@ __device__ __forceinline__ long long plane_row(const WeightsParams& p, int b, in
     return ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
 }
 
+// Each thread owns Q quads of four positions, a block's quads kThreadsW apart: with few
+// query rows a quad is one or two 16-byte loads of scores, and several are kept in flight.
+template <int Q>
 __global__ void __launch_bounds__(kThreadsW) weights_kernel(const WeightsParams p) {
     grid_dep_wait();
     grid_dep_launch();
-    const int chunks = (p.Lmax + kPosW - 1) / kPosW;
+    constexpr int POS = 4 * kThreadsW * Q;  // positions per block
+    const int chunks = (p.Lmax + POS - 1) / POS;
     const int seg = blockIdx.x / chunks, chunk = blockIdx.x - seg * chunks;
     const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
     const int L = __ldcg(p.seq_lens + b);
     if (L < 0 || L > p.Lmax - p.nq) return;  // inactive or overflowing: the planes stay as they are
-    const int t = chunk * kPosW + 4 * threadIdx.x;
     const int end = L + p.nq;
-    if (t >= end) return;
+    if (chunk * POS >= end) return;
     const int start = window_start(L, p.window);  // the oldest position any row sees
-    const bool unseen = t + 3 < start;
-    if (unseen && p.acc_out == p.acc) return;
-    const long long row = plane_row(p, b, kvh, t);
-    if (row < 0) return;
-    float a[4];
-    *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(p.acc + row);
+    int t[Q];
+    long long row[Q];  // -1: nothing to do
+    float a[Q][4], sum[Q][4];  // the old weights, and what this call adds (summed apart: one rounding against a)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (t + i >= L) a[i] = 0.f;
-    if (!unseen) {
-        const int rows = p.nq * p.group;
-        const size_t r0 = static_cast<size_t>(seg) * rows;
-        const float* s = p.scores + r0 * p.Lmax + t;
-        const float2* st = p.stats + r0;
-        for (int tok = 0; tok < p.nq; ++tok) {
-            const int hi = L + tok, lo = p.window > 0 ? hi + 1 - p.window : 0;  // this token sees lo .. hi
-            if (t <= hi && t + 3 >= lo) {
-                const float* sr = s + static_cast<size_t>(tok) * p.group * p.Lmax;
-                const float2* str = st + tok * p.group;
-                float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-                for (int g = 0; g < p.group; ++g) {
-                    const float4 x = __ldcs(reinterpret_cast<const float4*>(sr + static_cast<size_t>(g) * p.Lmax));
-                    const float2 ml = __ldcg(str + g);
-                    w[0] = fmaf(exp2f(x.x - ml.x), ml.y, w[0]);
-                    w[1] = fmaf(exp2f(x.y - ml.x), ml.y, w[1]);
-                    w[2] = fmaf(exp2f(x.z - ml.x), ml.y, w[2]);
-                    w[3] = fmaf(exp2f(x.w - ml.x), ml.y, w[3]);
-                }
-                // (scores outside lo .. hi were never written: whatever they gave is dropped)
+    for (int i = 0; i < Q; ++i) {
+        t[i] = chunk * POS + (i * kThreadsW + static_cast<int>(threadIdx.x)) * 4;
+        row[i] = t[i] >= end || (t[i] + 3 < start && p.acc_out == p.acc) ? -1 : plane_row(p, b, kvh, t[i]);
+    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (t + i >= lo && t + i <= hi) a[i] += w[i];
+    for (int i = 0; i < Q; ++i) {
+        const float4 x = row[i] >= 0 ? *reinterpret_cast<const float4*>(p.acc + row[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        a[i][0] = x.x;
+        a[i][1] = x.y;
+        a[i][2] = x.z;
+        a[i][3] = x.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
+    }
+    const size_t r0 = static_cast<size_t>(seg) * (p.nq * p.group);
+    float w[Q][4];
+    for (int tok = 0; tok < p.nq; ++tok) {
+        const int hi = L + tok, lo = p.window > 0 ? hi + 1 - p.window : 0;  // this token sees lo .. hi
+        const float* s = p.scores + (r0 + static_cast<size_t>(tok) * p.group) * p.Lmax;
+        const float2* st = p.stats + r0 + tok * p.group;
+        bool live[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            live[i] = row[i] >= 0 && t[i] <= hi && t[i] + 3 >= lo;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[i][e] = 0.f;
+        }
+#pragma unroll (8 / Q)
+        for (int g = 0; g < p.group; ++g) {
+            const float2 ml = __ldcg(st + g);
+            float4 x[Q];
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+                if (live[i]) x[i] = __ldcs(reinterpret_cast<const float4*>(s + static_cast<size_t>(g) * p.Lmax + t[i]));
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                if (!live[i]) continue;
+                w[i][0] = fmaf(exp2f(x[i].x - ml.x), ml.y, w[i][0]);
+                w[i][1] = fmaf(exp2f(x[i].y - ml.x), ml.y, w[i][1]);
+                w[i][2] = fmaf(exp2f(x[i].z - ml.x), ml.y, w[i][2]);
+                w[i][3] = fmaf(exp2f(x[i].w - ml.x), ml.y, w[i][3]);
             }
         }
-    }
-    if (t + 3 < end) {
-        *reinterpret_cast<float4*>(p.acc_out + row) = make_float4(a[0], a[1], a[2], a[3]);
-    } else {
+        // (scores outside lo .. hi were never written: whatever they gave is dropped)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (t + i < end) p.acc_out[row + i] = a[i];
-    }
-    if (p.positions && t + 3 >= L) {
-        const int base = __ldcg(p.next_pos + b) - L;
+        for (int i = 0; i < Q; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (t + i >= L && t + i < end) p.positions[row + i] = base + t + i;
+            for (int e = 0; e < 4; ++e)
+                if (live[i] && t[i] + e >= lo && t[i] + e <= hi) sum[i][e] += w[i][e];
     }
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        if (row[i] < 0) continue;
+        // the new tokens' positions start from 0, not from what acc holds there
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[i][e] = (t[i] + e < L ? a[i][e] : 0.f) + sum[i][e];
+        if (t[i] + 3 < end) {
+            *reinterpret_cast<float4*>(p.acc_out + row[i]) = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t[i] + e < end) p.acc_out[row[i] + e] = a[i][e];
+        }
+        if (p.positions && t[i] + 3 >= L) {
+            const int base = __ldcg(p.next_pos + b) - L;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t[i] + e >= L && t[i] + e < end) p.positions[row[i] + e] = base + t[i] + e;
+        }
+    }
+}
+
+// Many query rows: a block's warps take every kWarpsW-th row of the same 128 positions and add up
+// through shared memory, in warp order.
+constexpr int kWarpsW = 8;
+__global__ void __launch_bounds__(32 * kWarpsW) weights_rows_kernel(const WeightsParams p) {
+    __shared__ float4 part[kWarpsW][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    constexpr int POS = 128;
+    const int chunks = (p.Lmax + POS - 1) / POS;
+    const int seg = blockIdx.x / chunks, chunk = blockIdx.x - seg * chunks;
+    const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int L = __ldcg(p.seq_lens + b);
+    if (L < 0 || L > p.Lmax - p.nq) return;
+    const int end = L + p.nq, t0 = chunk * POS, t = t0 + 4 * lane;
+    if (t0 >= end || (t0 + POS <= window_start(L, p.window) && p.acc_out == p.acc)) return;
+    const int rows = p.nq * p.group;
+    const size_t r0 = static_cast<size_t>(seg) * rows;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 4;
+    for (int r = warp; r < rows; r += U * kWarpsW) {
+        float4 x[U];
+        float2 ml[U];
+        int hi[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = r + u * kWarpsW;
+            hi[u] = -1;
+            if (i < rows) {
+                hi[u] = L + i / p.group;  // the row's token sees positions up to hi
+                ml[u] = __ldcg(p.stats + r0 + i);
+                x[u] = __ldcs(reinterpret_cast<const float4*>(p.scores + (r0 + i) * p.Lmax + t));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (hi[u] < 0) continue;
+            const int lo = p.window > 0 ? hi[u] + 1 - p.window : 0;
+            const float s[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // (scores outside lo .. hi were never written)
+                if (t + e >= lo && t + e <= hi[u]) w[e] = fmaf(exp2f(s[e] - ml[u].x), ml[u].y, w[e]);
+        }
+    }
+    part[warp][lane] = make_float4(w[0], w[1], w[2], w[3]);
+    __syncthreads();
+    if (warp != 0 || t >= end) return;
+    const long long row = plane_row(p, b, kvh, t);
+    if (row < 0) return;
+    const float4 old = *reinterpret_cast<const float4*>(p.acc + row);
+    float a[4] = {old.x, old.y, old.z, old.w}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kWarpsW; ++k) {
+        const float4 x = part[k][lane];
+        sum[0] += x.x;
+        sum[1] += x.y;
+        sum[2] += x.z;
+        sum[3] += x.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = (t + e < L ? a[e] : 0.f) + sum[e];  // one rounding against the old weight
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (t + e >= end) break;
+        p.acc_out[row + e] = a[e];
+        if (p.positions && t + e >= L) p.positions[row + e] = __ldcg(p.next_pos + b) + t + e - L;
+    }
+}
+
+template <int Q>
+cudaError_t launch(const WeightsParams& p, cudaStream_t stream) {
+    const int chunks = (p.Lmax + 4 * kThreadsW * Q - 1) / (4 * kThreadsW * Q);
+    void* args[] = {const_cast<WeightsParams*>(&p)};
+    return launch_pdl(reinterpret_cast<const void*>(&weights_kernel<Q>),
+                      dim3(static_cast<unsigned>(p.B) * p.Hkv * chunks), kThreadsW, 0, args, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream) {
-    const int chunks = (p.Lmax + kPosW - 1) / kPosW;
+    // (above kMaxRowsPerThread rows, warps share them.) Four quads a thread for one or two query rows per kv head, one for eight and more (their rows
+    // keep the loads in flight).
+    const int rows = p.nq * p.group;
+    if (rows <= 2) return launch<4>(p, stream);
+    if (rows <= 4) return launch<2>(p, stream);
+    if (rows <= kMaxRowsPerThread) return launch<1>(p, stream);
     void* args[] = {const_cast<WeightsParams*>(&p)};
-    return launch_pdl(reinterpret_cast<const void*>(&weights_kernel),
-                      dim3(static_cast<unsigned>(p.B) * p.Hkv * chunks), kThreadsW, 0, args, stream);
+    return launch_pdl(reinterpret_cast<const void*>(&weights_rows_kernel),
+                      dim3(static_cast<unsigned>(p.B) * p.Hkv * ((p.Lmax + 127) / 128)), 32 * kWarpsW, 0, args, stream);
 }
 
 }  // namespace ftd

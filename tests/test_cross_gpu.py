@@ -68,6 +68,13 @@ SHAPES = {
     "wide32": ("bf16", "bf16", 32, 1, 128, False),
     "wide64": ("f16", "f16", 64, 1, 128, False),
     "two_wide": ("bf16", "bf16", 128, 1, 128, False),
+    # rows that fill no block of 4: padded tensor-core blocks, and 17, which no block divides
+    "gqa7": ("bf16", "bf16", 14, 2, 128, False),
+    "gqa3": ("f16", "f16", 6, 2, 128, False),
+    "gqa20": ("bf16", "bf16", 20, 1, 128, False),
+    "gqa17": ("f16", "f16", 17, 1, 128, False),
+    "gqa7_i8": ("i8", "f16", 14, 2, 128, False),
+    "gqa12_i8": ("i8", "f16", 24, 2, 128, False),
 }
 LENS = [0, 1, 2, 31, 127, 128, 129, 500, -3, 640]
 
@@ -118,6 +125,19 @@ def test_too_long_memory_is_skipped_and_reported(shape):
     assert status == ftd.FTD_ERR_SEQ_OVERFLOW
     assert not got[1:].any()
     assert_close(got[:1], expect(w, inp)[:1], i8=cache == "i8", what=shape)
+
+
+@pytest.mark.parametrize("shape", ["gqa8_tc", "gqa16_tc", "mha_bf16", "wide32"])
+def test_large_batches(shape):
+    """Up to the largest batch: past 788 slots the 16-row blocks' split has no room for its weights."""
+    cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
+    for B in (788, 789, 1024):
+        lens = np.random.default_rng(B).integers(0, 33, B)
+        lens[7], lens[B - 1] = 32, 0
+        w, inp = case(cache, qkv, B, Hq // Hkv, 1, D, 32, lens)
+        got, status = run(w, inp, cuda_core=cc)
+        assert status == ftd.FTD_OK
+        assert_close(got, expect(w, inp), what=f"{shape} B {B}")
 
 
 def test_every_memory_empty():

@@ -41,6 +41,13 @@ SHAPES = {
     "wide32": ("bf16", "bf16", 32, 1, 128, False),
     "wide64": ("f16", "f16", 64, 1, 128, False),
     "two_wide": ("bf16", "bf16", 128, 1, 128, False),
+    # rows that fill no block of 4: padded tensor-core blocks, and 17, which no block divides
+    "gqa7": ("bf16", "bf16", 14, 2, 128, False),
+    "gqa3": ("f16", "f16", 6, 2, 128, False),
+    "gqa20": ("bf16", "bf16", 20, 1, 128, False),
+    "gqa17": ("f16", "f16", 17, 1, 128, False),
+    "gqa7_i8": ("i8", "f16", 14, 2, 128, False),
+    "gqa12_i8": ("i8", "f16", 24, 2, 128, False),
 }
 
 
