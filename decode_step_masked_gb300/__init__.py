@@ -185,8 +185,8 @@ def ftd_set_rope(ctx, cfg: Optional[FtdRopeConfig]) -> int:
 
 def ftd_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out, k_out, v_out,
                  stream) -> int:
-    return load_library().ftd_rope_qkv(*_ptrs(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens,
-                                              q_out, k_out, v_out, stream))
+    return load_library().ftd_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out, k_out,
+                                       v_out, stream)
 
 
 def ftd_enable_scores(ctx, stream) -> int:
@@ -195,20 +195,18 @@ def ftd_enable_scores(ctx, stream) -> int:
 
 def ftd_decode_mha_scored(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, next_pos,
                           acc, acc_out, positions, out, stream) -> int:
-    return load_library().ftd_decode_mha_scored(*_ptrs(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table,
-                                                       seq_lens, scales, next_pos, acc, acc_out, positions, out,
-                                                       stream))
+    return load_library().ftd_decode_mha_scored(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table,
+                                                seq_lens, scales, next_pos, acc, acc_out, positions, out, stream)
 
 
 def ftd_cache_evict(ctx, k_cache, v_cache, scales, block_table, seq_lens, next_pos, acc, acc_out, positions,
                     positions_out, new_lens, budget, recent, sinks, stream) -> int:
-    return load_library().ftd_cache_evict(*_ptrs(ctx, k_cache, v_cache, scales, block_table, seq_lens, next_pos, acc,
-                                                 acc_out, positions, positions_out, new_lens, budget, recent, sinks,
-                                                 stream))
+    return load_library().ftd_cache_evict(ctx, k_cache, v_cache, scales, block_table, seq_lens, next_pos, acc, acc_out,
+                                          positions, positions_out, new_lens, budget, recent, sinks, stream)
 
 
 def ftd_cross_mha(ctx, q, q_bias, k_mem, v_mem, mem_lens, scales, out, stream) -> int:
-    return load_library().ftd_cross_mha(*_ptrs(ctx, q, q_bias, k_mem, v_mem, mem_lens, scales, out, stream))
+    return load_library().ftd_cross_mha(ctx, q, q_bias, k_mem, v_mem, mem_lens, scales, out, stream)
 
 
 def ftd_decode_mha_host(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, seq_lens, scales, out,
@@ -253,6 +251,13 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+def _current_stream(device: int) -> int:
+    """torch's current stream on a device, as an address (without a Stream object where torch has a way)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _row_stride(t, width: int, head_dim: int) -> int:
     """Elements from one token's row of ``width`` elements (heads flattened, or [heads, head_dim]) to the next; 0: dense."""
     if t.is_contiguous():
@@ -289,6 +294,8 @@ class DecodeStep:
         st, ctx = ftd_init(self.cfg, s)
         check(st)
         self.ctx = ctx
+        self.device = torch.cuda.current_device()
+        self._widths = (n_q_heads * head_dim, n_kv_heads * head_dim, head_dim)
         if scored:
             self.enable_scores(s)
 
@@ -324,37 +331,39 @@ class DecodeStep:
 
     def enable_scores(self, stream: Optional[int] = None):
         """Allocate what ``scored`` and ``evict`` need (``scored=True`` does it at construction)."""
-        import torch
-        check(ftd_enable_scores(self.ctx, torch.cuda.current_stream().cuda_stream if stream is None else stream))
+        check(ftd_enable_scores(self.ctx, _current_stream(self.device) if stream is None else stream))
 
     def scored(self, q, k_new, v_new, seq_lens, next_pos, acc, positions, out, acc_out=None, bias=None, k_cache=None,
                v_cache=None, scales=None, block_table=None, stream: Optional[int] = None):
         """The step, which also adds every position's attention weight to ``acc`` (into ``acc_out`` when
         given); the new rows of ``positions`` (may be None, with next_pos) become next_pos, next_pos + 1, ..."""
-        import torch
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
-        check(ftd_decode_mha_scored(self.ctx, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(bias), _ptr(k_cache),
-                                    _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(scales), _ptr(next_pos),
-                                    _ptr(acc), _ptr(acc_out), _ptr(positions), _ptr(out), s))
+        s = _current_stream(self.device) if stream is None else stream
+        st = ftd_decode_mha_scored(self.ctx, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _ptr(bias), _ptr(k_cache),
+                                   _ptr(v_cache), _ptr(block_table), seq_lens.data_ptr(), _ptr(scales), _ptr(next_pos),
+                                   acc.data_ptr(), _ptr(acc_out), _ptr(positions), out.data_ptr(), s)
+        if st:
+            check(st)
 
     def evict(self, acc, positions, seq_lens, next_pos, new_lens, budget, recent=0, sinks=0, acc_out=None,
               positions_out=None, k_cache=None, v_cache=None, scales=None, block_table=None,
               stream: Optional[int] = None):
         """Bring every slot down to ``budget`` rows per kv head by accumulated weight (``new_lens`` may be
         ``seq_lens``; planes change in place unless ``acc_out`` / ``positions_out`` are given)."""
-        import torch
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
-        check(ftd_cache_evict(self.ctx, _ptr(k_cache), _ptr(v_cache), _ptr(scales), _ptr(block_table),
-                              _ptr(seq_lens), _ptr(next_pos), _ptr(acc), _ptr(acc_out), _ptr(positions),
-                              _ptr(positions_out), _ptr(new_lens), int(budget), int(recent), int(sinks), s))
+        s = _current_stream(self.device) if stream is None else stream
+        st = ftd_cache_evict(self.ctx, _ptr(k_cache), _ptr(v_cache), _ptr(scales), _ptr(block_table),
+                             seq_lens.data_ptr(), next_pos.data_ptr(), acc.data_ptr(), _ptr(acc_out),
+                             positions.data_ptr(), _ptr(positions_out), new_lens.data_ptr(), budget, recent, sinks, s)
+        if st:
+            check(st)
 
     def cross(self, q, mem_lens, out, q_bias=None, k_mem=None, v_mem=None, scales=None,
               stream: Optional[int] = None):
         """Cross attention of the slots' tokens to memories of ``mem_lens`` rows (None: the context's pool)."""
-        import torch
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
-        check(ftd_cross_mha(self.ctx, _ptr(q), _ptr(q_bias), _ptr(k_mem), _ptr(v_mem), _ptr(mem_lens), _ptr(scales),
-                            _ptr(out), s))
+        s = _current_stream(self.device) if stream is None else stream
+        st = ftd_cross_mha(self.ctx, q.data_ptr(), _ptr(q_bias), _ptr(k_mem), _ptr(v_mem), mem_lens.data_ptr(),
+                           _ptr(scales), out.data_ptr(), s)
+        if st:
+            check(st)
 
     def set_rope(self, n_axes=1, sections=None, rotary_dim=0, theta=0.0, pairing="halves", order="sections",
                  inv_freq=None):
@@ -379,16 +388,17 @@ class DecodeStep:
         """Bias and rotary positions for the tokens of q, k (and v, which only takes the bias; None with
         v_out None): rows of heads a fixed stride apart, such as slices of a fused projection.  positions is
         int32 [n_axes, tokens]; the outputs are dense and may be their own dense inputs."""
-        import torch
-        s = torch.cuda.current_stream().cuda_stream if stream is None else stream
-        c = self.cfg
-        qw, kw = c.n_q_heads * c.head_dim, c.n_kv_heads * c.head_dim
+        s = _current_stream(self.device) if stream is None else stream
+        qw, kw, d = self._widths
         n = q.numel() // qw
-        qs, ks = _row_stride(q, qw, c.head_dim), _row_stride(k, kw, c.head_dim)
-        if v is not None and (_row_stride(v, kw, c.head_dim) or kw) != (ks or kw) and n > 1:
+        qs = 0 if q.is_contiguous() else _row_stride(q, qw, d)
+        ks = 0 if k.is_contiguous() else _row_stride(k, kw, d)
+        if v is not None and ((0 if v.is_contiguous() else _row_stride(v, kw, d)) or kw) != (ks or kw) and n > 1:
             raise ValueError("k and v must share one row stride")
-        check(ftd_rope_qkv(self.ctx, _ptr(q), _ptr(k), _ptr(v), qs, ks, _ptr(bias), _ptr(positions), n, _ptr(q_out),
-                           _ptr(k_out), _ptr(v_out), s))
+        st = ftd_rope_qkv(self.ctx, q.data_ptr(), k.data_ptr(), _ptr(v), qs, ks, _ptr(bias), positions.data_ptr(), n,
+                          q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out), s)
+        if st:
+            check(st)
 
     def get_error(self) -> int:
         return ftd_get_error(self.ctx)

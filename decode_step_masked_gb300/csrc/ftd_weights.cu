@@ -34,16 +34,17 @@ __device__ __forceinline__ long long plane_row(const WeightsParams& p, int b, in
 // query rows a quad is one or two 16-byte loads of scores, and several are kept in flight.
 template <int Q>
 __global__ void __launch_bounds__(kThreadsW) weights_kernel(const WeightsParams p) {
-    grid_dep_wait();
-    grid_dep_launch();
+    // Everything but the scores and their statistics is older than the step's kernel, which
+    // lets this grid start only after its own wait, and which writes none of it: lengths, pages and old
+    // weights are read while that kernel finishes.  Every block waits for it, those without work
+    // too: the next launch on the stream counts on this grid's end to come after the step's.
     constexpr int POS = 4 * kThreadsW * Q;  // positions per block
     const int chunks = (p.Lmax + POS - 1) / POS;
     const int seg = blockIdx.x / chunks, chunk = blockIdx.x - seg * chunks;
     const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
     const int L = __ldcg(p.seq_lens + b);
-    if (L < 0 || L > p.Lmax - p.nq) return;  // inactive or overflowing: the planes stay as they are
-    const int end = L + p.nq;
-    if (chunk * POS >= end) return;
+    // inactive or overflowing slots: the planes stay as they are
+    const int end = L < 0 || L > p.Lmax - p.nq ? 0 : L + p.nq;
     const int start = window_start(L, p.window);  // the oldest position any row sees
     int t[Q];
     long long row[Q];  // -1: nothing to do
@@ -64,6 +65,9 @@ __global__ void __launch_bounds__(kThreadsW) weights_kernel(const WeightsParams 
         for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
     }
     const size_t r0 = static_cast<size_t>(seg) * (p.nq * p.group);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (chunk * POS >= end) return;
     float w[Q][4];
     for (int tok = 0; tok < p.nq; ++tok) {
         const int hi = L + tok, lo = p.window > 0 ? hi + 1 - p.window : 0;  // this token sees lo .. hi
@@ -126,14 +130,14 @@ __global__ void __launch_bounds__(kThreadsW) weights_kernel(const WeightsParams 
 constexpr int kWarpsW = 8;
 __global__ void __launch_bounds__(32 * kWarpsW) weights_rows_kernel(const WeightsParams p) {
     __shared__ float4 part[kWarpsW][32];
-    grid_dep_wait();
-    grid_dep_launch();
     constexpr int POS = 128;
     const int chunks = (p.Lmax + POS - 1) / POS;
     const int seg = blockIdx.x / chunks, chunk = blockIdx.x - seg * chunks;
     const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = __ldcg(p.seq_lens + b);
+    grid_dep_wait();  // (as in weights_kernel)
+    grid_dep_launch();
     if (L < 0 || L > p.Lmax - p.nq) return;
     const int end = L + p.nq, t0 = chunk * POS, t = t0 + 4 * lane;
     if (t0 >= end || (t0 + POS <= window_start(L, p.window) && p.acc_out == p.acc)) return;
