@@ -18,13 +18,21 @@
 // a cache is kept at its budget from step to step, makes them itself; else it appends them
 // to the call's list (one atomic add reserves its part; the list's order varies, its
 // moves are independent).
-// move_kernel deals the list out to all warps in chunks of 4 KB, so that ragged slots
+// move_kernel deals the list out to all warps in chunks of 2 KB, so that ragged slots
 // do not leave SMs idle, and writes the new lengths, which may overwrite the old ones: every
 // cluster has read them by then.
 //
 // Bound: 8 bytes per position for the selection, then the moved rows, read and written.
+// Measured: one row over in each of 8 x 32 heads of 2049 rows 9.2 us a call in a graph (launches,
+// the selection's chain of barriers and two dependent reads of memory); 32 ragged slots of 40
+// heads cut to 2048 rows 129 us, of which the moves take about 110 at 5.6 TB/s; 4 x 8 heads of 65536
+// INT8 rows cut to 8192 49 us, half of it the selection, half 128-byte rows gathered and scattered.
+// With 4 KB a warp in flight the moves took 15 % longer, with 512 threads three times an SM 12 %:
+// more reads and writes in flight at once than that slow one another down.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "ftd_ops.cuh"
 
@@ -38,8 +46,8 @@ constexpr int kWarpsE = kThreadsE / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSmemKeys = 48 * 1024;  // keys of a block that fit shared memory (192 KB)
 constexpr int kLocalMoves = kMaxLocalMoves / kMaxCluster;  // moves per block that a cluster makes itself
-constexpr int kMoveThreads = 512;
-constexpr int kMoveU = 8;                 // 16-byte words a lane has in flight: 4 KB a warp
+constexpr int kMoveThreads = 256;
+constexpr int kMoveU = 4;                 // 16-byte words a lane has in flight: 2 KB a warp
 
 // Cache row of position index t, -1 behind a bad page (rows are below 2^31).
 __device__ __forceinline__ int evict_row(const EvictParams& p, int b, int kvh, int t) {
@@ -112,6 +120,7 @@ template <bool MULTI>
 __device__ __forceinline__ void evict_segment(const EvictParams& p, uint32_t* skeys, int seg, int rank, int cl) {
     __shared__ Shared sh;
     __shared__ __align__(16) uint32_t tot[256];
+    __shared__ int2 few[kLocalMoves];
     __shared__ int wsum[kWarpsE], wsum2[kWarpsE];
     __shared__ int found[3];  // digit, rows needed of it, keys with it
     constexpr unsigned FULL = 0xffffffffu;
@@ -159,7 +168,7 @@ __device__ __forceinline__ void evict_segment(const EvictParams& p, uint32_t* sk
     uint32_t* keys = S * kWarpsE <= p.smem_keys ? skeys : p.keys + static_cast<size_t>(seg) * p.Lmax + c0;
     const long long fresh = static_cast<long long>(__ldcg(p.next_pos + b)) - p.recent;
     bool bad = false;
-    constexpr int U = 4;  // rows a lane has in flight
+    constexpr int U = MULTI ? 8 : 4;  // rows a lane has in flight
     for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
         float a[U];
         int ps[U], row[U];
@@ -276,26 +285,36 @@ __device__ __forceinline__ void evict_segment(const EvictParams& p, uint32_t* sk
             ties_before += static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(lane < rank ? v : 0)));
         }
     }
-    auto kept_at = [&](int t, int& ties) {  // whole warp, consecutive groups in order
-        const uint32_t k = t < w1 ? keys[t - c0] : 0u;
-        bool kept = t < w1 && (whole ? k >= lo : k > lo);
-        if (!whole) {
-            const bool tie = t < w1 && k == lo;
-            const unsigned m = __ballot_sync(FULL, tie);
-            if (tie) kept = ties + __popc(m & ((1u << lane) - 1u)) < need;
-            ties += __popc(m);
+    // Calls f(t, ev, nb) for the warp's rows, 32 at a time in order: nb of the 32 lie below the budget,
+    // and ev says whether row t is a hole (below, not kept) or has to move (kept, not below).
+    auto for_rows = [&](auto all, auto&& f) {
+        int ties = ties_before;
+#pragma unroll 4
+        for (int t0 = w0; t0 < w1; t0 += 32) {
+            const int t = t0 + lane;
+            const bool in = t < w1;
+            const uint32_t k = in ? keys[t - c0] : 0u;
+            bool kept = k >= lo;
+            if constexpr (!decltype(all)::value) {
+                const bool tie = in && k == lo;
+                const unsigned m = __ballot_sync(FULL, tie);
+                if (tie) kept = ties + __popc(m & ((1u << lane) - 1u)) < need;
+                ties += __popc(m);
+            }
+            const int nb = p.budget - t0;
+            f(t, in && kept == (lane >= nb), nb);
         }
-        return kept;
     };
     // ---- holes below the budget and kept rows from it on: counted, then listed ----
-    int holes = 0, movers = 0, ties = ties_before;
-#pragma unroll 2
-    for (int t0 = w0; t0 < w1; t0 += 32) {
-        const int t = t0 + lane;
-        const bool kept = kept_at(t, ties);
-        holes += __popc(__ballot_sync(FULL, t < w1 && t < p.budget && !kept));
-        movers += __popc(__ballot_sync(FULL, t >= p.budget && kept));
-    }
+    int holes = 0, movers = 0;
+    auto count = [&](int, bool ev, int nb) {
+        holes += ev && lane < nb;
+        movers += ev && lane >= nb;
+    };
+    if (whole) for_rows(std::true_type{}, count);
+    else for_rows(std::false_type{}, count);
+    holes = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(holes)));
+    movers = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(movers)));
     if (lane == 0) {
         wsum[warp] = holes;
         wsum2[warp] = movers;
@@ -317,31 +336,30 @@ __device__ __forceinline__ void evict_segment(const EvictParams& p, uint32_t* sk
     }
     // the moves' place: shared by the whole call, or, for few, this cluster's own
     const bool local = total <= kLocalMoves * cl;
-    int2* list = p.local_moves + static_cast<size_t>(seg) * kMaxLocalMoves;
+    int2* list = MULTI ? p.local_moves + static_cast<size_t>(seg) * kMaxLocalMoves : few;
     if (!local) {
         if (rank == 0 && tid == 0) sh.list_base = atomicAdd(p.count, static_cast<uint32_t>(total));
         meet();
         list = p.moves + *peer(&sh.list_base, 0);
     }
-    ties = ties_before;
-#pragma unroll 2
-    for (int t0 = w0; t0 < w1; t0 += 32) {
-        const int t = t0 + lane;
-        const bool kept = kept_at(t, ties);
-        const bool hole = t < w1 && t < p.budget && !kept, mover = t >= p.budget && kept;
-        const unsigned hm = __ballot_sync(FULL, hole), mm = __ballot_sync(FULL, mover);
-        const unsigned below = (1u << lane) - 1u;
-        if (hole || mover) {
+    auto enter = [&](int t, bool ev, int nb) {
+        const unsigned m = __ballot_sync(FULL, ev);
+        if (!m) return;
+        const unsigned low = nb >= 32 ? FULL : nb <= 0 ? 0u : (1u << nb) - 1u;  // the rows below the budget
+        const unsigned before = (1u << lane) - 1u;
+        if (ev) {
             const int row = evict_row(p, b, kvh, t);
-            if (hole) list[holes + __popc(hm & below)].y = row;
-            else list[movers + __popc(mm & below)].x = row;
+            if (lane < nb) list[holes + __popc(m & low & before)].y = row;
+            else list[movers + __popc(m & ~low & before)].x = row;
         }
-        holes += __popc(hm);
-        movers += __popc(mm);
-    }
+        holes += __popc(m & low);
+        movers += __popc(m & ~low);
+    };
+    if (whole) for_rows(std::true_type{}, enter);
+    else for_rows(std::false_type{}, enter);
     meet();  // the list is complete (and no block's shared memory is read past this point)
     if (local)
-        for (int m = rank * kWarpsE + warp; m < total; m += cl * kWarpsE) copy_rows(p, __ldcg(list + m), 1, lane);
+        for (int m = rank * kWarpsE + warp; m < total; m += cl * kWarpsE) copy_rows(p, MULTI ? __ldcg(list + m) : list[m], 1, lane);
 }
 
 template <bool MULTI>
@@ -358,7 +376,7 @@ __global__ void __launch_bounds__(kThreadsE, 2) select_kernel(const EvictParams 
     evict_segment<MULTI>(p, skeys, static_cast<int>(blockIdx.x) / cl, rank, cl);
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictParams p) {
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31;
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const EvictParams
     if (M == 0) return;
     // Chunks of neighbouring rows in turn, so that all warps work in the same part of the cache; the
     // next chunk's moves are loaded while this one's rows are copied.
-    const int rows = 32 * kMoveU * 8 / p.row_bytes;  // 4 KB of K and V (4 to 32 rows)
+    const int rows = 32 * kMoveU * 8 / p.row_bytes;  // 2 KB of K and V (2 to 16 rows)
     const long long step = static_cast<long long>(W) * rows;
     long long m0 = static_cast<long long>(w) * rows;
     int2 mv = make_int2(0, 0);
@@ -414,7 +432,7 @@ cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream) {
     void* args[] = {&p};
     const cudaError_t e = launch_pdl(fn, dim3(static_cast<unsigned>(segs * cl)), kThreadsE, p.smem_keys * 4, args, stream, cl);
     if (e != cudaSuccess) return e;
-    return launch_pdl(reinterpret_cast<const void*>(&move_kernel), dim3(static_cast<unsigned>(sms) * 2), kMoveThreads, 0,
+    return launch_pdl(reinterpret_cast<const void*>(&move_kernel), dim3(static_cast<unsigned>(sms) * 4), kMoveThreads, 0,
                       args, stream);
 }
 
