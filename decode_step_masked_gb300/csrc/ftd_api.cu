@@ -84,23 +84,23 @@ EncodeTiledFn encode_tiled() {
     return fn;
 }
 
-// 2-D view of a [B][Hkv][Lmax][128] cache as rows of 128 elements, read in
+// 2-D view of a [B][Hkv][Lmax][D] cache as rows of D elements, read in
 // boxes of 128 rows with the 128-byte swizzle: 64 columns per box for fp16/bf16
-// (the tensor-core operand layout), whole 128-byte rows for INT8 (the kernel
-// converts those to the operand layout itself).
-bool encode_cache_map(CUtensorMap* map, void* base, ftd_dtype dt, size_t rows) {
+// (the tensor-core operand layout), whole rows for INT8 (the kernel converts
+// those to the operand layout itself; rows of 64 bytes with the 64-byte swizzle).
+bool encode_cache_map(CUtensorMap* map, void* base, ftd_dtype dt, size_t rows, int D = 128) {
     EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
     const bool i8 = dt == FTD_I8;
-    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(i8 ? 128 : 128 * 2)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(i8 ? 128 : 64), 128};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(i8 ? D : D * 2)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(i8 ? D : 64), 128};
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType ty = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                       : (dt == FTD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
     return fn(map, ty, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              i8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -137,7 +137,12 @@ namespace ftd {
 // Internal to the library (hidden), shared by ftd_init and the no-allocation
 // entry point; tki.fn is null when the CUDA-core kernel runs.
 // Smallest blocks of query rows for which the scored step and cross attention take the tensor cores.
-constexpr int kMinTcBlock = 3, kMinTcBlockI8 = 4;
+// Measured on cross attention to 16 ragged memories (32 kv heads, 33 to 2047 rows), CUDA cores
+// against tensor cores, us: 16-bit D 128, 2 / 3 / 4 rows 56 / 115 / 83 against 55 / 56 / 57; D 64 36 / 66 /
+// 55 against 48 / 49 / 50; INT8 D 128, 3 / 4 / 7 rows 64 / 85 / 134 against 78 / 80 / 78; D 64, 4 / 8
+// rows 58 / 121 against 75 / 75 (an odd count of rows runs one row a block on the CUDA cores).
+constexpr int kMinTcBlock = 3;
+constexpr int min_tc_block_i8(int D) { return D == 64 ? 5 : 4; }
 __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, int mode) {
     TcChoice r{};
     r.nhb = 1;
@@ -145,20 +150,21 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
     const int rows_q = (c.q_len > 1 ? c.q_len : 1) * (c.n_q_heads / c.n_kv_heads);
     const bool forced = c.kernel == FTD_KERNEL_CUDA_CORE;
     const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
-    if (mode != kStep && c.head_dim == 128 && !forced && encode_tiled() && (half || c.cache_dtype == FTD_I8) &&
-        !(half && rows_q % 32 == 0)) {
+    const int D = c.head_dim;
+    if (mode != kStep && (D == 128 || D == 64) && !forced && encode_tiled() && (half || c.cache_dtype == FTD_I8) &&
+        !(half && D == 128 && rows_q % 32 == 0)) {
         // The scored step and cross attention: blocks of any size up to 16 rows (INT8: 8), the
         // columns past them zero; the largest block that divides the rows, the CUDA cores when
         // that is too small to pay for the tensor cores.
         int blk = half ? 16 : 8;
         while (rows_q % blk) --blk;
-        if (blk < (half ? kMinTcBlock : kMinTcBlockI8)) return r;
+        if (blk < (half ? kMinTcBlock : min_tc_block_i8(D))) return r;
         const bool bf = c.cache_dtype == FTD_BF16, mt = c.q_len > 1;
         const int Gt = blk > 8 ? 16 : 8;
         r.qblk = blk;
         r.nhb = rows_q / blk;
-        r.tki = mode == kScored ? (half ? select_tc_scored(bf, Gt, mt) : select_tc_i8_scored(mt))
-                                : (half ? select_tc_cross(bf, Gt, mt) : select_tc_i8_cross(mt));
+        r.tki = mode == kScored ? (half ? select_tc_scored(bf, D, Gt, mt) : select_tc_i8_scored(D, mt))
+                                : (half ? select_tc_cross(bf, D, Gt, mt) : select_tc_i8_cross(D, mt));
         return r;
     }
     const bool want_tc = half && c.head_dim == 128 && rows_q % 4 == 0 && !forced;
@@ -168,8 +174,8 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
             // 32 or more query rows per kv head: the wide kernel, all rows of a block of
             // 32 or 64 in one pass per tile
             r.qblk = rows_q % 64 == 0 ? 64 : 32;
-            r.tki = mode == kScored  ? select_tc_scored(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1)
-                    : mode == kCross ? select_tc_cross(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1)
+            r.tki = mode == kScored  ? select_tc_scored(c.cache_dtype == FTD_BF16, D, r.qblk, c.q_len > 1)
+                    : mode == kCross ? select_tc_cross(c.cache_dtype == FTD_BF16, D, r.qblk, c.q_len > 1)
                                      : select_wide(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1);
         } else {
             const int Gt = (rows_q % 16 == 0 && !want_tc_i8) ? 16 : 8;
@@ -675,12 +681,12 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     if (tki.fn) {
         const size_t rows = ctx->rows;
         if (ctx->tm_k_base != k_cache) {
-            if (!encode_cache_map(&ctx->tmk, k_cache, c.cache_dtype, rows))
+            if (!encode_cache_map(&ctx->tmk, k_cache, c.cache_dtype, rows, c.head_dim))
                 return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for k_cache");
             ctx->tm_k_base = k_cache;
         }
         if (ctx->tm_v_base != v_cache) {
-            if (!encode_cache_map(&ctx->tmv, v_cache, c.cache_dtype, rows))
+            if (!encode_cache_map(&ctx->tmv, v_cache, c.cache_dtype, rows, c.head_dim))
                 return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for v_cache");
             ctx->tm_v_base = v_cache;
         }

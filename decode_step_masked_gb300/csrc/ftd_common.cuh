@@ -373,6 +373,17 @@ __device__ __forceinline__ float ld_qkv(const void* p, int dt, size_t i) {
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
+// A q, k, v or bias element's bits, and their value.
+__device__ __forceinline__ uint32_t ld_raw(const void* p, int dt, size_t i) {
+    if (dt == kF32) return static_cast<const uint32_t*>(p)[i];
+    return static_cast<const unsigned short*>(p)[i];
+}
+__device__ __forceinline__ float raw_to_f(uint32_t u, int dt) {
+    if (dt == kF32) return __uint_as_float(u);
+    if (dt == kF16) return __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+    return __uint_as_float(u << 16);
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));

@@ -63,6 +63,9 @@ constexpr int kAlpha = 1;
 // Of the scored step and of cross attention: ragged memories of four beams (B16 H32 D128, 33 to
 // 2047 rows) took 93 / 70 / 60 / 57 / 60 us at 1 / 2 / 3 / 4 / 6, a 70B-shaped memory 85 at each.
 constexpr int kModeAlpha = 4;
+// INT8 (its tiles take longer): 16 ragged memories of 8 rows per kv head 85 / 71 / 75 us at 1 / 2 / 4,
+// 70B-shaped ones 23 / 24 / 26.
+constexpr int kModeAlphaI8 = 2;
 
 // Margin (log2 units) by which a score may pass a column's running reference
 // before the softmax moves the reference: weights then stay below 2^8, well
@@ -439,7 +442,9 @@ static __device__ __noinline__ void tc_drain_copies(uint32_t full0, int stages, 
 
 // MQ: several new tokens per slot (q_len > 1), so the columns of S carry
 // their own causal limits; without it every column shares one row range.
-template <typename CT, int G, bool MQ, int MODE = kStep>
+// DH: the head dimension.  64 (the scored step and cross attention) fills one 64-column box of K and
+// the first of V's two; the second V box is zero, so lanes 64-127 of O are, and the MMAs stay M = 128.
+template <typename CT, int G, bool MQ, int MODE = kStep, int DH = tc::D>
 __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>), 1)
     decode_gqa_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                          const DecodeParams p) {
@@ -448,7 +453,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     constexpr bool I8 = std::is_same_v<CT, int8_t>;
     using MT = std::conditional_t<I8, __half, CT>;  // operand type of the MMAs
     using LY = tc::Layout<G, I8>;
-    constexpr int N = LY::N, TM = tc::TM, D = tc::D, NS = tc::NS, KB = tc::KB, NB = LY::NB;
+    constexpr int N = LY::N, TM = tc::TM, D = DH, NS = tc::NS, KB = tc::KB, NB = LY::NB;
+    constexpr int BOXES = D / 64;  // 64-column boxes of a K or V tile that hold data
     constexpr int EBC = I8 ? 1 : 2;  // bytes per cache element
     constexpr int SH = tc::softmax_groups(G);  // softmax warp groups, splitting the query columns
     constexpr int GH = G / SH;                  // query columns per softmax thread
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     int* VP = have_vp ? Ls + cap : P;
     // weight of a segment boundary: fixed for the step, else by whether the prefix fits
     constexpr int ALPHA = MODE == kStep ? LY::ALPHA : -1;
-    const int alpha = MODE == kStep ? LY::ALPHA : (have_vp ? tc::kModeAlpha : 0);
+    const int alpha = MODE == kStep ? LY::ALPHA : (have_vp ? (I8 ? tc::kModeAlphaI8 : tc::kModeAlpha) : 0);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
@@ -506,6 +512,12 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     const int spp = kPasses ? p.Hkv : p.Hkv * p.nhb;
     bool ovf = false;
     if (warp == 0) ovf = build_prefix<MODE>(p, TM, spp, alpha, P, VP, Ls, lane);
+    if constexpr (BOXES == 1) {
+        for (int i = tid; i < NB * (KB / 16); i += blockDim.x)
+            *reinterpret_cast<uint4*>(stages + (i / (KB / 16)) * LY::SSTR + LY::VOFF + KB + (i % (KB / 16)) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
     fence_mbar_init();
     tc::tc_fence_before();
     __syncthreads();
@@ -616,11 +628,11 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                                           p.wait_cycles))
                             break;
                         const uint32_t st = smem_addr(stages + s * tc::STAGE);
-                        mbar_arrive_expect_tx(bar(kBarFull + s), tc::STAGE);
+                        mbar_arrive_expect_tx(bar(kBarFull + s), 2 * BOXES * KB);
                         tc::tma_load_2d(st, &tmk, 0, row0, bar(kBarFull + s), l2pol);
-                        tc::tma_load_2d(st + KB, &tmk, 64, row0, bar(kBarFull + s), l2pol);
+                        if constexpr (BOXES > 1) tc::tma_load_2d(st + KB, &tmk, 64, row0, bar(kBarFull + s), l2pol);
                         tc::tma_load_2d(st + 2 * KB, &tmv, 0, row0, bar(kBarFull + s), l2pol);
-                        tc::tma_load_2d(st + 3 * KB, &tmv, 64, row0, bar(kBarFull + s), l2pol);
+                        if constexpr (BOXES > 1) tc::tma_load_2d(st + 3 * KB, &tmv, 64, row0, bar(kBarFull + s), l2pol);
                     }
                     if (k + 1 < n_my) advance_pass(cu, P, p.B, spp, np);
                 }
@@ -633,7 +645,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
             // patch the last tile of a segment together, lane 0 issues the MMAs.
             Cursor cu = locate_pass(t_begin, P, p.B, spp, np);
             const uint32_t id_s = tc::instr_desc(BF, TM, N, false);
-            const uint32_t id_o = tc::instr_desc(BF, D, N, true);
+            const uint32_t id_o = tc::instr_desc(BF, tc::D, N, true);
             int qcount = 0;
             bool ok = true;
             // Operand descriptors of stage 0 and of the first Q / P buffers.  An offset
@@ -677,7 +689,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     // their staged V so stale or non-finite history cannot reach O
                     const int nlo = window_start(Ls[cu.b], p.window) % TM;
                     unsigned char* st = stages + s * tc::STAGE;
-                    for (int c = lane; c < 2 * nlo * 8; c += 32) {
+                    for (int c = lane; c < BOXES * nlo * 8; c += 32) {
                         const int box = c / (nlo * 8), rem = c - box * nlo * 8;
                         *reinterpret_cast<uint4*>(st + 2 * KB + box * KB + (rem >> 3) * 128 + (rem & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
@@ -697,7 +709,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
                     unsigned char* st = stages + s * tc::STAGE;
                     const int nz = (TM - n_total) * 8;
-                    for (int c = lane; c < 2 * nz; c += 32) {
+                    for (int c = lane; c < BOXES * nz; c += 32) {
                         const int box = c / nz, rem = c - box * nz;
                         const int r = n_total + (rem >> 3);
                         *reinterpret_cast<uint4*>(st + 2 * KB + box * KB + r * 128 + (rem & 7) * 16) =
@@ -707,6 +719,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         const int tok = t0 + nr - L, pos = t0 + nr;
                         const bool isv = lane >= 16;  // lanes 0-15: K row, 16-31: V row, 8 elements each
                         const int d0 = (lane & 15) * 8;
+                        if (BOXES == 1 && d0 >= D) continue;
                         const void* src = isv ? p.v_new : p.k_new;
                         const size_t si = ((static_cast<size_t>(cu.b) * p.nq + tok) * p.Hkv + kvh) * D + d0;
                         const size_t bi = static_cast<size_t>(p.Hq + (isv ? p.Hkv : 0) + kvh) * D + d0;
@@ -779,6 +792,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
             constexpr int NCV = tc::converter_threads(I8);
             const int ct = warp < 4 ? tid - 64 : tid - (128 + SMX) + 64;  // 0 .. NCV - 1
             const bool isv = warp == 3;
+            // XOR of row r's 16-byte chunks in a raw stage: the 128-byte swizzle, 64-byte rows the 64-byte one
+            auto raw_swz = [](int r) { return BOXES > 1 ? r & 7 : (r >> 1) & 3; };
             Cursor cu = locate_pass(t_begin, P, p.B, spp, np);
             for (int k = 0; k < n_my; ++k) {
                 const int s8 = k & 1, sb = k % NB;
@@ -802,6 +817,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         float amax = 0.f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
+                            x[e] = 0.f;
+                            if (BOXES == 1 && lane * 4 >= D) continue;
                             x[e] = ld_qkv(src, p.qkv_dtype, si + e);
                             if (p.bias) x[e] += ld_qkv(p.bias, p.qkv_dtype, bi + e);  // one binary32 add
                             amax = fmaxf(amax, fabsf(x[e]));
@@ -815,12 +832,14 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             if (amax != 0.f) code = max(-127, min(127, __float2int_rn(__fdiv_rn(x[e], qs))));
                             w |= (static_cast<uint32_t>(code) & 0xffu) << (8 * e);
                         }
-                        *reinterpret_cast<uint32_t*>(st8 + (isv ? TM * D : 0) + nr * D +
-                                                     ((((lane >> 2) ^ (nr & 7)) << 4) | ((lane & 3) << 2))) = w;
+                        if (BOXES > 1 || lane * 4 < D)
+                            *reinterpret_cast<uint32_t*>(st8 + (isv ? TM * D : 0) + nr * D +
+                                                         (((lane >> 2) ^ raw_swz(nr)) << 4 | ((lane & 3) << 2))) = w;
                         if (lane == 0) ssc[(isv ? TM : 0) + nr] = qs;
                         const long long rowL = cache_row(p, cu.b, kvh, pos, page_of(p, cu.b, pos));
                         if (rowL >= 0 && hb == 0) {  // the first head block writes the cache
-                            *reinterpret_cast<uint32_t*>((isv ? p.v_cache : p.k_cache) + rowL * D + lane * 4) = w;
+                            if (BOXES > 1 || lane * 4 < D)
+                                *reinterpret_cast<uint32_t*>((isv ? p.v_cache : p.k_cache) + rowL * D + lane * 4) = w;
                             if (lane == 0) (isv ? p.v_scales : p.k_scales)[rowL] = qs;
                         }
                     }
@@ -838,7 +857,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     for (int i = ct; i < TM * (D / 16); i += NCV) {
                         const int r = i % TM, j = i / TM;
                         const uint4 u =
-                            *reinterpret_cast<const uint4*>(st8 + v * TM * D + r * D + ((j ^ (r & 7)) << 4));
+                            *reinterpret_cast<const uint4*>(st8 + v * TM * D + r * D + ((j ^ raw_swz(r)) << 4));
                         const uint32_t a0 = u.x ^ 0x80808080u, a1 = u.y ^ 0x80808080u;
                         const uint32_t a2 = u.z ^ 0x80808080u, a3 = u.w ^ 0x80808080u;
                         const uint4 h0 = make_uint4(tc::codes_to_h2(a0, 0x4140), tc::codes_to_h2(a0, 0x4342),
@@ -861,11 +880,11 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     // two per TMEM lane quarter, each widening half of its 32 rows' dimensions
                     tc::tc_fence_after();
                     const int h = (warp - (4 + 4 * SH)) >> 2, rr = (warp & 3) * 32 + lane;
-                    uint32_t wk[32];
+                    uint32_t wk[16 * BOXES];
 #pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) {
-                        const int j = 4 * h + jj;
-                        const uint4 u = *reinterpret_cast<const uint4*>(st8 + rr * D + ((j ^ (rr & 7)) << 4));
+                    for (int jj = 0; jj < 2 * BOXES; ++jj) {
+                        const int j = 2 * BOXES * h + jj;
+                        const uint4 u = *reinterpret_cast<const uint4*>(st8 + rr * D + ((j ^ raw_swz(rr)) << 4));
                         const uint32_t a0 = u.x ^ 0x80808080u, a1 = u.y ^ 0x80808080u;
                         const uint32_t a2 = u.z ^ 0x80808080u, a3 = u.w ^ 0x80808080u;
                         wk[8 * jj + 0] = tc::codes_to_h2(a0, 0x4140);
@@ -877,9 +896,9 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         wk[8 * jj + 6] = tc::codes_to_h2(a3, 0x4140);
                         wk[8 * jj + 7] = tc::codes_to_h2(a3, 0x4342);
                     }
-                    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + LY::KT * (1 + sb) + 32 * h;
+                    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + LY::KT * (1 + sb) + 16 * BOXES * h;
                     tc::tmem_st16(ta, wk);
-                    tc::tmem_st16(ta + 16, wk + 16);
+                    if constexpr (BOXES > 1) tc::tmem_st16(ta + 16, wk + 16);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc::tc_fence_before();
                 }
@@ -941,6 +960,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
             // The scaled query of the owned columns of piece c (dimension r), with the
             // token of each column; columns QB .. G-1 of a padded block get zero.
             float qn[GH];
+            uint32_t qraw[MODE != kStep ? GH : 1], braw[MODE != kStep ? GH : 1];
             int tkn[GH];
             auto load_q = [&](const Cursor& c) {
                 const int kvh = c.seg / p.nhb, hb = c.seg % p.nhb;
@@ -959,6 +979,15 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         h = kvh * p.group + hb * QB + j;
                         qrow = static_cast<size_t>(c.b) * p.Hq + h;
                     }
+                    if constexpr (MODE != kStep) {
+                        // the loads only: converted when staged, a tile's work later
+                        qraw[jj] = braw[jj] = 0u;
+                        if (j < QB && (BOXES > 1 || r < D)) {
+                            qraw[jj] = ld_raw(p.q, p.qkv_dtype, qrow * D + r);
+                            if (p.bias) braw[jj] = ld_raw(p.bias, p.qkv_dtype, static_cast<size_t>(h) * D + r);
+                        }
+                        continue;
+                    }
                     float x = 0.f;
                     if (j < QB) {
                         x = ld_qkv(p.q, p.qkv_dtype, qrow * D + r);
@@ -972,6 +1001,12 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
             auto store_q = [&]() {
 #pragma unroll
                 for (int jj = 0; jj < GH; ++jj) {
+                    if constexpr (MODE != kStep) {
+                        if (BOXES == 1 && r >= D) continue;
+                        qn[jj] = raw_to_f(qraw[jj], p.qkv_dtype);
+                        if (p.bias) qn[jj] += raw_to_f(braw[jj], p.qkv_dtype);
+                        qn[jj] *= p.qscale;
+                    }
                     const MT hi = tc::to_ct<MT>(qn[jj]);
                     const MT lo = tc::to_ct<MT>(qn[jj] - tc::from_ct<MT>(hi));
                     *reinterpret_cast<MT*>(Qs + tc::sw128_offset(c0 + jj, r, N)) = hi;
@@ -1149,7 +1184,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     if (piece_first == 0 && last) {
 #pragma unroll
                         for (int jj = 0; jj < GH; ++jj)
-                            if (c0 + jj < QB) {
+                            if (c0 + jj < QB && (BOXES > 1 || r < D)) {
                                 store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r, o[jj] / lt[jj]);
                                 if constexpr (MODE == kScored)
                                     if (r == 0)
@@ -1165,7 +1200,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             }
                         }
 #pragma unroll
-                        for (int jj = 0; jj < GH; ++jj) slot[LY::OOFF + (c0 + jj) * D + r] = o[jj];
+                        for (int jj = 0; jj < GH; ++jj)
+                            slot[LY::OOFF + (c0 + jj) * tc::D + r] = o[jj];
                         // the barrier orders the softmax threads' partial stores before the leader's release
                         tc::named_bar_sync(1, SMX);
                         const uint32_t piece_tiles = static_cast<uint32_t>(cu.tile - piece_first + 1);
@@ -1199,7 +1235,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                         for (int jj = 0; jj < GH; ++jj) {
                                             mw[i][jj] = __ldcg(sl + c0 + jj);
                                             lw[i][jj] = __ldcg(sl + G + c0 + jj);
-                                            ow[i][jj] = __ldcg(sl + LY::OOFF + (c0 + jj) * D + r);
+                                            ow[i][jj] = __ldcg(sl + LY::OOFF + (c0 + jj) * tc::D + r);
                                         }
                                     }
 #pragma unroll
@@ -1229,7 +1265,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                 for (int jj = 0; jj < GH; ++jj) {
                                     mw[jj] = __ldcg(sl + c0 + jj);
                                     lw[jj] = __ldcg(sl + G + c0 + jj);
-                                    ow[jj] = __ldcg(sl + LY::OOFF + (c0 + jj) * D + r);
+                                    ow[jj] = __ldcg(sl + LY::OOFF + (c0 + jj) * tc::D + r);
                                 }
 #pragma unroll
                                 for (int jj = 0; jj < GH; ++jj) {
@@ -1243,7 +1279,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             }
 #pragma unroll
                             for (int jj = 0; jj < GH; ++jj)
-                                if (c0 + jj < QB) {
+                                if (c0 + jj < QB && (BOXES > 1 || r < D)) {
                                     store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r,
                                                Ac[jj] / Ls_[jj]);
                                     if constexpr (MODE == kScored)
@@ -1289,20 +1325,20 @@ struct TcKernelInfo {
     int threads;  // threads per CTA (tc::threads_for)
 };
 
-template <typename CT, int G, bool MQ, int MODE = kStep>
+template <typename CT, int G, bool MQ, int MODE = kStep, int DH = tc::D>
 TcKernelInfo tc_kernel_info() {
     using LY = tc::Layout<G, std::is_same_v<CT, int8_t>>;
-    return TcKernelInfo{reinterpret_cast<const void*>(&decode_gqa_tc_kernel<CT, G, MQ, MODE>),
+    return TcKernelInfo{reinterpret_cast<const void*>(&decode_gqa_tc_kernel<CT, G, MQ, MODE, DH>),
                         MODE == kStep ? LY::SMEM : 232448, LY::SLOT, G,
                         tc::threads_for(G, std::is_same_v<CT, int8_t>)};
 }
 
 TcKernelInfo select_tc(bool bf16, int G, bool multi_token);
 TcKernelInfo select_tc_i8(bool multi_token);
-// the same for kScored and kCross, blocks of 8, 16, 32 and 64 query rows
-TcKernelInfo select_tc_scored(bool bf16, int G, bool multi_token);
-TcKernelInfo select_tc_i8_scored(bool multi_token);
-TcKernelInfo select_tc_cross(bool bf16, int G, bool multi_token);
-TcKernelInfo select_tc_i8_cross(bool multi_token);
+// the same for kScored and kCross: head dimension D, blocks of 8, 16 and, for 128, 32 and 64 query rows
+TcKernelInfo select_tc_scored(bool bf16, int D, int G, bool multi_token);
+TcKernelInfo select_tc_i8_scored(int D, bool multi_token);
+TcKernelInfo select_tc_cross(bool bf16, int D, int G, bool multi_token);
+TcKernelInfo select_tc_i8_cross(int D, bool multi_token);
 
 }  // namespace ftd

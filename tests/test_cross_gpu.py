@@ -69,6 +69,13 @@ SHAPES = {
     "wide64": ("f16", "f16", 64, 1, 128, False),
     "two_wide": ("bf16", "bf16", 128, 1, 128, False),
     # rows that fill no block of 4: padded tensor-core blocks, and 17, which no block divides
+    # head_dim 64 on the tensor cores
+    "gqa8_d64": ("bf16", "bf16", 16, 2, 64, False),
+    "gqa16_d64": ("f16", "f16", 16, 1, 64, False),
+    "gqa32_d64": ("bf16", "bf16", 64, 2, 64, False),
+    "gqa7_d64": ("f16", "f32", 14, 2, 64, False),
+    "gqa8_i8_d64": ("i8", "bf16", 16, 2, 64, False),
+    "gqa6_i8_d64": ("i8", "f16", 12, 2, 64, False),
     "gqa7": ("bf16", "bf16", 14, 2, 128, False),
     "gqa3": ("f16", "f16", 6, 2, 128, False),
     "gqa20": ("bf16", "bf16", 20, 1, 128, False),
@@ -106,7 +113,7 @@ def test_half_output_without_bias(shape, out_dtype):
     assert np.all(np.abs(got - want) <= tol)
 
 
-@pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "gqa8_tc", "gqa8_tc_i8", "wide32"])
+@pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "gqa8_tc", "gqa8_tc_i8", "wide32", "gqa8_d64", "gqa8_i8_d64"])
 def test_long_memory_split_over_blocks(shape):
     """One long memory and a short one: many pieces per segment, joined at the end."""
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]

@@ -42,6 +42,13 @@ SHAPES = {
     "wide64": ("f16", "f16", 64, 1, 128, False),
     "two_wide": ("bf16", "bf16", 128, 1, 128, False),
     # rows that fill no block of 4: padded tensor-core blocks, and 17, which no block divides
+    # head_dim 64 on the tensor cores
+    "gqa8_d64": ("bf16", "bf16", 16, 2, 64, False),
+    "gqa16_d64": ("f16", "f16", 16, 1, 64, False),
+    "gqa32_d64": ("bf16", "bf16", 64, 2, 64, False),
+    "gqa7_d64": ("f16", "f32", 14, 2, 64, False),
+    "gqa8_i8_d64": ("i8", "bf16", 16, 2, 64, False),
+    "gqa6_i8_d64": ("i8", "f16", 12, 2, 64, False),
     "gqa7": ("bf16", "bf16", 14, 2, 128, False),
     "gqa3": ("f16", "f16", 6, 2, 128, False),
     "gqa20": ("bf16", "bf16", 20, 1, 128, False),
@@ -155,7 +162,8 @@ def test_shapes(shape, T):
     check(w, inp, cc=cc, apart=T == 1)
 
 
-@pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "wide32", "wide64"])
+@pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "wide32", "wide64", "gqa8_d64",
+                                   "gqa8_i8_d64"])
 @pytest.mark.parametrize("T,window", [(1, 1), (1, 100), (2, 130), (4, 400)])
 @pytest.mark.parametrize("apart", [False, True])
 def test_windows(shape, T, window, apart):
@@ -164,7 +172,7 @@ def test_windows(shape, T, window, apart):
     check(w, inp, cc=cc, window=window, apart=apart)
 
 
-@pytest.mark.parametrize("shape", ["mha_bf16", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "wide64"])
+@pytest.mark.parametrize("shape", ["mha_bf16", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "wide64", "gqa8_d64", "gqa8_i8_d64"])
 @pytest.mark.parametrize("page", [128, 256])
 def test_pages(shape, page):
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
@@ -172,7 +180,8 @@ def test_pages(shape, page):
     check(w, inp, cc=cc, page=page)
 
 
-@pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "gqa8_tc", "wide32", "gqa8_tc_i8", "mha_i8"])
+@pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "gqa8_tc", "wide32", "gqa8_tc_i8", "mha_i8", "gqa16_d64",
+                                   "gqa8_i8_d64"])
 def test_long_context_split_over_blocks(shape):
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
     w, inp = ref.step_case(cache, qkv, 2, Hq, Hkv, D, 8192, [8190, 40], T=2)
