@@ -668,8 +668,9 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     if (mode == ftd::kScored) {
         p.scores = ctx->scores;
         p.stats = ctx->stats;
-        p.sscale = ctx->qscale;
-        p.qscale = 1.f;
+        // the softmax scale as a power of two, which leaves q's bits as they are, times the rest
+        p.qscale = exp2f(floorf(log2f(ctx->qscale)));
+        p.sscale = ctx->qscale / p.qscale;
     }
     p.stall = 0;
     if (ctx->stall_calls > 0) {
@@ -1064,6 +1065,8 @@ ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* sc
     if (!aligned(seq_lens, 4) || !aligned(next_pos, 4) || !aligned(acc, 4) || !aligned(acc_out, 4) ||
         !aligned(positions, 4) || !aligned(positions_out, 4) || !aligned(new_lens, 4))
         return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: lengths and planes must be 4-byte aligned");
+    if (new_lens != seq_lens && overlaps(new_lens, c.max_batch * sizeof(int32_t), seq_lens, c.max_batch * sizeof(int32_t)))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: new_lens must be seq_lens or apart from it");
     if (budget < 1 || budget > c.max_len)
         return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: budget %d outside 1..%d", budget, c.max_len);
     if (recent < 0 || sinks < 0 || static_cast<long long>(recent) + sinks > budget)
@@ -1222,7 +1225,7 @@ ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* 
         if (!out[o].p) continue;
         for (int i = 0; i < 3; ++i) {
             if (!in[i].p || !overlaps(in[i].p, in[i].bytes, out[o].p, out[o].bytes)) continue;
-            if (!(i == o && in[i].p == out[o].p && in[i].stride == in[i].width))
+            if (!(i == o && in[i].p == out[o].p && (in[i].stride == in[i].width || n == 1)))
                 return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: an output may only be its own dense input, or apart from every input");
         }
         for (int i = 0; i < o; ++i)

@@ -74,10 +74,10 @@ struct DecodeParams {
     void* proj_lo;
     int proj_dt;
     // kScored: the scores of query row qi of (b, kv head) at [((b * Hkv + kvh) * nq * group + qi) * Lmax + position],
-    // in the log2 domain, and the row's (reference m, 1 / sum of 2^(s - m)).  There q is staged
-    // unscaled (qscale 1) and the scores are multiplied by sscale: a 16-bit q, alone or with a
-    // bias, then splits into its hi and lo parts (almost) without rounding, which keeps the fp32
-    // weights as exact as fp32 products.
+    // in the log2 domain, and the row's (reference m, 1 / sum of 2^(s - m)).  There qscale is the
+    // power of two below the softmax scale and the scores are multiplied by the rest, sscale: a
+    // 16-bit q, alone or with a bias, then splits into its hi and lo parts (almost) without rounding,
+    // which keeps the fp32 weights as exact as fp32 products.
     float* scores;
     float2* stats;
     float sscale;

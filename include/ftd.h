@@ -403,6 +403,8 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream);
  *               become next_pos[b] + j (every kv head's).  Older entries are kept.
  *   next_pos  : device int32 [B], the sequence position of the slot's first new token
  *               (L_b as long as nothing was evicted); needed with positions.
+ * Pages that two active slots share would take both slots' weights in no order: a
+ * page belongs to one slot here.
  * Other arguments, out and the sticky errors as in ftd_decode_mha, and so are the
  * appended rows, but for an INT8 row's scale: absmax * (1 / 127) in fp32 here, at most an
  * ulp from ftd_decode_mha's absmax / 127 (codes are round(k' / scale) in both, so one that
@@ -429,6 +431,7 @@ ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new,
  *   acc_out, positions_out : planes that take the kept rows' entries 0 .. new length - 1;
  *               NULL or the input plane: in place.
  *   new_lens  : device int32 [B], may be seq_lens: budget, or L_b where that is no more.
+ * A page that holds rows of a slot over the budget must be that slot's alone.
  * Inactive slots (L_b < 0) are left alone; L_b > Lmax raises FTD_ERR_SEQ_OVERFLOW, a
  * bad table entry FTD_ERR_BAD_PAGE (that slot's rows stay where they are, its length
  * and planes are undefined).  Needs 1 <= budget <= Lmax and recent + sinks <= budget, a

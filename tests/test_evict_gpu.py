@@ -251,7 +251,8 @@ def test_refusals():
     for kw in (dict(lens=0), dict(next_pos=0), dict(acc=0), dict(pos=0), dict(new=0), dict(lens=258), dict(acc=p + 2),
                dict(pos=p + 1), dict(new=257), dict(next_pos=257), dict(budget=0), dict(budget=-1), dict(budget=257),
                dict(recent=-1), dict(sinks=-1), dict(recent=97), dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), dict(k=264),
-               dict(v=264), dict(table=256), dict(acc_out=p + 4), dict(pos_out=p + 4), dict(acc_out=p + 2)):
+               dict(v=264), dict(table=256), dict(acc_out=p + 4), dict(pos_out=p + 4), dict(acc_out=p + 2),
+               dict(new=260), dict(new=252)):
         assert call(step, **kw) == ftd.FTD_ERR_INVALID_ARG, kw
         assert ftd.ftd_last_error() != ""
     step.close()

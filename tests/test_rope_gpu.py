@@ -168,6 +168,23 @@ def test_in_place_and_without_values():
     step.close()
 
 
+def test_one_token_in_place_in_a_fused_row():
+    import torch
+    rng = np.random.default_rng(8)
+    step = make(4, 2, 64, "f32")
+    step.set_rope()
+    row, x = typed(rng.standard_normal((1, 8 * 64)), "f32")
+    q, k = row[:, :256], row[:, 256:384]
+    pos = dev(np.array([[77]], np.int32))
+    want = [torch.empty_like(q), torch.empty_like(k)]
+    step.rope(q, k, None, pos, *want)
+    step.rope(q, k, None, pos, q, k)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert np.array_equal(row[:, 384:].double().cpu().numpy(), x[:, 384:])
+    step.close()
+
+
 def test_batched_token_axes():
     """[B, T, heads, D] and slices of a fused [B, T, W] projection."""
     import torch

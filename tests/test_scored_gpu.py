@@ -8,7 +8,7 @@ import pytest
 import decode_step_masked_gb300 as ftd
 import oracle
 from tests import operators_ref as ref
-from tests.gpu_util import (assert_close, assert_same_bytes, dev, from_pages, host, make_step, page_layout, rising_scores,
+from tests.gpu_util import (assert_close, assert_same_bytes, dev, from_pages, host, make_step, page_layout, rising_scores, scale_q,
                             to_pages, valid_rows)
 
 pytestmark = pytest.mark.gpu
@@ -202,6 +202,21 @@ def test_weights_without_bias(shape):
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
     w, inp = ref.step_case(cache, qkv, 3, Hq, Hkv, D, 512, [500, 200, 7])
     run(w, inp, bias=False)
+
+
+@pytest.mark.parametrize("cache,qkv", [("f16", "f32"), ("i8", "bf16")])
+def test_large_queries(cache, qkv):
+    """Queries past fp16's range whose scaled values are within it, as the plain step takes them."""
+    w, inp = ref.step_case(cache, qkv, 2, 16, 2, 128, 256, [200, 5], bias=None)
+    inp = scale_q(w, inp, 30000.0)
+    inp["k_cache"] = (inp["k_cache"].astype(np.float32) * 1e-4).astype(np.float16) if cache == "f16" else inp["k_cache"]
+    if cache == "i8":
+        inp["scales"][0] *= np.float32(1e-4)
+    inp["k_new"] = ref.store(ref.widen(inp["k_new"], qkv) * 1e-4, qkv)
+    assert np.abs(ref.widen(inp["q"], qkv)).max() > 65504
+    out, *_ = run(w, inp, bias=False)
+    r = oracle.load().decode_step(w, inp, nthreads=8)
+    assert_close(out.double().cpu().numpy().reshape(r["out"].shape), r["out"], i8=cache == "i8")
 
 
 def test_weights_sum_to_the_rows():
