@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     // Test hook (DecodeParams::stall): worker 0 never issues its first tile, so its
     // bounded wait runs out and the abort path runs.
     const bool stall_me = p.stall && wid == 0;
-    auto issue = [&](int s, const Cursor& cu) {
+    auto issue = [&](int s, const Cursor& cu, bool refill) {
         const int L = Ls[cu.b];
         const int t0 = (window_start(L, p.window) / T + cu.tile) * T;
         const int n_cache = min(T, max(0, cached_rows<MODE>(L) - t0));  // rows before the new tokens come from the cache
@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         const uint32_t sb = (I8 && rb >= 0) ? static_cast<uint32_t>((n_cache * 4 + 15) & ~15) : 0u;
         unsigned char* st = wbase + s * STAGE;
         const uint32_t bar = smem_addr(&bars[s]);
-        fence_proxy_async_smem();
+        // (the first fill of a stage follows no access to it that the copy could overtake)
+        if (MODE == kStep || refill) fence_proxy_async_smem();
         mbar_arrive_expect_tx(bar, 2 * kb + 2 * sb);
         if (kb) {
             bulk_g2s_hint(smem_addr(st), p.k_cache + rowbase * ROW, kb, bar, l2pol);
@@ -562,9 +563,26 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     Cursor ci = locate(t_begin, P, p.B, segs);
     Cursor cc = ci;
     if (!I8) prefetch_segment(ci);  // the first segment's new K/V rows are needed at its last tile
+    // kScored, kCross, blocks of one or two rows: the first segment's q as loaded, ahead of the first copies
+    constexpr bool QRAW = MODE != kStep && G <= 2 && !I8;
+    uint32_t q0[QRAW ? G : 1][EPL], b0[QRAW ? G : 1][EPL];
+    if constexpr (QRAW) {
+        const int kvh = ci.seg / p.nhb, hb = ci.seg % p.nhb;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const size_t qi = q_row(p, ci.b, kvh, hb * G + j) * D + c * EPL;
+            const int tok = q_token(p, hb * G + j);
+            const size_t bi = static_cast<size_t>(kvh * p.group + (hb * G + j - tok * p.group)) * D + c * EPL;
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) {
+                q0[j][e] = ld_raw(p.q, p.qkv_dtype, qi + e);
+                b0[j][e] = p.bias ? ld_raw(p.bias, p.qkv_dtype, bi + e) : 0u;
+            }
+        }
+    }
     const int npre = min(SPW, n_my);
     for (int k = 0; k < npre; ++k) {
-        if (lane == 0 && !(stall_me && k == 0)) issue(k, ci);
+        if (lane == 0 && !(stall_me && k == 0)) issue(k, ci, false);
         if (k + 1 < n_my) {
             advance(ci, P, segs);
             if (!I8 && ci.tile == 0) prefetch_segment(ci);
@@ -580,7 +598,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
     // (kScored adds a third level, s1 / 254^2: the weights are kept in fp32.)
     uint32_t qh[G][I8 ? EPL / 4 : 1], ql[G][I8 ? EPL / 4 : 1], qx[G][I8 && MODE == kScored ? EPL / 4 : 1];
     float qsc[G];
-    auto begin_segment = [&](const Cursor& cu) {
+    auto begin_segment = [&](const Cursor& cu, bool first = false) {
         const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
@@ -591,8 +609,14 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
 #pragma unroll
             for (int e = 0; e < EPL; ++e) {
                 const int d = c * EPL + e;
-                float x = ld_qkv(p.q, p.qkv_dtype, qrow * D + d);
-                if (p.bias) x += ld_qkv(p.bias, p.qkv_dtype, static_cast<size_t>(h) * D + d);
+                float x;
+                if (QRAW && first) {
+                    x = raw_to_f(q0[QRAW ? j : 0][e], p.qkv_dtype);
+                    if (p.bias) x += raw_to_f(b0[QRAW ? j : 0][e], p.qkv_dtype);
+                } else {
+                    x = ld_qkv(p.q, p.qkv_dtype, qrow * D + d);
+                    if (p.bias) x += ld_qkv(p.bias, p.qkv_dtype, static_cast<size_t>(h) * D + d);
+                }
                 qr[j][e] = x * p.qscale;
                 o[j][e] = 0.f;
             }
@@ -631,7 +655,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
             }
         }
     };
-    begin_segment(cc);
+    begin_segment(cc, true);
     int piece_first = cc.tile;
 
     // Log-sum-exp merge of all partials of segment mc, by the worker whose
@@ -655,7 +679,68 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         // pieces in batches of NB: the loads of a batch are issued together, so a merge
         // costs one L2 round trip per batch rather than one per piece
         constexpr int NB = G >= 8 ? 1 : 8 / G;
-        if constexpr (NB == 1) {  // eight query rows: one piece at a time keeps registers in budget
+        if constexpr (MODE != kStep && !I8) {  // (INT8's twelve warps have no registers for this)
+            // Lane i weighs piece i of up to 32: one round trip for all their maxima and sums (every worker
+            // from wf to wl holds a piece), then the outputs, whose loads wait for nothing.
+            for (int w0 = wf; w0 <= wl; w0 += 32) {
+                const int n = min(32, wl - w0 + 1);
+                const float* ml = p.ws + static_cast<size_t>(segg + w0 + min(lane, n - 1)) * TL::SLOT;
+                float f[G], lw[G];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    f[j] = __ldcg(ml + j);
+                    lw[j] = __ldcg(ml + G + j);
+                }
+                auto load_o = [&](int i, float (&ow)[G][DL]) {
+                    const float* ov = p.ws + static_cast<size_t>(segg + w0 + i) * TL::SLOT + TL::OOFF + lane * DL;
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        if constexpr (DL == 4) {
+                            const float4 u = __ldcg(reinterpret_cast<const float4*>(ov + j * D));
+                            ow[j][0] = u.x; ow[j][1] = u.y; ow[j][2] = u.z; ow[j][3] = u.w;
+                        } else {
+                            const float2 u = __ldcg(reinterpret_cast<const float2*>(ov + j * D));
+                            ow[j][0] = u.x; ow[j][1] = u.y;
+                        }
+                    }
+                };
+                float ow[NB][G][DL];
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    if (i < n) load_o(i, ow[i]);
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    // a piece that saw nothing has m = -inf and weighs nothing
+                    const float mw = lane < n ? f[j] : -INFINITY;
+                    const float mn = fmaxf(Mx[j], warp_max(mw));
+                    const float mref = mn == -INFINITY ? 0.f : mn;
+                    const float a = exp2f(Mx[j] - mref);
+                    f[j] = exp2f(mw - mref);
+                    float sum = lw[j] * f[j];
+#pragma unroll
+                    for (int mm = 16; mm >= 1; mm >>= 1) sum += __shfl_xor_sync(FULL, sum, mm);
+                    Ls_[j] = Ls_[j] * a + sum;
+#pragma unroll
+                    for (int e = 0; e < DL; ++e) Ac[j][e] *= a;
+                    Mx[j] = mn;
+                }
+                for (int i0 = 0; i0 < n; i0 += NB) {
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        if (i0 + i >= n) break;
+#pragma unroll
+                        for (int j = 0; j < G; ++j) {
+                            const float fj = __shfl_sync(FULL, f[j], i0 + i);
+#pragma unroll
+                            for (int e = 0; e < DL; ++e) Ac[j][e] += ow[i][j][e] * fj;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+                        if (i0 + NB + i < n) load_o(i0 + NB + i, ow[i]);
+                }
+            }
+        } else if constexpr (NB == 1) {  // eight query rows: one piece at a time keeps registers in budget
             for (int w = wf; w <= wl; ++w) {
                 if (!has_piece(w)) continue;
                 const float* sl = p.ws + static_cast<size_t>(segg + w) * TL::SLOT;
@@ -1029,7 +1114,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
 
         // ---- refill this stage with the tile SPW ahead ----
         if (k + SPW < n_my) {
-            if (lane == 0) issue(s, ci);
+            if (lane == 0) issue(s, ci, true);
             if (k + SPW + 1 < n_my) {
                 advance(ci, P, segs);
                 if (!I8 && ci.tile == 0) prefetch_segment(ci);
