@@ -212,6 +212,30 @@ def test_step_and_cross_share_a_context():
     step.close()
 
 
+@pytest.mark.parametrize("shape", ["mha_f16_d64", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "gqa8_d64", "wide32", "wide64"])
+def test_withheld_copy_times_out_and_the_next_call_is_right(shape):
+    """Bounded waits: block 0's first copy is never issued, the call reports it, the next ones are whole."""
+    import torch
+    cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
+    w, inp = case(cache, qkv, 2, Hq, Hkv, D, 512, [500, 130], T=2)
+    step = make_step(w, q_len=2, wait_limit_us=2000)
+    d = {x: dev(inp[x]) for x in ("q", "k_cache", "v_cache", "seq_lens", "q_bias")}
+    sc = dev(inp["scales"]) if inp.get("scales") is not None else None
+    out = torch.empty((2, 2, Hq, D), device="cuda")
+    call = lambda: step.cross(d["q"], d["seq_lens"], out, q_bias=d["q_bias"], k_mem=d["k_cache"],  # noqa: E731
+                              v_mem=d["v_cache"], scales=sc)
+    assert ftd.ftd_debug_stall_next(step.ctx, 1) == ftd.FTD_OK
+    call()
+    torch.cuda.synchronize()
+    assert step.get_error() == ftd.FTD_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        call()
+        torch.cuda.synchronize()
+        assert step.get_error() == ftd.FTD_OK
+        assert_close(out.double().cpu().numpy(), expect(w, inp), i8=cache == "i8", what=shape)
+    step.close()
+
+
 def test_refusals():
     w, _ = case("bf16", "bf16", 2, 8, 8, 128, 256, [1, 1])
     n = ftd.ftd_kernel_launches()

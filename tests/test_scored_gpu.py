@@ -323,6 +323,32 @@ def test_bad_page_is_reported_and_nothing_is_written_through_it():
     step.close()
 
 
+@pytest.mark.parametrize("shape", ["mha_bf16", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "gqa8_d64", "wide32", "wide64"])
+def test_withheld_copy_times_out_and_the_next_call_is_right(shape):
+    import torch
+    cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
+    w, inp = ref.step_case(cache, qkv, 2, Hq, Hkv, D, 512, [500, 130])
+    step = make_step(w, scored=True, wait_limit_us=2000)
+    q, kn, vn, b, sl, kc, vc = (dev(inp[x]) for x in ("q", "k_new", "v_new", "bias", "seq_lens", "k_cache", "v_cache"))
+    sc = dev(inp["scales"]) if inp.get("scales") is not None else None
+    acc, out = torch.zeros((2, Hkv, 512), device="cuda"), torch.empty((2, Hq, D), device="cuda")
+    acc_out = torch.zeros_like(acc)
+    call = lambda: step.scored(q, kn, vn, sl, sl, acc, None, out, acc_out=acc_out, bias=b, k_cache=kc, v_cache=vc, scales=sc)  # noqa: E731
+    assert ftd.ftd_debug_stall_next(step.ctx, 1) == ftd.FTD_OK
+    call()
+    torch.cuda.synchronize()
+    assert step.get_error() == ftd.FTD_ERR_DEVICE_TIMEOUT
+    r = oracle.load().decode_step(w, inp, nthreads=8)
+    for _ in range(2):
+        call()
+        torch.cuda.synchronize()
+        assert step.get_error() == ftd.FTD_OK
+        assert_close(out.double().cpu().numpy(), r["out"], i8=cache == "i8", what=shape)
+        n = Hq // Hkv  # each query row's weights sum to 1
+        assert np.all(np.abs(acc_out.double().sum(-1).cpu().numpy() - n) <= n * 2.0 ** -16)
+    step.close()
+
+
 def test_refusals():
     import torch
     w, _ = ref.step_case("bf16", "bf16", 2, 8, 8, 128, 256, [1, 1])
