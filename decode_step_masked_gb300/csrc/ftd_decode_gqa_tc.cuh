@@ -709,13 +709,74 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     const int kvh = cu.seg / p.nhb, hb = cu.seg % p.nhb;
                     unsigned char* st = stages + s * tc::STAGE;
                     const int nz = (TM - n_total) * 8;
-                    for (int c = lane; c < BOXES * nz; c += 32) {
+                    if constexpr (MODE != kStep) {
+                        // (a box's last rows are one run of memory)
+                        for (int c = lane; c < nz; c += 32)
+#pragma unroll
+                            for (int box = 0; box < BOXES; ++box)
+                                *reinterpret_cast<uint4*>(st + 2 * KB + box * KB + n_total * 128 + c * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    for (int c = lane; MODE == kStep && c < BOXES * nz; c += 32) {
                         const int box = c / nz, rem = c - box * nz;
                         const int r = n_total + (rem >> 3);
                         *reinterpret_cast<uint4*>(st + 2 * KB + box * KB + r * 128 + (rem & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
-                    for (int nr = MODE == kCross ? n_total : max(0, L - t0); nr < n_total; ++nr) {
+                    int nr1 = MODE == kCross ? n_total : max(0, L - t0);  // the first new row
+                    if (MODE == kScored && MQ && p.qkv_dtype != kF32 &&
+                        ((reinterpret_cast<uintptr_t>(p.k_new) | reinterpret_cast<uintptr_t>(p.v_new) |
+                          reinterpret_cast<uintptr_t>(p.bias)) & 15u) == 0) {
+                        // Several new tokens of 16-bit rows at 16-byte boundaries: four rows' loads in flight (one
+                        // by one, eight tokens cost a segment 5 us)
+                        const bool isv = lane >= 16;
+                        const int d0 = (lane & 15) * 8, dt = p.qkv_dtype;
+                        const unsigned short* src = static_cast<const unsigned short*>(isv ? p.v_new : p.k_new);
+                        uint4 b8 = make_uint4(0u, 0u, 0u, 0u);
+                        if (p.bias && d0 < D)
+                            b8 = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(p.bias) +
+                                                                 static_cast<size_t>(p.Hq + (isv ? p.Hkv : 0) + kvh) * D + d0);
+                        for (; nr1 < n_total; nr1 += 4) {
+                            uint4 r8[4];
+                            long long row[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int pos = t0 + nr1 + u;
+                                row[u] = -1;
+                                if (nr1 + u >= n_total || d0 >= D) continue;
+                                r8[u] = *reinterpret_cast<const uint4*>(
+                                    src + ((static_cast<size_t>(cu.b) * p.nq + pos - L) * p.Hkv + kvh) * D + d0);
+                                if (hb == 0) row[u] = cache_row(p, cu.b, kvh, pos, page_of(p, cu.b, pos));
+                            }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int nr = nr1 + u;
+                                if (nr >= n_total || d0 >= D) continue;
+                                const uint32_t rw[4] = {r8[u].x, r8[u].y, r8[u].z, r8[u].w};
+                                const uint32_t bw[4] = {b8.x, b8.y, b8.z, b8.w};
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float x0 = raw_to_f(rw[e] & 0xffffu, dt), x1 = raw_to_f(rw[e] >> 16, dt);
+                                    if (p.bias) {
+                                        x0 += raw_to_f(bw[e] & 0xffffu, dt);
+                                        x1 += raw_to_f(bw[e] >> 16, dt);
+                                    }
+                                    const MT y0 = tc::to_ct<MT>(x0), y1 = tc::to_ct<MT>(x1);
+                                    uint16_t u0, u1;
+                                    memcpy(&u0, &y0, 2);
+                                    memcpy(&u1, &y1, 2);
+                                    w[e] = static_cast<uint32_t>(u0) | (static_cast<uint32_t>(u1) << 16);
+                                }
+                                const uint4 wv = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4*>(st + (isv ? 2 * KB : 0) + (d0 >> 6) * KB + nr * 128 +
+                                                          ((((d0 & 63) >> 3) ^ (nr & 7)) << 4)) = wv;
+                                if (row[u] >= 0)
+                                    *reinterpret_cast<uint4*>((isv ? p.v_cache : p.k_cache) + (row[u] * D + d0) * 2) = wv;
+                            }
+                        }
+                    }
+                    for (int nr = nr1; nr < n_total; ++nr) {
                         const int tok = t0 + nr - L, pos = t0 + nr;
                         const bool isv = lane >= 16;  // lanes 0-15: K row, 16-31: V row, 8 elements each
                         const int d0 = (lane & 15) * 8;
@@ -962,8 +1023,39 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
             float qn[GH];
             uint32_t qraw[MODE != kStep ? GH : 1], braw[MODE != kStep ? GH : 1];
             int tkn[GH];
+            // kScored, kCross: the owned query rows one after the other, with one division
+            auto for_cols = [&](int hb, auto&& f) {
+                int tok = 0, g = hb * QB + c0;
+                if constexpr (MQ) {
+                    tok = g / p.group;
+                    g -= tok * p.group;
+                }
+#pragma unroll
+                for (int jj = 0; jj < GH; ++jj) {
+                    f(jj, tok, g);
+                    if (MQ && ++g == p.group) {
+                        g = 0;
+                        ++tok;
+                    } else if (!MQ) {
+                        ++g;
+                    }
+                }
+            };
             auto load_q = [&](const Cursor& c) {
                 const int kvh = c.seg / p.nhb, hb = c.seg % p.nhb;
+                if constexpr (MODE != kStep) {
+                    // the loads only: converted when staged, a tile's work later
+                    for_cols(hb, [&](int jj, int tok, int g) {
+                        tkn[jj] = tok;
+                        qraw[jj] = braw[jj] = 0u;
+                        if (c0 + jj < QB && (BOXES > 1 || r < D)) {
+                            const int h = kvh * p.group + g;
+                            qraw[jj] = ld_raw(p.q, p.qkv_dtype, ((static_cast<size_t>(c.b) * p.nq + tok) * p.Hq + h) * D + r);
+                            if (p.bias) braw[jj] = ld_raw(p.bias, p.qkv_dtype, static_cast<size_t>(h) * D + r);
+                        }
+                    });
+                    return;
+                }
 #pragma unroll
                 for (int jj = 0; jj < GH; ++jj) {
                     const int j = c0 + jj;
@@ -978,15 +1070,6 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         tkn[jj] = 0;
                         h = kvh * p.group + hb * QB + j;
                         qrow = static_cast<size_t>(c.b) * p.Hq + h;
-                    }
-                    if constexpr (MODE != kStep) {
-                        // the loads only: converted when staged, a tile's work later
-                        qraw[jj] = braw[jj] = 0u;
-                        if (j < QB && (BOXES > 1 || r < D)) {
-                            qraw[jj] = ld_raw(p.q, p.qkv_dtype, qrow * D + r);
-                            if (p.bias) braw[jj] = ld_raw(p.bias, p.qkv_dtype, static_cast<size_t>(h) * D + r);
-                        }
-                        continue;
                     }
                     float x = 0.f;
                     if (j < QB) {
@@ -1092,8 +1175,10 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 // which is valid (any reference is) as long as they stay below 2^margin.
                 // One barrier then both publishes P and takes the vote; only when some
                 // thread saw a larger score do the columns move to the tile's maximum.
+                // (kScored, kCross: a piece's first tile has no reference yet and goes straight to its maximum)
+                const bool first = MODE != kStep && new_piece;
                 float pq[GH];
-                if (!need) {
+                if (!need && !first) {
 #pragma unroll
                     for (int jj = 0; jj < GH; ++jj) {
                         // a column with no visible row yet keeps m = -inf; 0 stands in as the reference
@@ -1103,7 +1188,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 }
                 fence_proxy_async_smem();
                 tc::tc_fence_before();
-                if (!tc::bar_any(1, SMX, need)) {
+                if (!first && !tc::bar_any(1, SMX, need)) {
 #pragma unroll
                     for (int jj = 0; jj < GH; ++jj) {
                         alpha[jj] = 1.f;
@@ -1182,14 +1267,22 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                     const int ss = kPasses ? kvh : cu.seg, sh_ = kPasses ? hb : 0;
                     const int segg = seg_ordinal(p.B, spp, cu.b, ss, sh_);
                     if (piece_first == 0 && last) {
+                        if constexpr (MODE != kStep) {
+                            for_cols(hb, [&](int jj, int tok, int g) {
+                                if (c0 + jj >= QB) return;
+                                const float inv = 1.f / lt[jj];
+                                if (BOXES > 1 || r < D)
+                                    store_out1(p, ((static_cast<size_t>(cu.b) * p.nq + tok) * p.Hq + kvh * p.group + g) * D + r, o[jj] * inv);
+                                if (MODE == kScored && r == 0)
+                                    p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] = make_float2(m[jj], inv);
+                            });
+                        } else {
 #pragma unroll
                         for (int jj = 0; jj < GH; ++jj)
-                            if (c0 + jj < QB && (BOXES > 1 || r < D)) {
+                            if (c0 + jj < QB) {
                                 store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r, o[jj] / lt[jj]);
-                                if constexpr (MODE == kScored)
-                                    if (r == 0)
-                                        p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] = make_float2(m[jj], 1.f / lt[jj]);
                             }
+                        }
                     } else {
                         float* slot = p.ws + static_cast<size_t>(segg + wid) * LY::SLOT;
                         if (r == 0) {

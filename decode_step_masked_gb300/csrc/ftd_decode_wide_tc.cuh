@@ -376,7 +376,13 @@ static __device__ __noinline__ void append_rows(const DecodeParams& p, unsigned 
     const int n_total = min(TM, L + step_nq<MODE>(p) - t0);
     const int kvh = seg / p.nhb, hb = seg % p.nhb;
     const int nz = (TM - n_total) * 8;
-    for (int c = lane; c < 2 * nz; c += 32) {
+    if constexpr (MODE != kStep) {
+        for (int c = lane; c < nz; c += 32) {  // (a box's last rows are one run of memory)
+            *reinterpret_cast<uint4*>(vst + n_total * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(vst + KB + n_total * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    for (int c = lane; MODE == kStep && c < 2 * nz; c += 32) {
         const int box = c / nz, rem = c - box * nz;
         const int r = n_total + (rem >> 3);
         *reinterpret_cast<uint4*>(vst + box * KB + r * 128 + (rem & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
