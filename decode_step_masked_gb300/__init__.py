@@ -262,6 +262,8 @@ def _row_stride(t, width: int, head_dim: int) -> int:
     """Elements from one token's row of ``width`` elements (heads flattened, or [heads, head_dim]) to the next; 0: dense."""
     if t.is_contiguous():
         return 0
+    if t.dim() == 2 and t.shape[1] == width and t.stride(1) == 1:
+        return t.stride(0)
     split = t.shape[-1] != width
     lead = t.dim() - (2 if split else 1)
     ok = lead >= 1 and t.stride(-1) == 1 and (not split or (t.shape[-1] == head_dim and t.stride(-2) == head_dim

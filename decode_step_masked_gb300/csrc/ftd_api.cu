@@ -1208,10 +1208,12 @@ ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* 
                     static_cast<long long>(kw));
     const int eb = elem_bytes(c.qkv_dtype);
     const void* ptrs[] = {q, k, v, qkv_bias, q_out, k_out, v_out};
-    bool vec = (q_stride * eb) % 16 == 0 && (kv_stride * eb) % 16 == 0 && (ctx->rope.R / 2) % (16 / eb) == 0;
+    // the widest access that every row, pointer and pair of runs allows
+    int vec = 16 / eb;
+    while (vec > 1 && (q_stride % vec != 0 || kv_stride % vec != 0 || (ctx->rope.R / 2) % vec != 0)) vec >>= 1;
     for (const void* p : ptrs) {
         if (!aligned(p, eb)) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: pointers must be aligned to their element");
-        vec = vec && aligned16(p);
+        while (vec > 1 && !aligned(p, static_cast<uintptr_t>(vec * eb))) vec >>= 1;
     }
     if (!aligned(positions, 4)) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: positions must be 4-byte aligned");
     // An output may be its own input (same rows); any other overlap would be read after it was written.

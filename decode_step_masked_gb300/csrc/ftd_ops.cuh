@@ -48,8 +48,8 @@ struct RopeParams {
     int tile, heads_per_block;
     uint32_t div_h[2];
 };
-// vec: every pointer and stride 16-byte aligned and R / 2 a multiple of the 16-byte width.
-cudaError_t launch_rope(RopeParams p, bool vec, int sms, cudaStream_t stream);
+// vec: elements per access (up to 16 bytes); every pointer and stride aligned to it, R / 2 a multiple of it.
+cudaError_t launch_rope(RopeParams p, int vec, int sms, cudaStream_t stream);
 
 struct WeightsParams {
     const float* scores;  // as DecodeParams::scores / stats

@@ -11,14 +11,14 @@
 // integer multiplication; only the wrapped fraction is rounded to fp32 for sincospi.
 //
 // Bound: each head is read and written once.  A block takes a tile of tokens, forms
-// each token's cosines and sines once in shared memory (one sincospi per thread for
-// four tokens of 64 pairs) and applies them to all its heads, 16 bytes of both
-// members of eight (four in fp32) pairs per thread and item, two items in flight.
-// Small calls spread one token's heads over several blocks instead.
+// each token's cosines and sines once in shared memory and applies them to all its heads, 16 bytes
+// (less where runs of pairs or addresses want it) of both members of eight (four in fp32)
+// pairs per thread and item, two items in flight.  Small calls spread one token's heads over several
+// blocks instead.
 // Measured: 16381 tokens of 64 + 2 x 8 bf16 heads of 128 from a fused projection
-// 115.5 us, 5.8 TB/s (one / two / four items in flight: 117 / 116 / 125 us; blocks that keep
-// one group of heads and walk the tokens, with the bias in registers: 119 us at best);
-// eight tokens of 32 + 32 heads 1.7 us a call in a graph.
+// 111 us, 6.0 TB/s (tiles of 1280 / 2560 / 5120 / 10240 items 123 / 115 / 111 / 121 us; one / two / four
+// items in flight 117 / 116 / 125 us; blocks that keep one group of heads and walk the tokens, with the
+// bias in registers, 119 us at best); eight tokens of 32 + 32 heads 1.7 us a call in a graph.
 #include <cuda_runtime.h>
 
 #include "ftd_internal.cuh"
@@ -28,7 +28,8 @@ namespace ftd {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTile = 4;  // tokens per tile of a large call
+constexpr int kRopeTile = 16;         // most tokens of a tile
+constexpr int kRopeTileItems = 5120;  // most items of a large call's tile
 
 template <typename T>
 __device__ __forceinline__ float to_f(T x) {
@@ -43,25 +44,22 @@ __device__ __forceinline__ T from_f(float x) {
     else return __float2bfloat16_rn(x);
 }
 
-// VEC consecutive elements: one 16-byte access, or one element.
+// VEC consecutive elements, as one access of 2 to 16 bytes.
 template <typename T, int VEC>
 struct Chunk {
-    alignas(VEC == 1 ? sizeof(T) : 16) T e[VEC];
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (VEC == 1) e[0] = *p;
-        else *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
-    }
-    __device__ __forceinline__ void store(T* p) const {
-        if constexpr (VEC == 1) *p = e[0];
-        else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
-    }
+    static constexpr int BYTES = VEC * static_cast<int>(sizeof(T));
+    using W = std::conditional_t<BYTES == 16, uint4,
+                                 std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, T>>>;
+    alignas(BYTES) T e[VEC];
+    __device__ __forceinline__ void load(const T* p) { *reinterpret_cast<W*>(e) = *reinterpret_cast<const W*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<W*>(p) = *reinterpret_cast<const W*>(e); }
 };
 
 // Place of pair p's value in a token's table: the quads of an item's pairs lie a whole
 // row of items apart, so the threads of a quarter-warp read consecutive 16-byte words.
 template <int VEC>
 __device__ __forceinline__ int table_at(int pair, int items) {
-    if constexpr (VEC == 1) return pair;
+    if constexpr (VEC < 4) return pair;
     return (((pair % VEC) >> 2) * items + pair / VEC) * 4 + (pair & 3);
 }
 
@@ -170,9 +168,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 }
                 if (it[u] >= 0) {
                     float c[VEC], s[VEC];
-                    if constexpr (VEC == 1) {
-                        c[0] = cs[buf][tk[u]][it[u]];
-                        s[0] = sn[buf][tk[u]][it[u]];
+                    if constexpr (VEC < 4) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            c[e] = cs[buf][tk[u]][it[u] * VEC + e];
+                            s[e] = sn[buf][tk[u]][it[u] * VEC + e];
+                        }
                     } else {
 #pragma unroll
                         for (int h = 0; h < VEC / 4; ++h) {
@@ -215,27 +216,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 }
 
 template <typename T>
-const void* pick(bool vec) {
-    constexpr int V = 16 / sizeof(T);
-    return vec ? reinterpret_cast<const void*>(&rope_kernel<T, V>) : reinterpret_cast<const void*>(&rope_kernel<T, 1>);
+const void* pick(int vec) {
+    if constexpr (sizeof(T) == 2)
+        if (vec == 8) return reinterpret_cast<const void*>(&rope_kernel<T, 8>);
+    return vec == 4   ? reinterpret_cast<const void*>(&rope_kernel<T, 4>)
+           : vec == 2 ? reinterpret_cast<const void*>(&rope_kernel<T, 2>)
+                      : reinterpret_cast<const void*>(&rope_kernel<T, 1>);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(RopeParams p, bool vec, int sms, cudaStream_t stream) {
+cudaError_t launch_rope(RopeParams p, int vec, int sms, cudaStream_t stream) {
     const void* fn = p.dt == kF32 ? pick<float>(vec) : p.dt == kF16 ? pick<__half>(vec) : pick<__nv_bfloat16>(vec);
-    // Large calls: tiles of four tokens, up to eight blocks an SM; tiles of two, then one, where
-    // four would give an SM fewer than four blocks (1001 fp32 tokens of 120 heads: 25.4 -> 21.4 us).
+    // Large calls: tiles of up to kRopeTileItems items, up to eight blocks an SM; fewer tokens where
+    // that would give an SM fewer than four blocks (1001 fp32 tokens of 120 heads: 25.4 -> 21.4 us).
     // Calls with fewer tiles than SMs: their heads over enough blocks to reach every SM (at least
     // 8 heads each).
-    p.tile = p.n >= 16LL * sms ? kRopeTile : p.n >= 8LL * sms ? 2 : 1;
+    const int per_token = p.heads * (p.D / (2 * vec));
+    p.tile = kRopeTile;
+    while (p.tile > 1 && (p.tile * per_token > kRopeTileItems || p.n < 4LL * p.tile * sms)) p.tile >>= 1;
     const long long tiles = (p.n + p.tile - 1) / p.tile;
     long long split = tiles >= sms ? 1 : sms / tiles;
     p.heads_per_block = static_cast<int>((p.heads + split - 1) / split);
     if (p.heads_per_block < 8) p.heads_per_block = p.heads < 8 ? p.heads : 8;
     if (p.heads_per_block > 4096) p.heads_per_block = 4096;
     const int gy = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
-    // ceil(2^32 / H): hh / H as the high half of a product, exact for hh < tile * H <= 4 * 2^12
+    // ceil(2^32 / H): hh / H as the high half of a product, exact for hh < tile * H <= 16 * 2^12
     for (int last = 0; last < 2; ++last) {
         const uint32_t h = static_cast<uint32_t>(last ? p.heads - (gy - 1) * p.heads_per_block : p.heads_per_block);
         p.div_h[last] = h == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + h - 1) / h);

@@ -370,8 +370,9 @@ ftd_status ftd_set_rope(ftd_ctx* ctx, const ftd_rope_config* cfg);
  *   positions : device int32 [n_axes][n_tokens].
  *   q_out, k_out, v_out : device, dense [n_tokens][Hq][D] and [n_tokens][Hkv][D]; each
  *               may be its own dense input.  Other overlaps are refused.
- * Pointers need the alignment of their elements; with 16-byte aligned pointers and
- * strides, and R / 2 a multiple of 8 (fp32: 4), the kernel moves 16 bytes at a time.
+ * Pointers need the alignment of their elements.  The kernel moves 16 bytes at a time where
+ * pointers and strides are 16-byte aligned and R / 2 is a multiple of 8 (fp32: 4), else the
+ * half, quarter or eighth of that.
  * n_tokens 0 launches nothing.
  */
 ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,

@@ -91,10 +91,10 @@ def check(Hq, Hkv, D, dt, n, axes=1, R=0, pairing="halves", order="sections", fu
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("D,R", [(128, 128), (64, 64), (128, 64), (128, 32), (64, 8), (128, 22), (64, 2)])
+@pytest.mark.parametrize("D,R", [(128, 128), (64, 64), (128, 64), (128, 32), (64, 8), (128, 22), (64, 2), (128, 120), (64, 52)])
 @pytest.mark.parametrize("pairing", ["halves", "adjacent"])
 def test_types_and_rotary_dims(dt, D, R, pairing):
-    """(22 and 2 leave pairs that no 16-byte access covers: element accesses.)"""
+    """(8, 120 and 52 leave runs of 4, 4 and 2 pairs, 22 and 2 single ones: narrower accesses.)"""
     check(6, 2, D, dt, 5, axes=1, R=R, pairing=pairing)
 
 
@@ -119,7 +119,7 @@ def test_far_positions(far):
     check(2, 2, 64, "f32", 64, far=far, theta=1e6, pairing="adjacent")
 
 
-@pytest.mark.parametrize("shift", [0, 1, 4, 8])
+@pytest.mark.parametrize("shift", [0, 1, 2, 4, 8])
 @pytest.mark.parametrize("dt", ["f32", "f16"])
 def test_alignment(dt, shift):
     check(5, 1, 64, dt, 9, shift=shift)
