@@ -354,7 +354,8 @@ class DecodeStep:
         s = _current_stream(self.device) if stream is None else stream
         st = ftd_cache_evict(self.ctx, _ptr(k_cache), _ptr(v_cache), _ptr(scales), _ptr(block_table),
                              seq_lens.data_ptr(), next_pos.data_ptr(), acc.data_ptr(), _ptr(acc_out),
-                             positions.data_ptr(), _ptr(positions_out), new_lens.data_ptr(), budget, recent, sinks, s)
+                             positions.data_ptr(), _ptr(positions_out), new_lens.data_ptr(), int(budget), int(recent),
+                             int(sinks), s)
         if st:
             check(st)
 

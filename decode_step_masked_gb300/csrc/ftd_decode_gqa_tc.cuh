@@ -60,12 +60,10 @@ constexpr int softmax_groups(int G) { return G >= 16 ? 4 : (G >= 8 ? 2 : 1); }
 
 // Weight of a segment boundary in the static split (in 128-row tiles; see WeightedSplit).
 constexpr int kAlpha = 1;
-// Of the scored step and of cross attention: ragged memories of four beams (B16 H32 D128, 33 to
-// 2047 rows) took 93 / 70 / 60 / 57 / 60 us at 1 / 2 / 3 / 4 / 6, a 70B-shaped memory 85 at each.
-constexpr int kModeAlpha = 4;
-// INT8 (its tiles take longer): 16 ragged memories of 8 rows per kv head 85 / 71 / 75 us at 1 / 2 / 4,
-// 70B-shaped ones 23 / 24 / 26.
-constexpr int kModeAlphaI8 = 2;
+// Of the scored step and of cross attention.  Ragged memories of four beams (B16 H32 D128, 33 to 2047
+// rows) 53.4 / 54.7 / 55.9 / 57.2 us at 2 / 3 / 4 / 5, 70B-shaped memories 84.2 / 85.0 / 85.1 / 85.6, INT8
+// memories with 8 rows per kv head (longer tiles) 85 / 71 / 75 us at 1 / 2 / 4.
+constexpr int kModeAlpha = 2;
 
 // Margin (log2 units) by which a score may pass a column's running reference
 // before the softmax moves the reference: weights then stay below 2^8, well
@@ -487,7 +485,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
     int* VP = have_vp ? Ls + cap : P;
     // weight of a segment boundary: fixed for the step, else by whether the prefix fits
     constexpr int ALPHA = MODE == kStep ? LY::ALPHA : -1;
-    const int alpha = MODE == kStep ? LY::ALPHA : (have_vp ? (I8 ? tc::kModeAlphaI8 : tc::kModeAlpha) : 0);
+    const int alpha = MODE == kStep ? LY::ALPHA : (have_vp ? tc::kModeAlpha : 0);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
@@ -1046,7 +1044,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                 if constexpr (MODE != kStep) {
                     // the loads only: converted when staged, a tile's work later
                     for_cols(hb, [&](int jj, int tok, int g) {
-                        tkn[jj] = tok;
+                        tkn[jj] = c0 + jj < QB ? tok : 0;
                         qraw[jj] = braw[jj] = 0u;
                         if (c0 + jj < QB && (BOXES > 1 || r < D)) {
                             const int h = kvh * p.group + g;
@@ -1054,8 +1052,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             if (p.bias) braw[jj] = ld_raw(p.bias, p.qkv_dtype, static_cast<size_t>(h) * D + r);
                         }
                     });
-                    return;
-                }
+                } else {
 #pragma unroll
                 for (int jj = 0; jj < GH; ++jj) {
                     const int j = c0 + jj;
@@ -1078,6 +1075,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         x *= p.qscale;
                     }
                     qn[jj] = x;
+                }
                 }
             };
             // Q operand (hi / lo) into shared memory, published to the MMA issuer

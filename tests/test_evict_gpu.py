@@ -232,6 +232,43 @@ def test_graph_replay_from_other_lengths():
     step.close()
 
 
+@pytest.mark.parametrize("cache", ["bf16", "i8"])
+def test_pool_caches(cache):
+    """The scored step and the eviction on the context's own caches give what they give on the caller's."""
+    import torch
+    from tests.gpu_util import device_view
+    w, inp = ref.step_case(cache, "f16" if cache == "i8" else cache, 2, 8, 2, 128, 128, [100, 77])
+    np_dt = {"bf16": np.int16, "i8": np.int8}[cache]
+    res = []
+    for own in (True, False):
+        step = make_step(w, scored=True)
+        kc, vc = dev(inp["k_cache"]), dev(inp["v_cache"])
+        sc = dev(inp["scales"]) if cache == "i8" else None
+        if own:
+            kp, vp, sp = step.cache_ptrs()
+            pk, pv = (device_view(p, inp["k_cache"].shape, np_dt) for p in (kp, vp))
+            pk.copy_(kc), pv.copy_(vc)
+            if sc is not None:
+                ps = device_view(sp, inp["scales"].shape, np.float32)
+                ps.copy_(sc)
+                sc = ps
+            kc, vc = pk, pv
+        lens = dev(inp["seq_lens"])
+        acc = torch.zeros((2, 2, 128), device="cuda")
+        pos = torch.arange(128, dtype=torch.int32, device="cuda").expand(2, 2, 128).contiguous()
+        out = torch.empty((2, 8, 128), device="cuda")
+        kw = {} if own else dict(k_cache=kc, v_cache=vc, scales=sc)
+        step.scored(dev(inp["q"]), dev(inp["k_new"]), dev(inp["v_new"]), lens, lens, acc, pos, out, bias=dev(inp["bias"]), **kw)
+        lens += 1
+        step.evict(acc, pos, lens, lens, lens, np.int64(50), recent=np.int64(10), **kw)
+        torch.cuda.synchronize()
+        assert step.get_error() == ftd.FTD_OK
+        res.append([t.clone() for t in (out, acc, pos, lens, kc[:, :, :50], vc[:, :, :50])] + ([sc[:, :, :, :50].clone()] if sc is not None else []))
+        step.close()
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 def test_refusals():
     import torch
     w = Workload("evict", B=2, Hq=2, Hkv=2, D=64, Lmax=256, qkv_dtype="f16", cache_dtype="f16")
