@@ -62,8 +62,9 @@ struct WeightsParams {
     int32_t* positions;  // or nullptr
     int B, Hkv, Lmax, nq, group, window;
     int pages_per_seq, page_shift, num_pages;
+    bool discard;  // set by the launcher: the scores' lines are dropped from L2 once read
 };
-cudaError_t launch_weights(const WeightsParams& p, cudaStream_t stream);
+cudaError_t launch_weights(WeightsParams p, cudaStream_t stream);
 
 struct EvictParams {
     unsigned char* k_cache;

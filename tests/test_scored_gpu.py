@@ -188,6 +188,48 @@ def test_long_context_split_over_blocks(shape):
     check(w, inp, cc=cc)
 
 
+@pytest.mark.parametrize("shape,B,Lmax", [("gqa8_tc", 12, 32768), ("mha_bf16", 20, 32800), ("wide32", 8, 20000),
+                                          ("wide64", 4, 20016), ("gqa8_tc_i8", 12, 32768)])
+def test_scores_dropped_from_l2(shape, B, Lmax):
+    """Score workspaces past 16 MB, whose lines are dropped after their reading (and, with 20016 positions a
+    row, are not): two calls in a row, the second on other lengths, with many query rows and with few."""
+    import torch
+    cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
+    rng = np.random.default_rng(B)
+    w = ref.Workload("drop", B=B, Hq=Hq, Hkv=Hkv, D=D, Lmax=Lmax, qkv_dtype=qkv, cache_dtype=cache)
+    assert B * Hq * Lmax * 4 >= 16 << 20
+    step = make_step(w, scored=True)
+    td = {"bf16": torch.bfloat16, "f16": torch.float16, "i8": torch.int8}
+    g = torch.Generator(device="cuda").manual_seed(3)
+    shp = (B, Hkv, Lmax, D)
+    if cache == "i8":
+        k, v = (torch.randint(-127, 128, shp, dtype=torch.int8, device="cuda", generator=g) for _ in range(2))
+        sc = torch.rand((2,) + shp[:3], device="cuda", generator=g) * 0.02
+    else:
+        k, v = (torch.randn(shp, device="cuda", generator=g, dtype=td[cache]) for _ in range(2))
+        sc = None
+    q = torch.randn((B, Hq, D), device="cuda", generator=g, dtype=td[qkv])
+    kn, vn = (torch.randn((B, Hkv, D), device="cuda", generator=g, dtype=td[qkv]) for _ in range(2))
+    out = torch.empty((B, Hq, D), device="cuda")
+    acc, acc_out = torch.zeros(shp[:3], device="cuda"), torch.empty(shp[:3], device="cuda")
+    for _ in range(3):
+        lens = torch.from_numpy(rng.integers(0, Lmax, B).astype(np.int32)).cuda()
+        acc_out.fill_(-1.0)
+        step.scored(q, kn, vn, lens, lens, acc, None, out, acc_out=acc_out, k_cache=k, v_cache=v, scales=sc)
+        torch.cuda.synchronize()
+        for b in {0, B // 2, B - 1}:
+            n = int(lens[b]) + 1
+            kk = k[b, :, :n].double() * (sc[0, b, :, :n, None].double() if sc is not None else 1.0)
+            s = torch.einsum("hgd,hnd->hgn", q[b].double().view(Hkv, Hq // Hkv, D), kk) / np.sqrt(D)
+            want = torch.softmax(s, -1).sum(1)
+            got = acc_out[b, :, :n].double()
+            mass = float((q[b].double().abs().view(Hkv, -1, D).amax(1)[:, None] * kk.abs()).sum(-1).max()) / np.sqrt(D)
+            assert torch.all((got - want).abs() <= want * ref.weight_tolerance(w, mass, False) + 1e-30)
+            assert torch.all(acc_out[b, :, n:] == -1.0)
+    assert step.get_error() == ftd.FTD_OK
+    step.close()
+
+
 @pytest.mark.parametrize("shape", ["mha_bf16", "gqa8_tc", "wide64"])
 def test_rising_scores(shape):
     """The running reference moves all along the context, so early weights come out near zero."""
