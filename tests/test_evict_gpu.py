@@ -232,6 +232,49 @@ def test_graph_replay_from_other_lengths():
     step.close()
 
 
+def test_two_contexts_on_two_streams():
+    """Each context has its own workspace: two decoders interleaved on two streams, not the current one,
+    give what each gives alone."""
+    import torch
+    rng = np.random.default_rng(14)
+    cases = [ref.step_case("bf16", "bf16", 3, 16, 2, 128, 512, [500, 300, 2], seed=s) for s in (1, 2)]
+    pos0 = torch.arange(512, dtype=torch.int32, device="cuda").expand(3, 2, 512).contiguous()
+    acc0 = [torch.from_numpy(rng.random((3, 2, 512)).astype(np.float32)).cuda() for _ in cases]
+    results = []
+    for together in (False, True):
+        state = []
+        for (w, inp), a in zip(cases, acc0):
+            d = {x: dev(inp[x]) for x in ("q", "k_new", "v_new", "bias", "k_cache", "v_cache", "seq_lens")}
+            st = dict(d, step=make_step(w, scored=True), acc=a.clone(), pos=pos0.clone(), s=torch.cuda.Stream(),
+                      out=torch.empty((3, 16, 128), device="cuda"), cross=torch.empty((3, 16, 128), device="cuda"))
+            st["step"].set_rope()
+            state.append(st)
+        torch.cuda.synchronize()
+        for _ in range(6):
+            for st in state:
+                with torch.cuda.stream(st["s"]):
+                    n = st["seq_lens"]
+                    bf = lambda x: st[x].view(torch.bfloat16)  # noqa: E731
+                    q, k = torch.empty_like(bf("q")), torch.empty_like(bf("k_new"))
+                    st["step"].rope(bf("q"), bf("k_new"), None, n.view(1, 3), q, k)
+                    st["step"].scored(q, k, st["v_new"], n, n, st["acc"], st["pos"], st["out"], k_cache=st["k_cache"],
+                                      v_cache=st["v_cache"])
+                    n += 1
+                    st["step"].evict(st["acc"], st["pos"], n, n, n, 280, recent=20, k_cache=st["k_cache"],
+                                     v_cache=st["v_cache"])
+                    st["step"].cross(q, n, st["cross"], k_mem=st["k_cache"], v_mem=st["v_cache"])
+                    if not together:
+                        st["s"].synchronize()
+        torch.cuda.synchronize()
+        for st in state:
+            assert st["step"].get_error() == ftd.FTD_OK
+            st["step"].close()
+        results.append([[st[x].clone() for x in ("out", "cross", "acc", "pos", "seq_lens", "k_cache", "v_cache")] for st in state])
+    for a, b in zip(*results):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("cache", ["bf16", "i8"])
 def test_pool_caches(cache):
     """The scored step and the eviction on the context's own caches give what they give on the caller's."""
