@@ -142,6 +142,7 @@ namespace ftd {
 // 55 against 48 / 49 / 50; INT8 D 128, 3 / 4 / 7 rows 64 / 85 / 134 against 78 / 80 / 78; D 64, 4 / 8
 // rows 58 / 121 against 75 / 75 (an odd count of rows runs one row a block on the CUDA cores).
 constexpr int kMinTcBlock = 3;
+constexpr int kSmCount = 152;  // of a GB300
 constexpr int min_tc_block_i8(int D) { return D == 64 ? 5 : 4; }
 __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, int mode) {
     TcChoice r{};
@@ -151,8 +152,14 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
     const bool forced = c.kernel == FTD_KERNEL_CUDA_CORE;
     const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
     const int D = c.head_dim;
-    if (mode != kStep && (D == 128 || D == 64) && !forced && encode_tiled() && (half || c.cache_dtype == FTD_I8) &&
-        !(half && D == 128 && rows_q % 32 == 0)) {
+    // The wide kernel's 64- and 32-row blocks take multiples of 32 rows, except where its tiles could not
+    // give every SM one: blocks of 16 rows make four times the tiles (one or two slots of 64 rows per kv
+    // head over 2500 and 8192 rows 21.9 -> 15.0 and 29.3 -> 19.7 us; 24 slots of 2000 rows, 384
+    // tiles, would take 29 instead of 24.5).
+    const long long wide_tiles = static_cast<long long>(c.max_batch) * c.n_kv_heads * (rows_q / (rows_q % 64 == 0 ? 64 : 32)) *
+                                 ((c.max_len + 127) / 128);
+    const bool wide = half && D == 128 && rows_q % 32 == 0 && wide_tiles > kSmCount;
+    if (mode != kStep && (D == 128 || D == 64) && !forced && encode_tiled() && (half || c.cache_dtype == FTD_I8) && !wide) {
         // The scored step and cross attention: blocks of any size up to 16 rows (INT8: 8), the
         // columns past them zero; the largest block that divides the rows, the CUDA cores when
         // that is too small to pay for the tensor cores.

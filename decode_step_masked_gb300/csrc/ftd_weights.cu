@@ -11,7 +11,10 @@
 // Why two kernels: a weight needs its row's final maximum and sum, which the split over
 // the cache's length knows only at its end.  Keeping the scores costs 4 bytes written
 // and read per (query row, position), most of it in L2; reading K a second time
-// would cost 2 D bytes per position.  Bound: those scores and 8 bytes of plane.
+// would cost 2 D bytes per position.  Bound: those scores and 8 bytes of plane.  Measured on top
+// of the step's kernel: 4 us for 8 x 32 heads of 2048 rows (launch and latency), 6.4 us for 16 x 8
+// heads of 8192 rows with 8 query rows each (42 MB, 6.5 TB/s from L2), 12 us for 64 x 32 heads of 1280 rows
+// (32 MB in short rows).
 #include <cuda_runtime.h>
 
 #include "ftd_ops.cuh"

@@ -102,6 +102,21 @@ def test_shapes(shape, T):
             assert not got[b].any(), f"slot {b} without a memory"
 
 
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,T", [(64, 1, 1), (32, 1, 1), (64, 2, 1), (64, 1, 3), (16, 1, 2)])
+def test_wide_and_narrow_blocks(cache, Hq, Hkv, T):
+    """Multiples of 32 query rows: in 64- or 32-row blocks where the memories hold more tiles than SMs, else in
+    16-row blocks."""
+    for B, Lmax in ((3, 1024), (20, 1280), (40, 2048)):
+        lens = np.random.default_rng(B).integers(0, Lmax + 1, B)
+        if B == 40:
+            lens = lens // 16
+        w, inp = case(cache, cache, B, Hq, Hkv, 128, Lmax, lens, T=T)
+        got, status = run(w, inp)
+        assert status == ftd.FTD_OK
+        assert_close(got, expect(w, inp), what=f"B {B}")
+
+
 @pytest.mark.parametrize("out_dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("shape", ["mha_bf16", "gqa8_tc", "gqa8_tc_i8", "wide64"])
 def test_half_output_without_bias(shape, out_dtype):
@@ -132,6 +147,17 @@ def test_too_long_memory_is_skipped_and_reported(shape):
     assert status == ftd.FTD_ERR_SEQ_OVERFLOW
     assert not got[1:].any()
     assert_close(got[:1], expect(w, inp)[:1], i8=cache == "i8", what=shape)
+
+
+@pytest.mark.parametrize("shape", ["wide32", "wide64", "two_wide"])
+@pytest.mark.parametrize("T", [1, 2])
+def test_wide_lengths(shape, T):
+    """The edge lengths on the wide kernel (memories long enough for its blocks)."""
+    cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
+    w, inp = case(cache, qkv, len(LENS), Hq, Hkv, D, 2560, LENS, T=T)
+    got, status = run(w, inp)
+    assert status == ftd.FTD_OK
+    assert_close(got, expect(w, inp), what=shape)
 
 
 @pytest.mark.parametrize("shape", ["gqa8_tc", "gqa16_tc", "mha_bf16", "wide32"])
@@ -217,7 +243,8 @@ def test_withheld_copy_times_out_and_the_next_call_is_right(shape):
     """Bounded waits: block 0's first copy is never issued, the call reports it, the next ones are whole."""
     import torch
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
-    w, inp = case(cache, qkv, 2, Hq, Hkv, D, 512, [500, 130], T=2)
+    # (long memories, of which little is used, for the wide kernel's blocks)
+    w, inp = case(cache, qkv, 2, Hq, Hkv, D, 12288 if shape.startswith("wide") else 512, [500, 130], T=2)
     step = make_step(w, q_len=2, wait_limit_us=2000)
     d = {x: dev(inp[x]) for x in ("q", "k_cache", "v_cache", "seq_lens", "q_bias")}
     sc = dev(inp["scales"]) if inp.get("scales") is not None else None

@@ -162,6 +162,17 @@ def test_shapes(shape, T):
     check(w, inp, cc=cc, apart=T == 1)
 
 
+@pytest.mark.parametrize("Hq,Hkv,T", [(64, 1, 1), (32, 1, 1), (64, 2, 1), (32, 1, 3), (128, 1, 1)])
+def test_wide_and_narrow_blocks(Hq, Hkv, T):
+    """Multiples of 32 query rows, with more tiles than SMs (64- or 32-row blocks) and with fewer (16-row ones)."""
+    for B, Lmax in ((3, 512), (40, 1024)):
+        lens = np.random.default_rng(B).integers(0, Lmax - T, B)
+        if B == 40:
+            lens = lens // 4
+        w, inp = ref.step_case("bf16", "bf16", B, Hq, Hkv, 128, Lmax, lens, T=T)
+        check(w, inp)
+
+
 @pytest.mark.parametrize("shape", ["mha_bf16", "mha_f32", "mha_i8", "gqa8_tc", "gqa8_tc_i8", "wide32", "wide64", "gqa8_d64",
                                    "gqa8_i8_d64"])
 @pytest.mark.parametrize("T,window", [(1, 1), (1, 100), (2, 130), (4, 400)])
@@ -186,6 +197,17 @@ def test_long_context_split_over_blocks(shape):
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
     w, inp = ref.step_case(cache, qkv, 2, Hq, Hkv, D, 8192, [8190, 40], T=2)
     check(w, inp, cc=cc)
+
+
+@pytest.mark.parametrize("shape", ["wide32", "wide64", "two_wide"])
+@pytest.mark.parametrize("T,window,page", [(1, 0, 0), (3, 0, 0), (1, 100, 0), (2, 130, 0), (2, 0, 256)])
+def test_wide_options(shape, T, window, page):
+    """Edge lengths, windows and pages on the wide kernel (caches long enough for its blocks)."""
+    cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
+    if Hq * T > 200:
+        T = 1
+    w, inp = ref.step_case(cache, qkv, 6, Hq, Hkv, D, 4096, [0, 99, 127, 128, 1500, -1], T=T)
+    check(w, inp, window=window, page=page, apart=window == 0)
 
 
 @pytest.mark.parametrize("shape,B,Lmax", [("gqa8_tc", 12, 32768), ("mha_bf16", 20, 32800), ("wide32", 8, 20000),
@@ -369,11 +391,12 @@ def test_bad_page_is_reported_and_nothing_is_written_through_it():
 def test_withheld_copy_times_out_and_the_next_call_is_right(shape):
     import torch
     cache, qkv, Hq, Hkv, D, cc = SHAPES[shape]
-    w, inp = ref.step_case(cache, qkv, 2, Hq, Hkv, D, 512, [500, 130])
+    Lmax = 12288 if shape.startswith("wide") else 512  # (long enough for the wide kernel's blocks)
+    w, inp = ref.step_case(cache, qkv, 2, Hq, Hkv, D, Lmax, [500, 130])
     step = make_step(w, scored=True, wait_limit_us=2000)
     q, kn, vn, b, sl, kc, vc = (dev(inp[x]) for x in ("q", "k_new", "v_new", "bias", "seq_lens", "k_cache", "v_cache"))
     sc = dev(inp["scales"]) if inp.get("scales") is not None else None
-    acc, out = torch.zeros((2, Hkv, 512), device="cuda"), torch.empty((2, Hq, D), device="cuda")
+    acc, out = torch.zeros((2, Hkv, Lmax), device="cuda"), torch.empty((2, Hq, D), device="cuda")
     acc_out = torch.zeros_like(acc)
     call = lambda: step.scored(q, kn, vn, sl, sl, acc, None, out, acc_out=acc_out, bias=b, k_cache=kc, v_cache=vc, scales=sc)  # noqa: E731
     assert ftd.ftd_debug_stall_next(step.ctx, 1) == ftd.FTD_OK
