@@ -57,10 +57,11 @@ __device__ __forceinline__ int evict_row(const EvictParams& p, int b, int kvh, i
     return ((page * p.Hkv + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
 }
 
-// Unsigned key in the order of the weights (NaN below every number), all below ~0u.
+// Unsigned key in the order of the weights (NaN below every number), all below ~0u.  The two zeros are
+// equal weights, which go by their rows, so they share a key: -0 + 0 is +0, other sums are w.
 __device__ __forceinline__ uint32_t weight_key(float w) {
     if (w != w) return 0u;
-    const uint32_t u = __float_as_uint(w);
+    const uint32_t u = __float_as_uint(w + 0.f);
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
