@@ -185,7 +185,7 @@ __device__ __forceinline__ void evict_segment(const EvictParams& p, uint32_t* sk
         for (int u = 0; u < U; ++u) {
             const int t = t0 + 32 * u;
             if (row[u] == -2) continue;
-            keys[t - c0] = ((ps[u] >= 0 && ps[u] < p.sinks) || (p.recent > 0 && ps[u] >= fresh)) ? 0xffffffffu : weight_key(a[u]);
+            keys[t - c0] = ps[u] < p.sinks || ps[u] >= fresh ? 0xffffffffu : weight_key(a[u]);
             // planes apart: entries below the budget go over as they are, and the moves then
             // overwrite those of the rows that go
             if (row[u] >= 0 && t < p.budget) {

@@ -419,8 +419,9 @@ ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new,
 /*
  * ftd_cache_evict -- bring every slot with more than `budget` cached rows down to
  * budget, each kv head by its own weights.  Of its L_b = seq_lens[b] rows a head keeps
- *   first those whose position is below `sinks` or at least next_pos[b] - `recent`,
- *   then the largest acc (NaN below all), equal ones by the lower row.
+ *   first those whose position is below `sinks` (negative ones too) or at least
+ *   next_pos[b] - `recent` (later ones too, whatever `recent` is),
+ *   then the largest acc (NaN below all), equal ones (0 and -0 are) by the lower row.
  * Rows are not kept in order: the j-th kept row at index >= budget moves into the
  * j-th row below budget that is not kept, K and V (INT8: and their scales), weight
  * and position; no other row moves, and rows from budget on keep their old content.
