@@ -1,0 +1,81 @@
+"""The planes of ftd_decode_mha_scored: calls back to back in place."""
+import numpy as np
+import pytest
+
+import decode_step_masked_gb300 as ftd
+from tests import operators_ref as ref
+from tests.gpu_util import dev, make_step, to_pages
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    ftd.build_library()
+    ftd.load_library()
+
+
+@pytest.mark.parametrize("cache,Hq,Hkv,T,page", [("bf16", 32, 32, 1, 0), ("f16", 16, 2, 1, 128), ("bf16", 32, 2, 1, 0),
+                                                 ("i8", 8, 8, 1, 256), ("f32", 4, 4, 2, 0)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_back_to_back_in_place(cache, Hq, Hkv, T, page, captured):
+    """Scored step, lengths, eviction, scored step, ... in place and without the host waiting in between give
+    the bytes of the same calls with a wait after each: what a call reads is what the one before it left."""
+    import torch
+    B, D, Lmax, budget, steps = 6, 128, 512, 300, 24
+    qkv = "f16" if cache == "i8" else cache
+    lens0 = [400, 301, 300, 299, 40, 0]
+    w, inp = ref.step_case(cache, qkv, B, Hq, Hkv, D, Lmax, lens0, T=T)
+    opts, table, shape = {}, None, (B, Hkv, Lmax)
+    arrs = {n: inp[n] for n in ("k_cache", "v_cache")}
+    sc0 = inp.get("scales")
+    if page:
+        # (every page of every slot: the lengths grow)
+        per = Lmax // page
+        table = np.random.default_rng(2).permutation(B * per).reshape(B, per).astype(np.int32)
+        opts, shape = dict(page_size=page, num_pages=B * per), (B * per, Hkv, page)
+        arrs = {n: to_pages(w, a, table, B * per, page, np.zeros((), a.dtype)) for n, a in arrs.items()}
+        if sc0 is not None:
+            sc0 = np.stack([to_pages(w, x, table, B * per, page, np.float32(0)) for x in sc0])
+    q, kn, vn, bias = (dev(inp[x]) for x in ("q", "k_new", "v_new", "bias"))
+    tb = dev(table) if page else None
+    g0 = torch.Generator(device="cuda").manual_seed(4)
+    acc0 = torch.rand(shape, device="cuda", generator=g0)
+    results = []
+    for wait in (True, False):
+        step = make_step(w, scored=True, q_len=T, **opts)
+        k, v = dev(arrs["k_cache"]), dev(arrs["v_cache"])
+        sc = dev(sc0) if sc0 is not None else None
+        lens, npos = torch.tensor(lens0, dtype=torch.int32, device="cuda"), torch.tensor(lens0, dtype=torch.int32, device="cuda")
+        acc, pos = acc0.clone(), torch.arange(shape[2], dtype=torch.int32, device="cuda").expand(shape).contiguous()
+        out = torch.empty((steps, B, T, Hq, D), device="cuda")
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        torch.cuda.synchronize()
+
+        def run(pause):
+            for i in range(steps):
+                step.scored(q, kn, vn, lens, npos, acc, pos, out[i], bias=bias, k_cache=k, v_cache=v, scales=sc, block_table=tb)
+                pause()
+                lens.add_(T)
+                npos.add_(T)
+                pause()
+                if i % 3 == 2:
+                    step.evict(acc, pos, lens, npos, lens, budget, recent=20, sinks=2, k_cache=k, v_cache=v, scales=sc,
+                               block_table=tb)
+                    pause()
+        if captured and not wait:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                run(pause)
+            g.replay()
+        else:
+            run(pause)
+        torch.cuda.synchronize()
+        assert step.get_error() == ftd.FTD_OK
+        step.close()
+        results.append([t.clone() for t in (lens, out, acc, pos)] + [t.view(torch.uint8).clone() for t in (k, v)])
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
