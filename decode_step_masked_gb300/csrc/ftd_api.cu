@@ -1175,6 +1175,7 @@ ftd_status ftd_set_rope(ftd_ctx* ctx, const ftd_rope_config* cfg) {
     ftd::RopeParams r{};
     r.R = R;
     r.D = D;
+    r.axes = cfg->n_axes;
     r.adjacent = cfg->pairing == FTD_ROPE_ADJACENT;
     const double theta = cfg->theta > 0.0 ? cfg->theta : 10000.0;
     int axis = 0;
@@ -1240,7 +1241,7 @@ ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* 
         for (int i = 0; i < o; ++i)
             if (out[i].p && overlaps(out[i].p, out[i].bytes, out[o].p, out[o].bytes))
                 return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: outputs overlap");
-        if (overlaps(positions, n * 4, out[o].p, out[o].bytes) ||
+        if (overlaps(positions, n * ctx->rope.axes * 4, out[o].p, out[o].bytes) ||
             (qkv_bias && overlaps(qkv_bias, static_cast<size_t>(qw + 2 * kw) * eb, out[o].p, out[o].bytes)))
             return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: an output overlaps positions or the bias");
     }

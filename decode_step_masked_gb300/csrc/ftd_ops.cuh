@@ -40,7 +40,7 @@ struct RopeParams {
     const int32_t* pos;  // [axes][n]
     long long n, q_stride, kv_stride;
     int Hq, Hkv, heads;  // heads: Hq + Hkv, and Hkv value heads more when they are moved too
-    int D, R, dt;
+    int D, R, dt, axes;
     int adjacent;        // pairs (2i, 2i + 1) instead of (i, i + R / 2)
     uint64_t step[64];   // turns per position of pair i, in units of 2^-64
     unsigned char axis[64];
