@@ -251,11 +251,27 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+_raw_stream = None
+
+
 def _current_stream(device: int) -> int:
     """torch's current stream on a device, as an address (without a Stream object where torch has a way)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(device)
+
+
+def _expect(name, t, n, dtype=None, itemsize=0, dense=True):
+    """Raise where t does not hold n elements of dtype (or of itemsize bytes), one after the other."""
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} elements, {n} are needed")
+    if (dtype is not None and t.dtype is not dtype) or (itemsize and t.element_size() != itemsize):
+        raise ValueError(f"{name} is {t.dtype}, it has to be {dtype or f'the qkv type of {itemsize} bytes'}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous")
 
 
 def _row_stride(t, width: int, head_dim: int) -> int:
@@ -298,6 +314,9 @@ class DecodeStep:
         self.ctx = ctx
         self.device = torch.cuda.current_device()
         self._widths = (n_q_heads * head_dim, n_kv_heads * head_dim, head_dim)
+        self._qkv_bytes = 4 if qkv_dtype == "f32" else 2
+        self._int32 = torch.int32
+        self._axes = 0
         if scored:
             self.enable_scores(s)
 
@@ -386,20 +405,50 @@ class DecodeStep:
                 raise ValueError("inv_freq holds one value per pair")
             cfg.inv_freq = (ctypes.c_double * len(f))(*f)
         check(ftd_set_rope(self.ctx, cfg))
+        self._axes = int(n_axes)
+
+    def _check_rope(self, n, q, k, v, positions, q_out, k_out, v_out, bias):
+        """Raise for what the pointers of a rope call cannot show."""
+        qw, kw, _ = self._widths
+        eb = self._qkv_bytes
+        if (v is None) != (v_out is None):
+            raise ValueError("v and v_out go together")
+        for name, t, width in (("q", q, qw), ("k", k, kw), ("v", v, kw)):
+            if t is not None:
+                _expect(name, t, n * width, itemsize=eb, dense=False)  # (_row_stride looks at the strides)
+        for name, t, width in (("q_out", q_out, qw), ("k_out", k_out, kw), ("v_out", v_out, kw)):
+            if t is not None:
+                _expect(name, t, n * width, itemsize=eb)
+        if bias is not None:
+            _expect("bias", bias, qw + 2 * kw, itemsize=eb)
+        if self._axes:  # (else the library says that set_rope comes first)
+            _expect("positions", positions, n * self._axes, dtype=self._int32)
 
     def rope(self, q, k, v, positions, q_out, k_out, v_out=None, bias=None, stream: Optional[int] = None):
         """Bias and rotary positions for the tokens of q, k (and v, which only takes the bias; None with
         v_out None): rows of heads a fixed stride apart, such as slices of a fused projection.  positions is
         int32 [n_axes, tokens]; the outputs are dense and may be their own dense inputs."""
-        s = _current_stream(self.device) if stream is None else stream
         qw, kw, d = self._widths
+        eb = self._qkv_bytes
         n = q.numel() // qw
+        bq, bk = n * qw * eb, n * kw * eb
+        # every size and type in one expression (a call for few tokens is bound by the host); _check_rope says
+        # which it is
+        if (q.nbytes != bq or k.nbytes != bk or q_out.nbytes != bq or k_out.nbytes != bk
+                or positions.nbytes != 4 * n * self._axes or positions.dtype is not self._int32
+                or not positions.is_contiguous() or not q_out.is_contiguous() or not k_out.is_contiguous()
+                or (v is not None or v_out is not None)
+                and (v is None or v_out is None or v.nbytes != bk or v_out.nbytes != bk or not v_out.is_contiguous())
+                or bias is not None and (bias.nbytes != (qw + 2 * kw) * eb or not bias.is_contiguous())):
+            self._check_rope(n, q, k, v, positions, q_out, k_out, v_out, bias)
+        s = _current_stream(self.device) if stream is None else stream
         qs = 0 if q.is_contiguous() else _row_stride(q, qw, d)
         ks = 0 if k.is_contiguous() else _row_stride(k, kw, d)
         if v is not None and ((0 if v.is_contiguous() else _row_stride(v, kw, d)) or kw) != (ks or kw) and n > 1:
             raise ValueError("k and v must share one row stride")
-        st = ftd_rope_qkv(self.ctx, q.data_ptr(), k.data_ptr(), _ptr(v), qs, ks, _ptr(bias), positions.data_ptr(), n,
-                          q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out), s)
+        st = ftd_rope_qkv(self.ctx, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), qs, ks,
+                          None if bias is None else bias.data_ptr(), positions.data_ptr(), n, q_out.data_ptr(),
+                          k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), s)
         if st:
             check(st)
 

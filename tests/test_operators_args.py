@@ -1,0 +1,61 @@
+"""What DecodeStep's methods for the operators around the step refuse before the library is called: types,
+sizes and strides that its pointers cannot show.  Needs no GPU."""
+import types
+
+import pytest
+import torch
+
+import decode_step_masked_gb300 as ftd
+
+B, HQ, HKV, D, LMAX, T = 3, 4, 2, 64, 32, 2
+
+
+class Called(Exception):
+    pass
+
+
+@pytest.fixture
+def step(monkeypatch):
+    """A DecodeStep without a context, whose library calls raise Called."""
+    def call(*_):
+        raise Called
+    names = ("ftd_rope_qkv", "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha")
+    monkeypatch.setattr(ftd, "load_library", lambda: types.SimpleNamespace(**{n: call for n in names}))
+    monkeypatch.setattr(ftd, "ftd_init", lambda cfg, stream=0: (ftd.FTD_OK, 0))
+    monkeypatch.setattr(ftd, "ftd_set_rope", lambda ctx, cfg: ftd.FTD_OK)
+    monkeypatch.setattr(ftd, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    s = ftd.DecodeStep(B, HQ, HKV, D, LMAX, "f16", "f16", stream=0, q_len=T)
+    s.set_rope(2, [16, 16])
+    return s
+
+
+def rope_args(n=5):
+    z = lambda h: torch.zeros((n, h, D), dtype=torch.float16)  # noqa: E731
+    return dict(q=z(HQ), k=z(HKV), v=z(HKV), positions=torch.zeros((2, n), dtype=torch.int32), q_out=z(HQ), k_out=z(HKV),
+                v_out=z(HKV), bias=torch.zeros((HQ + 2 * HKV) * D, dtype=torch.float16))
+
+
+def test_rope_arguments(step):
+    ok = rope_args()
+    fused = torch.zeros((5, (HQ + 2 * HKV) * D), dtype=torch.float16)
+    good = [{}, dict(v=None, v_out=None), dict(bias=None), dict(bias=torch.zeros((HQ + 2 * HKV, D), dtype=torch.float16)),
+            dict(q=fused[:, :HQ * D], k=fused[:, HQ * D:(HQ + HKV) * D], v=fused[:, (HQ + HKV) * D:]),
+            dict(q_out=ok["q_out"].view(5, HQ * D)), dict(q=ok["q"].view(torch.int16)),  # (bits of the same width)
+            dict(positions=torch.zeros(10, dtype=torch.int32))]
+    for kw in good:
+        with pytest.raises(Called):
+            step.rope(**dict(ok, **kw))
+    with pytest.raises(Called):
+        step.rope(**rope_args(0))
+    p, z = ok["positions"], ok["q"]
+    bad = [dict(positions=p.long()), dict(positions=p.float()), dict(positions=p[:1]), dict(positions=p[:, :4].contiguous()),
+           dict(positions=torch.zeros((5, 2), dtype=torch.int32).t()), dict(k=ok["k"][:4]), dict(v=ok["v"][:4]),
+           dict(q=torch.zeros((5, HQ * D + 1), dtype=torch.float16)), dict(q=z.float()), dict(k=ok["k"].float()),
+           dict(v=ok["v"].float()), dict(q_out=z[:4]), dict(q_out=z.float()), dict(k_out=ok["k"][:4]), dict(v_out=ok["v"][:4]),
+           dict(q_out=fused[:, :HQ * D]), dict(k_out=fused[:, :HKV * D]), dict(v_out=fused[:, :HKV * D]),
+           dict(v=None), dict(v_out=None), dict(bias=ok["bias"][:-1]), dict(bias=ok["bias"].float()),
+           dict(bias=torch.zeros(2 * (HQ + 2 * HKV) * D, dtype=torch.float16)[::2])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            step.rope(**dict(ok, **kw))
