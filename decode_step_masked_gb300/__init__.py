@@ -317,6 +317,10 @@ class DecodeStep:
         self._qkv_bytes = 4 if qkv_dtype == "f32" else 2
         self._int32 = torch.int32
         self._axes = 0
+        self._float32 = torch.float32
+        # cache rows: elements of a plane
+        self._rows = num_pages * n_kv_heads * page_size if page_size else max_batch * n_kv_heads * max_len
+        self._entries = max_batch * -(-max_len // page_size) if page_size else 0  # of a block table
         if scored:
             self.enable_scores(s)
 
@@ -350,6 +354,24 @@ class DecodeStep:
                                    _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(scales), _ptr(out),
                                    s))
 
+    def _check_planes(self, lens=(), ints=(), floats=(), table=None):
+        """Raise where a length, a plane or the block table (None: absent) has another type or size than the kernels take:
+        int32 per slot, int32 and fp32 per cache row."""
+        i32, f32, nb, nr = self._int32, self._float32, 4 * self.cfg.max_batch, 4 * self._rows
+        for t in lens:
+            if t is not None and (t.dtype is not i32 or t.nbytes != nb or not t.is_contiguous()):
+                raise ValueError(f"lengths and next_pos are contiguous int32 of {nb // 4} slots, not {t.dtype} {tuple(t.shape)}")
+        for t in ints:
+            if t is not None and (t.dtype is not i32 or t.nbytes != nr or not t.is_contiguous()):
+                raise ValueError(f"a positions plane is contiguous int32 of {nr // 4} rows, not {t.dtype} {tuple(t.shape)}")
+        for t in floats:
+            if t is not None and (t.dtype is not f32 or t.nbytes != nr or not t.is_contiguous()):
+                raise ValueError(f"a weights plane is contiguous fp32 of {nr // 4} rows, not {t.dtype} {tuple(t.shape)}")
+        if table is not None and self._entries and (table.dtype is not i32 or table.nbytes != 4 * self._entries
+                                                    or not table.is_contiguous()):
+            raise ValueError(f"the block table is contiguous int32 of {self._entries} entries, not {table.dtype} "
+                             f"{tuple(table.shape)}")
+
     def enable_scores(self, stream: Optional[int] = None):
         """Allocate what ``scored`` and ``evict`` need (``scored=True`` does it at construction)."""
         check(ftd_enable_scores(self.ctx, _current_stream(self.device) if stream is None else stream))
@@ -358,6 +380,7 @@ class DecodeStep:
                v_cache=None, scales=None, block_table=None, stream: Optional[int] = None):
         """The step, which also adds every position's attention weight to ``acc`` (into ``acc_out`` when
         given); the new rows of ``positions`` (may be None, with next_pos) become next_pos, next_pos + 1, ..."""
+        self._check_planes((seq_lens, next_pos), (positions,), (acc, acc_out), block_table)
         s = _current_stream(self.device) if stream is None else stream
         st = ftd_decode_mha_scored(self.ctx, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _ptr(bias), _ptr(k_cache),
                                    _ptr(v_cache), _ptr(block_table), seq_lens.data_ptr(), _ptr(scales), _ptr(next_pos),
@@ -370,6 +393,7 @@ class DecodeStep:
               stream: Optional[int] = None):
         """Bring every slot down to ``budget`` rows per kv head by accumulated weight (``new_lens`` may be
         ``seq_lens``; planes change in place unless ``acc_out`` / ``positions_out`` are given)."""
+        self._check_planes((seq_lens, next_pos, new_lens), (positions, positions_out), (acc, acc_out), block_table)
         s = _current_stream(self.device) if stream is None else stream
         st = ftd_cache_evict(self.ctx, _ptr(k_cache), _ptr(v_cache), _ptr(scales), _ptr(block_table),
                              seq_lens.data_ptr(), next_pos.data_ptr(), acc.data_ptr(), _ptr(acc_out),
@@ -381,6 +405,7 @@ class DecodeStep:
     def cross(self, q, mem_lens, out, q_bias=None, k_mem=None, v_mem=None, scales=None,
               stream: Optional[int] = None):
         """Cross attention of the slots' tokens to memories of ``mem_lens`` rows (None: the context's pool)."""
+        self._check_planes((mem_lens,))
         s = _current_stream(self.device) if stream is None else stream
         st = ftd_cross_mha(self.ctx, q.data_ptr(), _ptr(q_bias), _ptr(k_mem), _ptr(v_mem), mem_lens.data_ptr(),
                            _ptr(scales), out.data_ptr(), s)

@@ -59,3 +59,41 @@ def test_rope_arguments(step):
     for kw in bad:
         with pytest.raises(ValueError):
             step.rope(**dict(ok, **kw))
+
+
+def test_scored_evict_and_cross_arguments(step):
+    lens, plane = torch.zeros(B, dtype=torch.int32), torch.zeros((B, HKV, LMAX))
+    pos = plane.int()
+    q, kn, out = torch.zeros((B, T, HQ, D), dtype=torch.float16), torch.zeros((B, T, HKV, D), dtype=torch.float16), torch.zeros((B, T, HQ, D))
+    calls = [(step.scored, dict(q=q, k_new=kn, v_new=kn, seq_lens=lens, next_pos=lens, acc=plane, positions=pos, out=out),
+              [dict(acc_out=plane.clone()), dict(positions=None, next_pos=None)]),
+             (step.evict, dict(acc=plane, positions=pos, seq_lens=lens, next_pos=lens, new_lens=lens, budget=8),
+              [dict(acc_out=plane.clone(), positions_out=pos.clone())]),
+             (step.cross, dict(q=q, mem_lens=lens, out=out), [])]
+    ints = {"seq_lens": lens, "next_pos": lens, "new_lens": lens, "mem_lens": lens, "positions": pos, "positions_out": pos}
+    floats = {"acc": plane, "acc_out": plane}
+    for fn, args, more in calls:
+        for kw in [{}] + more:
+            with pytest.raises(Called):
+                fn(**dict(args, **kw))
+        names = [n for n in list(ints) + list(floats) if n in args or any(n in m for m in more)]
+        for name in names:
+            x = ints.get(name, floats.get(name))
+            bad = [x.long() if name in ints else x.double(), x.float() if name in ints else x.half(), x[:-1],
+                   torch.cat([x, x]), torch.stack([x, x], -1)[..., 0]]
+            for y in bad:
+                with pytest.raises(ValueError):
+                    fn(**dict(args, **{name: y}))
+
+
+def test_paged_planes(step, monkeypatch):
+    """A paged context's planes are [num_pages][Hkv][page_size]."""
+    s = ftd.DecodeStep(B, HQ, HKV, D, 256, "f16", "f16", stream=0, page_size=128, num_pages=7)
+    lens, plane, table = torch.zeros(B, dtype=torch.int32), torch.zeros((7, HKV, 128)), torch.zeros((B, 2), dtype=torch.int32)
+    args = dict(acc=plane, positions=plane.int(), seq_lens=lens, next_pos=lens, new_lens=lens, budget=8, block_table=table)
+    with pytest.raises(Called):
+        s.evict(**args)
+    for kw in (dict(acc=plane[:6]), dict(acc=torch.zeros((B, HKV, 256))), dict(block_table=table.long()), dict(block_table=table[:, :1]),
+               dict(block_table=table[:2])):
+        with pytest.raises(ValueError):
+            s.evict(**dict(args, **kw))
