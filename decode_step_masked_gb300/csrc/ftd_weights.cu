@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarpsW) weights_rows_kernel(const Weight
         for (int u = 0; u < U; ++u) {
             const int i = r + u * kWarpsW;
             hi[u] = -1;
-            if (i < rows) {
+            if (i < rows && t < end) {  // (a row may end inside the block's positions)
                 hi[u] = L + i / p.group;  // the row's token sees positions up to hi
                 ml[u] = __ldcg(p.stats + r0 + i);
                 x[u] = __ldcs(reinterpret_cast<const float4*>(p.scores + (r0 + i) * p.Lmax + t));

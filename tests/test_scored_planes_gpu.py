@@ -1,10 +1,12 @@
-"""The planes of ftd_decode_mha_scored: calls back to back in place."""
+"""The planes of ftd_decode_mha_scored: calls back to back in place, and caches
+whose rows end inside the last block of positions."""
 import numpy as np
 import pytest
 
 import decode_step_masked_gb300 as ftd
 from tests import operators_ref as ref
 from tests.gpu_util import dev, make_step, to_pages
+from tests.test_scored_gpu import check
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +81,14 @@ def test_back_to_back_in_place(cache, Hq, Hkv, T, page, captured):
         results.append([t.clone() for t in (lens, out, acc, pos)] + [t.view(torch.uint8).clone() for t in (k, v)])
     for a, b in zip(*results):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("cache,Hq,Hkv,D", [("bf16", 16, 1, 128), ("f16", 24, 1, 64), ("i8", 32, 2, 128), ("f32", 14, 1, 64),
+                                            ("bf16", 13, 1, 128)])
+@pytest.mark.parametrize("Lmax", [16, 144, 272, 400])
+def test_many_rows_with_a_ragged_end(cache, Hq, Hkv, D, Lmax):
+    """More than twelve query rows per kv head, cache rows that end 16 positions into a block of 128: nothing
+    past a row's end counts, whatever the next row's scores are."""
+    lens = [Lmax - 1, Lmax, 0, Lmax - 5, Lmax - 1]
+    w, inp = ref.step_case(cache, "f16" if cache == "i8" else cache, len(lens), Hq, Hkv, D, Lmax, lens)
+    check(w, inp)
