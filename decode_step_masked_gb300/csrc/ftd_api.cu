@@ -1041,6 +1041,7 @@ ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new,
     w.acc = acc;
     w.acc_out = acc_out;
     w.positions = positions;
+    w.err = ctx->err;
     w.B = c.max_batch;
     w.Hkv = c.n_kv_heads;
     w.Lmax = c.max_len;

@@ -60,6 +60,7 @@ struct WeightsParams {
     const float* acc;
     float* acc_out;
     int32_t* positions;  // or nullptr
+    const uint32_t* err;  // the step's error word: after a timeout the planes stay as they are
     int B, Hkv, Lmax, nq, group, window;
     int pages_per_seq, page_shift, num_pages;
     bool discard;  // set by the launcher: the scores' lines are dropped from L2 once read

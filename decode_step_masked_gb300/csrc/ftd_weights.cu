@@ -50,6 +50,21 @@ __device__ __forceinline__ long long plane_row(const WeightsParams& p, int b, in
     return ((static_cast<long long>(page) * p.Hkv + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
 }
 
+// Whether a page that slot b's rows see, positions [start, end), is bad (every lane of a warp gets the answer):
+// the step's weights are then undefined, and the planes keep the slot's old ones.
+__device__ __forceinline__ bool bad_slot(const WeightsParams& p, int b, int start, int end) {
+    if (!p.block_table) return false;
+    const int32_t* row = p.block_table + static_cast<size_t>(b) * p.pages_per_seq;
+    bool bad = false;
+    for (int i = (start >> p.page_shift) + (static_cast<int>(threadIdx.x) & 31); i < (end + (1 << p.page_shift) - 1) >> p.page_shift; i += 32) {
+        const int page = ld_early(row + i);
+        bad |= page < 0 || page >= p.num_pages;
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+// Whether the step gave up on a copy (read after the wait: the step's kernel sets it).
+__device__ __forceinline__ bool gave_up(const WeightsParams& p) { return *p.err & kErrTimeout; }
+
 // The scores of 128 positions from t0 are read: drop their lines from L2, or they would go to memory
 // on their way out, dirty as they are.  Thread i of n drops every n-th line of the segment's rows.
 __device__ __forceinline__ void drop_scores(const WeightsParams& p, size_t r0, int t0, int end, int i, int n) {
@@ -95,9 +110,11 @@ __global__ void __launch_bounds__(kThreadsW) weights_kernel(const WeightsParams 
         for (int e = 0; e < 4; ++e) sum[i][e] = 0.f;
     }
     const size_t r0 = static_cast<size_t>(seg) * (p.nq * p.group);
+    const bool bad = bad_slot(p, b, start, end);
     grid_dep_wait();
     grid_dep_launch();
-    if (chunk * POS >= end) return;
+    if (chunk * POS >= end || bad) return;
+    const bool keep = gave_up(p);
     float w[Q][4];
     for (int tok = 0; tok < p.nq; ++tok) {
         const int hi = L + tok, lo = p.window > 0 ? hi + 1 - p.window : 0;  // this token sees lo .. hi
@@ -133,6 +150,7 @@ __global__ void __launch_bounds__(kThreadsW) weights_kernel(const WeightsParams 
             for (int e = 0; e < 4; ++e)
                 if (live[i] && t[i] + e >= lo && t[i] + e <= hi) sum[i][e] += w[i][e];
     }
+    if (keep) return;
     if (p.discard) {
         __syncwarp();  // (orders every lane's reads before the drops)
         const int lane = threadIdx.x & 31;
@@ -172,11 +190,13 @@ __global__ void __launch_bounds__(32 * kWarpsW) weights_rows_kernel(const Weight
     const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = ld_early(p.seq_lens + b);
+    const int start = window_start(L, p.window), t0 = chunk * POS, t = t0 + 4 * lane;
+    int end = L < 0 || L > p.Lmax - p.nq ? 0 : L + p.nq;
+    if (bad_slot(p, b, start, end)) end = 0;
     grid_dep_wait();  // (as in weights_kernel)
     grid_dep_launch();
-    if (L < 0 || L > p.Lmax - p.nq) return;
-    const int end = L + p.nq, t0 = chunk * POS, t = t0 + 4 * lane;
-    if (t0 >= end || (t0 + POS <= window_start(L, p.window) && p.acc_out == p.acc)) return;
+    if (t0 >= end || (t0 + POS <= start && p.acc_out == p.acc)) return;
+    const bool keep = gave_up(p);
     const int rows = p.nq * p.group;
     const size_t r0 = static_cast<size_t>(seg) * rows;
     float w[4] = {0.f, 0.f, 0.f, 0.f};
@@ -205,6 +225,7 @@ __global__ void __launch_bounds__(32 * kWarpsW) weights_rows_kernel(const Weight
                 if (t + e >= lo && t + e <= hi[u]) w[e] = fmaf(exp2f(s[e] - ml[u].x), ml[u].y, w[e]);
         }
     }
+    if (keep) return;
     part[warp][lane] = make_float4(w[0], w[1], w[2], w[3]);
     __syncthreads();
     if (p.discard) drop_scores(p, r0, t0, end, static_cast<int>(threadIdx.x), 32 * kWarpsW);

@@ -406,6 +406,10 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream);
  *               (L_b as long as nothing was evicted); needed with positions.
  * Pages that two active slots share would take both slots' weights in no order: a
  * page belongs to one slot here.
+ * A slot with a bad entry among its visible pages (FTD_ERR_BAD_PAGE) keeps its acc_out and
+ * positions entries, and so do all slots of a call that gives up on a copy, and of later ones
+ * until ftd_get_error has reported that FTD_ERR_DEVICE_TIMEOUT: the weights gathered before
+ * are not lost, and the call can be made again.
  * Other arguments, out and the sticky errors as in ftd_decode_mha, and so are the
  * appended rows, but for an INT8 row's scale: absmax * (1 / 127) in fp32 here, at most an
  * ulp from ftd_decode_mha's absmax / 127 (codes are round(k' / scale) in both, so one that

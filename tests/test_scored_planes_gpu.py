@@ -1,11 +1,11 @@
-"""The planes of ftd_decode_mha_scored: calls back to back in place, and caches
+"""The planes of ftd_decode_mha_scored: calls back to back in place, calls that fail part-way, and caches
 whose rows end inside the last block of positions."""
 import numpy as np
 import pytest
 
 import decode_step_masked_gb300 as ftd
 from tests import operators_ref as ref
-from tests.gpu_util import dev, make_step, to_pages
+from tests.gpu_util import dev, make_step, page_layout, to_pages
 from tests.test_scored_gpu import check
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +92,78 @@ def test_many_rows_with_a_ragged_end(cache, Hq, Hkv, D, Lmax):
     lens = [Lmax - 1, Lmax, 0, Lmax - 5, Lmax - 1]
     w, inp = ref.step_case(cache, "f16" if cache == "i8" else cache, len(lens), Hq, Hkv, D, Lmax, lens)
     check(w, inp)
+
+
+SHAPES = {"mha_bf16": ("bf16", "bf16", 8, 8), "gqa8_tc": ("bf16", "bf16", 16, 2), "gqa16_tc": ("f16", "f16", 32, 2),
+          "mha_i8": ("i8", "f16", 4, 4)}
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_a_call_that_gave_up_leaves_the_planes(shape):
+    """A withheld copy: the weights gathered so far and the positions are kept, and the same call made again
+    gives what it gives on a fresh context."""
+    import torch
+    cache, qkv, Hq, Hkv = SHAPES[shape]
+    w, inp = ref.step_case(cache, qkv, 2, Hq, Hkv, 128, 512, [500, 130])
+    rng = np.random.default_rng(6)
+    acc0 = dev(rng.random((2, Hkv, 512)).astype(np.float32))
+    pos0 = dev(rng.integers(0, 999, (2, Hkv, 512)).astype(np.int32))
+    after = []
+    for stall in (0, 1):
+        step = make_step(w, scored=True, wait_limit_us=2000)
+        q, kn, vn, b, sl, kc, vc = (dev(inp[x]) for x in ("q", "k_new", "v_new", "bias", "seq_lens", "k_cache", "v_cache"))
+        sc = dev(inp["scales"]) if inp.get("scales") is not None else None
+        acc, pos, out = acc0.clone(), pos0.clone(), torch.empty((2, Hq, 128), device="cuda")
+        call = lambda: step.scored(q, kn, vn, sl, sl, acc, pos, out, bias=b, k_cache=kc, v_cache=vc, scales=sc)  # noqa: E731
+        if stall:
+            assert ftd.ftd_debug_stall_next(step.ctx, 1) == ftd.FTD_OK
+            call()
+            torch.cuda.synchronize()
+            assert step.get_error() == ftd.FTD_ERR_DEVICE_TIMEOUT
+            assert torch.equal(acc, acc0) and torch.equal(pos, pos0)
+        call()
+        torch.cuda.synchronize()
+        assert step.get_error() == ftd.FTD_OK
+        assert not torch.equal(acc, acc0)
+        after.append((acc.clone(), pos.clone(), out.clone()))
+        step.close()
+    for a, b in zip(*after):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hq,Hkv,T,window", [(8, 8, 1, 0), (16, 2, 1, 0), (32, 1, 1, 0), (16, 2, 2, 0), (8, 8, 1, 100)])
+@pytest.mark.parametrize("apart", [False, True])
+def test_a_bad_page_leaves_its_slot_in_the_planes(Hq, Hkv, T, window, apart):
+    """The slot behind a bad table entry keeps its weights and positions, the others' are those of a sound call;
+    entries behind a window are not looked at."""
+    import torch
+    lens = [300, 200, 250]
+    w, inp = ref.step_case("bf16", "bf16", 3, Hq, Hkv, 128, 512, lens, T=T)
+    table, num_pages, _ = page_layout(w, lens, 128, 2, seed=3, q_len=T)
+    bad = table.copy()
+    bad[0, 1] = num_pages  # positions 128 .. 255: visible in slot 0, with the window too
+    if window:
+        bad[2, 0] = -7  # positions 0 .. 127: slot 2 sees 151 .. 250
+    k0, v0 = (to_pages(w, inp[n], table, num_pages, 128, np.zeros((), inp[n].dtype)) for n in ("k_cache", "v_cache"))
+    rng = np.random.default_rng(8)
+    acc0 = dev(rng.random((num_pages, Hkv, 128)).astype(np.float32))
+    pos0 = dev(rng.integers(0, 999, (num_pages, Hkv, 128)).astype(np.int32))
+    res = []
+    for tb in (table, bad):
+        step = make_step(w, scored=True, page_size=128, num_pages=num_pages, q_len=T, window=window)
+        acc, pos = acc0.clone(), pos0.clone()
+        acc_out = acc0.clone() if apart else None
+        out = torch.empty((3, T, Hq, 128), device="cuda")
+        sl = dev(inp["seq_lens"])
+        step.scored(dev(inp["q"]), dev(inp["k_new"]), dev(inp["v_new"]), sl, sl, acc, pos, out, acc_out=acc_out,
+                    bias=dev(inp["bias"]), k_cache=dev(k0), v_cache=dev(v0), block_table=dev(tb))
+        torch.cuda.synchronize()
+        assert step.get_error() == (ftd.FTD_OK if tb is table else ftd.FTD_ERR_BAD_PAGE)
+        res.append(((acc_out if apart else acc).clone(), pos.clone()))
+        step.close()
+    mine = {b: [int(x) for x in table[b] if 0 <= x < num_pages] for b in range(3)}
+    for i, first in ((0, acc0), (1, pos0)):
+        assert torch.equal(res[1][i][mine[0]], first[mine[0]])
+        assert torch.equal(res[1][i][mine[1]], res[0][i][mine[1]])
+        assert not torch.equal(res[0][i][mine[0]], first[mine[0]])
+        assert torch.equal(res[1][i][mine[2]], res[0][i][mine[2]])
