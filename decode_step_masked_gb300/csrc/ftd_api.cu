@@ -1026,6 +1026,8 @@ ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new,
     const size_t plane = ctx->rows * sizeof(float);
     if (acc_out != acc && overlaps(acc, plane, acc_out, plane))
         return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: acc_out must be acc or a plane apart from it");
+    if (positions && (overlaps(positions, plane, acc, plane) || overlaps(positions, plane, acc_out, plane)))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_decode_mha_scored: positions must be apart from acc and acc_out");
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1094,6 +1096,9 @@ ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* sc
     if ((acc_out != acc && overlaps(acc, plane, acc_out, plane)) ||
         (positions_out != positions && overlaps(positions, plane, positions_out, plane)))
         return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: an output plane must be its input plane or apart from it");
+    if (overlaps(acc, plane, positions, plane) || overlaps(acc_out, plane, positions, plane) ||
+        overlaps(acc, plane, positions_out, plane) || overlaps(acc_out, plane, positions_out, plane))
+        return fail(FTD_ERR_INVALID_ARG, "ftd_cache_evict: planes of weights must be apart from planes of positions");
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
     ftd::EvictParams p{};

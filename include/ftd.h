@@ -401,7 +401,8 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream);
  *   acc_out   : the same, NULL or acc: in place.  Entries past L_b + T - 1, and
  *               slots without work, keep what they hold.
  *   positions : device int32 plane of the same layout, or NULL: the new rows' entries
- *               become next_pos[b] + j (every kv head's).  Older entries are kept.
+ *               become next_pos[b] + j (every kv head's).  Older entries are kept.  Apart
+ *               from acc and acc_out.
  *   next_pos  : device int32 [B], the sequence position of the slot's first new token
  *               (L_b as long as nothing was evicted); needed with positions.
  * Pages that two active slots share would take both slots' weights in no order: a
@@ -435,7 +436,7 @@ ftd_status ftd_decode_mha_scored(ftd_ctx* ctx, const void* q, const void* k_new,
  *               and scales: the pool).
  *   acc, positions : planes as in ftd_decode_mha_scored, 4-byte aligned.
  *   acc_out, positions_out : planes that take the kept rows' entries 0 .. new length - 1;
- *               NULL or the input plane: in place.
+ *               NULL or the input plane: in place.  Other overlaps are refused.
  *   new_lens  : device int32 [B], may be seq_lens: budget, or L_b where that is no more.
  * A page that holds rows of a slot over the budget must be that slot's alone.
  * Inactive slots (L_b < 0) are left alone; L_b > Lmax raises FTD_ERR_SEQ_OVERFLOW, a

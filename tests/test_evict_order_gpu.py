@@ -1,5 +1,5 @@
 """The order in which ftd_cache_evict keeps rows, on the inputs where it can go wrong: zeros of both
-signs, positions before 0 and from next_pos on."""
+signs, positions before 0 and from next_pos on, and planes that may not overlap."""
 import numpy as np
 import pytest
 
@@ -83,3 +83,38 @@ def test_positions_before_zero_and_from_next_pos_on(recent, sinks, lo, hi):
                 want[d] = s
             assert np.array_equal(rows[b, h], want), (b, h)
             assert np.array_equal(a1[b, h], acc[b, h][want]) and np.array_equal(p1[b, h], pos[b, h][want])
+
+
+def test_planes_of_different_kinds_are_apart():
+    """An output plane may be its own input and nothing else's."""
+    import torch
+    w = Workload("evict", B=2, Hq=2, Hkv=2, D=64, Lmax=256, qkv_dtype="f16", cache_dtype="f16")
+    step = make_step(w, scored=True)
+    n = 2 * 2 * 256 * 4
+    buf = torch.zeros(8 * n, dtype=torch.uint8, device="cuda")
+    p = [buf.data_ptr() + i * n for i in range(8)]
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")  # (no slot has work: a call that is not refused moves nothing)
+    q = torch.zeros(4096, dtype=torch.float16, device="cuda")
+    before = ftd.ftd_kernel_launches()
+
+    def evict(acc, acc_out, pos, pos_out):
+        return ftd.ftd_cache_evict(step.ctx, 0, 0, 0, 0, lens.data_ptr(), lens.data_ptr(), acc, acc_out, pos, pos_out,
+                                   lens.data_ptr(), 100, 0, 0, 0)
+    for a, ao, s, so in ((p[0], 0, p[0], 0), (p[0], p[2], p[2], p[3]), (p[0], p[2], p[1], p[0]), (p[0], p[2], p[1], p[2]),
+                         (p[0], 0, p[0] + n - 4, 0), (p[0], p[2], p[1], p[2] + 4), (p[1], p[2], p[0] + 4, 0)):
+        assert evict(a, ao, s, so) == ftd.FTD_ERR_INVALID_ARG and ftd.ftd_last_error()
+    # the scored step writes acc_out and positions
+    skip = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    out = torch.zeros((2, 2, 64), device="cuda")
+
+    def scored(acc, acc_out, pos):
+        return ftd.ftd_decode_mha_scored(step.ctx, q.data_ptr(), q.data_ptr(), q.data_ptr(), 0, 0, 0, 0, skip.data_ptr(), 0,
+                                         lens.data_ptr(), acc, acc_out, pos, out.data_ptr(), 0)
+    for a, ao, s in ((p[0], 0, p[0]), (p[0], p[2], p[2]), (p[0], p[2], p[0]), (p[1], p[2], p[0] + 4), (p[0], p[2], p[2] + n - 4)):
+        assert scored(a, ao, s) == ftd.FTD_ERR_INVALID_ARG and ftd.ftd_last_error()
+    assert ftd.ftd_kernel_launches() == before
+    assert evict(p[0], p[1], p[2], p[3]) == ftd.FTD_OK and evict(p[0], 0, p[1], 0) == ftd.FTD_OK
+    assert scored(p[0], p[1], p[2]) == ftd.FTD_OK and scored(p[0], 0, p[1]) == ftd.FTD_OK and scored(p[0], p[0], 0) == ftd.FTD_OK
+    torch.cuda.synchronize()
+    assert step.get_error() == ftd.FTD_OK
+    step.close()
