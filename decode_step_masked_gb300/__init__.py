@@ -36,7 +36,7 @@ DTYPES = {"f32": FTD_F32, "f16": FTD_F16, "bf16": FTD_BF16, "i8": FTD_I8}
 EXPORTS = ("ftd_init", "ftd_cache_ptrs", "ftd_decode_mha", "ftd_decode_mha_current", "ftd_decode_mha_paged",
            "ftd_decode_mha_host", "ftd_get_error", "ftd_destroy", "ftd_status_str", "ftd_last_error",
            "ftd_kernel_launches", "ftd_decode_mha_noalloc", "ftd_debug_stall_next",
-           "ftd_debug_late_lengths", "ftd_decode_mha_proj", "ftd_set_rope", "ftd_rope_qkv", "ftd_enable_scores",
+           "ftd_debug_late_lengths", "ftd_debug_kernel", "ftd_decode_mha_proj", "ftd_set_rope", "ftd_rope_qkv", "ftd_enable_scores",
            "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha")
 
 
@@ -117,6 +117,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ftd_cache_evict.restype = I
     lib.ftd_cross_mha.argtypes = [P] * 9
     lib.ftd_cross_mha.restype = I
+    lib.ftd_debug_kernel.argtypes = [P, I, ctypes.POINTER(I), ctypes.POINTER(I)]
+    lib.ftd_debug_kernel.restype = I
     lib.ftd_debug_late_lengths.argtypes = [P, P, I, I, P]
     lib.ftd_debug_late_lengths.restype = I
     if path == LIB:
@@ -231,6 +233,13 @@ def ftd_debug_stall_next(ctx, calls: int) -> int:
 def ftd_debug_late_lengths(src, dst, n: int, delay_us: int, stream) -> int:
     """Test hook: a kernel that lets the next launch start at once and copies n lengths src -> dst late."""
     return load_library().ftd_debug_late_lengths(src, dst, int(n), int(delay_us), stream)
+
+
+def ftd_debug_kernel(ctx, entry: int):
+    """Test hook: (status, query rows of a block, on the tensor cores) for entry 0 the step, 1 scored, 2 cross."""
+    rows, tc = ctypes.c_int(), ctypes.c_int()
+    st = load_library().ftd_debug_kernel(ctypes.c_void_p(ctx or None), int(entry), ctypes.byref(rows), ctypes.byref(tc))
+    return st, rows.value, bool(tc.value)
 
 
 def ftd_get_error(ctx) -> int:

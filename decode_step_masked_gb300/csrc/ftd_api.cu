@@ -887,6 +887,16 @@ ftd_status ftd_debug_stall_next(ftd_ctx* ctx, int calls) {
     return FTD_OK;
 }
 
+ftd_status ftd_debug_kernel(ftd_ctx* ctx, int entry, int* block_rows, int* tensor_cores) {
+    g_last_error.clear();
+    if (!ctx || !block_rows || !tensor_cores) return fail(FTD_ERR_INVALID_ARG, "ftd_debug_kernel: ctx, block_rows or tensor_cores is NULL");
+    if (entry < ftd::kStep || entry > ftd::kCross) return fail(FTD_ERR_INVALID_ARG, "ftd_debug_kernel: entry %d outside 0..2", entry);
+    const ftd::TcChoice tcc = ftd::choose_tc(ctx->cfg, entry);
+    *tensor_cores = tcc.tki.fn != nullptr;
+    *block_rows = tcc.tki.fn ? tcc.qblk : ctx->G;
+    return FTD_OK;
+}
+
 void ftd_destroy(ftd_ctx* ctx) {
     if (!ctx) return;
     {

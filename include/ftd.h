@@ -321,6 +321,14 @@ ftd_status ftd_debug_stall_next(ftd_ctx* ctx, int calls);
 ftd_status ftd_debug_late_lengths(const int32_t* src, int32_t* dst, int n, int delay_us, void* stream);
 
 /*
+ * ftd_debug_kernel -- test hook; the pages have no counterpart.  Which kernel an entry point takes on
+ * ctx: entry 0 the step, 1 ftd_decode_mha_scored, 2 ftd_cross_mha.  *block_rows gets the query
+ * rows of a block, *tensor_cores 1 or 0 (the CUDA cores); blocks of 32 and 64 rows on the
+ * tensor cores are the wide kernel's.  Host work only.
+ */
+ftd_status ftd_debug_kernel(ftd_ctx* ctx, int entry, int* block_rows, int* tensor_cores);
+
+/*
  * Operators around the step: rotary positions before it, the step that also
  * accumulates attention weights, the eviction by those weights, and cross
  * attention.  They take the context's shapes, types and caches, follow the
