@@ -138,9 +138,10 @@ namespace ftd {
 // entry point; tki.fn is null when the CUDA-core kernel runs.
 // Smallest blocks of query rows for which the scored step and cross attention take the tensor cores.
 // Measured on cross attention to 16 ragged memories (32 kv heads, 33 to 2047 rows), CUDA cores
-// against tensor cores, us: 16-bit D 128, 2 / 3 / 4 rows 56 / 115 / 83 against 55 / 56 / 57; D 64 36 / 66 /
-// 55 against 48 / 49 / 50; INT8 D 128, 3 / 4 / 7 rows 64 / 85 / 134 against 78 / 80 / 78; D 64, 4 / 8
-// rows 58 / 121 against 75 / 75 (an odd count of rows runs one row a block on the CUDA cores).
+// against tensor cores, us: 16-bit D 128, 1 / 2 / 3 / 4 / 8 rows 47 / 55 / 113 / 83 / 277 against 53 / 53 / 53 /
+// 54 / 53; D 64 28 / 35 / 66 / 54 / 98 against 47 / 47 / 47 / 48 / 48; INT8 D 128, 2 / 3 / 4 / 5 / 8 rows 39 / 62 /
+// 83 / 97 / 246 against 72 / 73 / 74 / 74 / 72; D 64, 3 / 4 / 5 / 8 rows 53 / 56 / 83 / 123 against 61 / 63 / 62 / 63 (an
+// odd count of rows runs one row a block on the CUDA cores).
 constexpr int kMinTcBlock = 3;
 constexpr int kSmCount = 152;  // of a GB300
 constexpr int min_tc_block_i8(int D) { return D == 64 ? 5 : 4; }
@@ -152,10 +153,13 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
     const bool forced = c.kernel == FTD_KERNEL_CUDA_CORE;
     const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
     const int D = c.head_dim;
-    // The wide kernel's 64- and 32-row blocks take multiples of 32 rows, except where its tiles could not
-    // give every SM one: blocks of 16 rows make four times the tiles (one or two slots of 64 rows per kv
-    // head over 2500 and 8192 rows 21.9 -> 15.0 and 29.3 -> 19.7 us; 24 slots of 2000 rows, 384
-    // tiles, would take 29 instead of 24.5).
+    // The wide kernel's 64- and 32-row blocks take multiples of 32 rows, except (scored step and cross attention)
+    // where its tiles could not give every SM one: blocks of 16 rows make four or two times the tiles.  Cross
+    // attention of 64 rows per kv head over memories of 2018 rows, 32 / 128 / 192 / 256 / 384 tiles: wide
+    // 20.9 / 22.0 / 23.0 / 23.4 / 25.2 us, 16-row blocks 14.1 / 18.1 / 20.9 / 24.1 / 29.5; 32 rows 15.2 / 17.7 / 18.5 / 19.2 / 19.9
+    // against 13.6 / 15.5 / 17.4 / 18.4 / 21.1; scored 64 rows 29.3 / 31.5 / 32.6 / 33.6 / 36.7 against 20.5 / 26.5 /
+    // 29.4 / 32.6 / 38.7, 32 rows 19.2 / 28.1 / 28.1 / 29.0 / 31.2 against 19.4 / 21.5 / 23.3 / 24.2 / 27.3.  (The crossing lies
+    // above one tile an SM, between 192 and 512 tiles.)
     const long long wide_tiles = static_cast<long long>(c.max_batch) * c.n_kv_heads * (rows_q / (rows_q % 64 == 0 ? 64 : 32)) *
                                  ((c.max_len + 127) / 128);
     const bool wide = half && D == 128 && rows_q % 32 == 0 && wide_tiles > kSmCount;

@@ -396,7 +396,7 @@ struct WeightedSplit {
 };
 
 // Workers for a tile space of weighted length V over segs segments (some may be empty), at most
-// Wmax: each gets at least sqrt(V / segs / cost) tiles.  Never more workers than tiles, so
+// Wmax: each gets at least sqrt(V / segs / cost) tiles.  Never more workers than the weighted length, so
 // every worker between a segment's first and last holds a piece of it.
 __device__ __forceinline__ int limited_workers(int V, int segs, float cost, int Wmax) {
     const int m = static_cast<int>(sqrtf(static_cast<float>(V) / (cost * static_cast<float>(segs))) + 0.5f);

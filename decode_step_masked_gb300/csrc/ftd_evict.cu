@@ -23,10 +23,11 @@
 // cluster has read them by then.
 //
 // Bound: 8 bytes per position for the selection, then the moved rows, read and written.
-// Measured: one row over in each of 8 x 32 heads of 2049 rows 9.2 us a call in a graph (launches,
-// the selection's chain of barriers and two dependent reads of memory); 32 ragged slots of 40
-// heads cut to 2048 rows 129 us, of which the moves take about 110 at 5.6 TB/s; 4 x 8 heads of 65536
-// INT8 rows cut to 8192 49 us, half of it the selection, half 128-byte rows gathered and scattered.
+// Measured (a graph on one cache; a stream over three caches in turn): one row over in each of 8 x 32 heads of
+// 2049 rows 9.2 us, 9.5 (launches, the selection's chain of barriers and two dependent reads of memory); 32
+// ragged slots of 40 heads cut to 2048 rows 129 us, 133, of which the moves take about 110 at 5.6 TB/s; 4 x 8
+// heads of 65536 INT8 rows cut to 8192 49 us, 56, half of it the selection, half 128-byte rows gathered
+// and scattered.
 // With 4 KB a warp in flight the moves took 15 % longer, with 512 threads three times an SM 12 %:
 // more reads and writes in flight at once than that slow one another down.
 #include <cooperative_groups.h>

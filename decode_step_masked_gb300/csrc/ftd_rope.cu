@@ -19,6 +19,9 @@
 // 111 us, 6.0 TB/s (tiles of 1280 / 2560 / 5120 / 10240 items 123 / 115 / 111 / 121 us; one / two / four
 // items in flight 117 / 116 / 125 us; blocks that keep one group of heads and walk the tokens, with the
 // bias in registers, 119 us at best); eight tokens of 32 + 32 heads 1.7 us a call in a graph.
+// Narrower accesses, where R / 2 or an address is no multiple of 16 bytes, cost as much more as they
+// are more: that prompt with R 120 / 52 / 22 (accesses of 8 / 4 / 2 bytes) 142 / 205 / 346 us, with
+// rows one element past a boundary 348.
 #include <cuda_runtime.h>
 
 #include "ftd_internal.cuh"
@@ -229,7 +232,8 @@ const void* pick(int vec) {
 cudaError_t launch_rope(RopeParams p, int vec, int sms, cudaStream_t stream) {
     const void* fn = p.dt == kF32 ? pick<float>(vec) : p.dt == kF16 ? pick<__half>(vec) : pick<__nv_bfloat16>(vec);
     // Large calls: tiles of up to kRopeTileItems items, up to eight blocks an SM; fewer tokens where
-    // that would give an SM fewer than four blocks (1001 fp32 tokens of 120 heads: 25.4 -> 21.4 us).
+    // that would give an SM fewer than four blocks (64 + 2 x 8 bf16 heads, 1200 / 2400 / 4000 tokens 11.2 /
+    // 22.1 / 37.6 -> 9.9 / 19.2 / 33.3 us; 40 + 2 x 40 fp32 heads, 200 / 600 / 1001 tokens 8.4 / 13.1 / 19.9 -> 7.5 / 10.1 / 20.3).
     // Calls with fewer tiles than SMs: their heads over enough blocks to reach every SM (at least
     // 8 heads each).
     const int per_token = p.heads * (p.D / (2 * vec));

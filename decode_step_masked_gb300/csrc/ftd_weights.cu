@@ -263,12 +263,18 @@ cudaError_t launch(const WeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_weights(WeightsParams p, cudaStream_t stream) {
-    // (above kMaxRowsPerThread rows, warps share them.) Four quads a thread for one or two query rows per kv head, one for eight and more (their rows
-    // keep the loads in flight).
+    // Quads of positions a thread: four for one or two query rows per kv head, two for three and four, one from five
+    // on (their rows keep the loads in flight); above kMaxRowsPerThread rows a block's warps share them.  Whole
+    // scored steps of 16 slots, 8 kv heads, 4080 rows, us with four / two / one quad / shared: 1 query row 49.4 / 50.0 /
+    // 48.8 / 59.4, 2 62.6 / 61.5 / 61.8 / 71.5, 4 55.6 / 54.5 / 55.0 / 64.4, 8 60.5 / 58.3 / 58.8 / 65.0, 12 72.8 / 69.1 / 69.5 /
+    // 74.5, 16 76.7 / 72.3 / 72.4 / 75.8; where a kv head has the blocks to itself, 8 slots, one kv head, 8176 rows: 16
+    // query rows 37.4 / 33.0 / 33.4 / 28.7, 24 47.4 / 40.6 / 42.1 / 31.4, 128 167 / 132 / 136 / 55.5.
     const int rows = p.nq * p.group;
-    // Scores of 16 MB and more, an eighth of L2, are dropped after their reading where rows are whole lines:
-    // three 70B-shaped batches in turn (33.5 MB of scores each) 101.8 -> 96.5 us a step, INT8 (16.8 MB)
-    // 136.2 -> 134.4; the 7B-shaped step (4.2 MB) would take 1 us more.
+    // Workspaces of 16 MB of scores and more, an eighth of L2, are dropped after their reading where rows are
+    // whole lines.  Three states in turn, kept -> dropped, us: 16-bit one query row 4.2 / 8.4 / 16.8 MB, half full 49.5 -> 49.6,
+    // 89.6 -> 89.0, 172.6 -> 169.6; eight query rows 8.4 / 16.8 / 25.2 / 33.6 MB, full 38.1 -> 39.5, 59.6 -> 58.2, 80.9 -> 77.9, 103.0 ->
+    // 97.8; INT8 16.8 MB 132.8 -> 132.9.  The rule goes by the context's size: short contents in a large context (33.6 MB,
+    // 512 of 8192 rows) pay for it, 24.3 -> 25.4.
     p.discard = p.Lmax % 32 == 0 && static_cast<size_t>(p.B) * p.Hkv * rows * p.Lmax * sizeof(float) >= (16u << 20);
     if (rows <= 2) return launch<4>(p, stream);
     if (rows <= 4) return launch<2>(p, stream);
