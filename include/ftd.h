@@ -403,7 +403,9 @@ ftd_status ftd_enable_scores(ftd_ctx* ctx, void* stream);
  * in fp32 and in a fixed order.  A row whose window or causal limit hides t adds
  * nothing there.  With T > 1 every token's row counts, also of tokens that the
  * caller then rejects.
- *   block_table : as in ftd_decode_mha_paged; NULL on a contiguous context.
+ *   block_table : as in ftd_decode_mha_paged; NULL on a contiguous context.  With a window and acc_out
+ *               apart from acc, the weights behind the window are copied, so entries there
+ *               name the slot's own pages too, or none: outside [0, num_pages) they are passed over.
  *   acc       : device fp32 plane laid out like one INT8 scale plane: [B][Hkv][Lmax],
  *               paged [num_pages][Hkv][page_size]; 16-byte aligned.
  *   acc_out   : the same, NULL or acc: in place.  Entries past L_b + T - 1, and
