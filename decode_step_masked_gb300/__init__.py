@@ -273,14 +273,17 @@ def _current_stream(device: int) -> int:
     return _raw_stream(device)
 
 
-def _expect(name, t, n, dtype=None, itemsize=0, dense=True):
-    """Raise where t does not hold n elements of dtype (or of itemsize bytes), one after the other."""
-    if t.numel() != n:
+def _expect(name, t, n, dtype=None, itemsize=0, dense=True, tail=()):
+    """Raise where t does not begin with n elements of dtype (or of itemsize bytes), one after the other.  It may hold
+    more, as a buffer kept for larger calls does, if its last dimensions are tail's."""
+    if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, {n} are needed")
     if (dtype is not None and t.dtype is not dtype) or (itemsize and t.element_size() != itemsize):
         raise ValueError(f"{name} is {t.dtype}, it has to be {dtype or f'the qkv type of {itemsize} bytes'}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name} has to be contiguous")
+    if t.numel() > n and t.dim() > 1 and any(a != b for a, b in zip(reversed(t.shape), reversed(tail))):
+        raise ValueError(f"{name} is laid out as {tuple(t.shape)}, its last dimensions have to be {tuple(tail)}")
 
 
 def _row_stride(t, width: int, head_dim: int) -> int:
@@ -329,6 +332,7 @@ class DecodeStep:
         self._float32 = torch.float32
         # cache rows: elements of a plane
         self._rows = num_pages * n_kv_heads * page_size if page_size else max_batch * n_kv_heads * max_len
+        self._plane_tail = (n_kv_heads, page_size or max_len)
         self._entries = max_batch * -(-max_len // page_size) if page_size else 0  # of a block table
         if scored:
             self.enable_scores(s)
@@ -364,22 +368,21 @@ class DecodeStep:
                                    s))
 
     def _check_planes(self, lens=(), ints=(), floats=(), table=None):
-        """Raise where a length, a plane or the block table (None: absent) has another type or size than the kernels take:
-        int32 per slot, int32 and fp32 per cache row."""
+        """Raise where a length, a plane or the block table (None: absent) has another type or layout than the kernels
+        take: int32 per slot, int32 and fp32 per cache row."""
         i32, f32, nb, nr = self._int32, self._float32, 4 * self.cfg.max_batch, 4 * self._rows
         for t in lens:
             if t is not None and (t.dtype is not i32 or t.nbytes != nb or not t.is_contiguous()):
-                raise ValueError(f"lengths and next_pos are contiguous int32 of {nb // 4} slots, not {t.dtype} {tuple(t.shape)}")
+                _expect("a list of lengths or next_pos", t, nb // 4, dtype=i32)
         for t in ints:
             if t is not None and (t.dtype is not i32 or t.nbytes != nr or not t.is_contiguous()):
-                raise ValueError(f"a positions plane is contiguous int32 of {nr // 4} rows, not {t.dtype} {tuple(t.shape)}")
+                _expect("a positions plane", t, nr // 4, dtype=i32, tail=self._plane_tail)
         for t in floats:
             if t is not None and (t.dtype is not f32 or t.nbytes != nr or not t.is_contiguous()):
-                raise ValueError(f"a weights plane is contiguous fp32 of {nr // 4} rows, not {t.dtype} {tuple(t.shape)}")
+                _expect("a weights plane", t, nr // 4, dtype=f32, tail=self._plane_tail)
         if table is not None and self._entries and (table.dtype is not i32 or table.nbytes != 4 * self._entries
                                                     or not table.is_contiguous()):
-            raise ValueError(f"the block table is contiguous int32 of {self._entries} entries, not {table.dtype} "
-                             f"{tuple(table.shape)}")
+            _expect("the block table", table, self._entries, dtype=i32, tail=(self._entries // self.cfg.max_batch,))
 
     def enable_scores(self, stream: Optional[int] = None):
         """Allocate what ``scored`` and ``evict`` need (``scored=True`` does it at construction)."""
@@ -443,20 +446,23 @@ class DecodeStep:
 
     def _check_rope(self, n, q, k, v, positions, q_out, k_out, v_out, bias):
         """Raise for what the pointers of a rope call cannot show."""
-        qw, kw, _ = self._widths
+        qw, kw, d = self._widths
         eb = self._qkv_bytes
-        if (v is None) != (v_out is None):
-            raise ValueError("v and v_out go together")
+        if q.numel() != n * qw:
+            raise ValueError(f"q holds {q.numel()} elements, no whole number of rows of {qw}")
         for name, t, width in (("q", q, qw), ("k", k, kw), ("v", v, kw)):
             if t is not None:
                 _expect(name, t, n * width, itemsize=eb, dense=False)  # (_row_stride looks at the strides)
         for name, t, width in (("q_out", q_out, qw), ("k_out", k_out, kw), ("v_out", v_out, kw)):
             if t is not None:
-                _expect(name, t, n * width, itemsize=eb)
+                _expect(name, t, n * width, itemsize=eb, tail=(width,) if t.shape[-1] == width else (width // d, d))
         if bias is not None:
             _expect("bias", bias, qw + 2 * kw, itemsize=eb)
         if self._axes:  # (else the library says that set_rope comes first)
             _expect("positions", positions, n * self._axes, dtype=self._int32)
+            if self._axes > 1 and positions.numel() > n * self._axes and positions.dim() > 1 and (
+                    positions.numel() // positions.shape[0] != n):
+                raise ValueError(f"positions is laid out as {tuple(positions.shape)}, an axis has {n} tokens")
 
     def rope(self, q, k, v, positions, q_out, k_out, v_out=None, bias=None, stream: Optional[int] = None):
         """Bias and rotary positions for the tokens of q, k (and v, which only takes the bias; None with

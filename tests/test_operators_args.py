@@ -42,7 +42,12 @@ def test_rope_arguments(step):
     good = [{}, dict(v=None, v_out=None), dict(bias=None), dict(bias=torch.zeros((HQ + 2 * HKV, D), dtype=torch.float16)),
             dict(q=fused[:, :HQ * D], k=fused[:, HQ * D:(HQ + HKV) * D], v=fused[:, (HQ + HKV) * D:]),
             dict(q_out=ok["q_out"].view(5, HQ * D)), dict(q=ok["q"].view(torch.int16)),  # (bits of the same width)
-            dict(positions=torch.zeros(10, dtype=torch.int32))]
+            dict(positions=torch.zeros(10, dtype=torch.int32)),
+            # buffers kept for larger calls, and what the library itself refuses
+            dict(positions=torch.zeros(64, dtype=torch.int32)), dict(positions=torch.zeros((4, 5), dtype=torch.int32)),
+            dict(k=torch.zeros((9, HKV, D), dtype=torch.float16)), dict(q_out=torch.zeros((9, HQ, D), dtype=torch.float16)),
+            dict(k_out=torch.zeros((9, HKV * D), dtype=torch.float16)), dict(v_out=torch.zeros(9 * HKV * D, dtype=torch.float16)),
+            dict(bias=torch.zeros((HQ + 2 * HKV) * D + 7, dtype=torch.float16)), dict(v=None), dict(v_out=None)]
     for kw in good:
         with pytest.raises(Called):
             step.rope(**dict(ok, **kw))
@@ -54,7 +59,8 @@ def test_rope_arguments(step):
            dict(q=torch.zeros((5, HQ * D + 1), dtype=torch.float16)), dict(q=z.float()), dict(k=ok["k"].float()),
            dict(v=ok["v"].float()), dict(q_out=z[:4]), dict(q_out=z.float()), dict(k_out=ok["k"][:4]), dict(v_out=ok["v"][:4]),
            dict(q_out=fused[:, :HQ * D]), dict(k_out=fused[:, :HKV * D]), dict(v_out=fused[:, :HKV * D]),
-           dict(v=None), dict(v_out=None), dict(bias=ok["bias"][:-1]), dict(bias=ok["bias"].float()),
+           dict(positions=torch.zeros((2, 8), dtype=torch.int32)), dict(q_out=torch.zeros((9, HQ, D + 8), dtype=torch.float16)),
+           dict(k_out=torch.zeros((9, HKV * D + 64), dtype=torch.float16)), dict(bias=ok["bias"][:-1]), dict(bias=ok["bias"].float()),
            dict(bias=torch.zeros(2 * (HQ + 2 * HKV) * D, dtype=torch.float16)[::2])]
     for kw in bad:
         with pytest.raises(ValueError):
@@ -80,7 +86,13 @@ def test_scored_evict_and_cross_arguments(step):
         for name in names:
             x = ints.get(name, floats.get(name))
             bad = [x.long() if name in ints else x.double(), x.float() if name in ints else x.half(), x[:-1],
-                   torch.cat([x, x]), torch.stack([x, x], -1)[..., 0]]
+                   torch.stack([x, x], -1)[..., 0]]
+            if x.dim() == 3:
+                bad += [torch.cat([x, x], 2), torch.cat([x, x], 1)]  # (another context's layout)
+            # a buffer kept for more slots, and a flat one
+            for y in (torch.cat([x, x]), torch.cat([x, x]).view(-1)):
+                with pytest.raises(Called):
+                    fn(**dict(args, **{name: y}))
             for y in bad:
                 with pytest.raises(ValueError):
                     fn(**dict(args, **{name: y}))
@@ -91,9 +103,11 @@ def test_paged_planes(step, monkeypatch):
     s = ftd.DecodeStep(B, HQ, HKV, D, 256, "f16", "f16", stream=0, page_size=128, num_pages=7)
     lens, plane, table = torch.zeros(B, dtype=torch.int32), torch.zeros((7, HKV, 128)), torch.zeros((B, 2), dtype=torch.int32)
     args = dict(acc=plane, positions=plane.int(), seq_lens=lens, next_pos=lens, new_lens=lens, budget=8, block_table=table)
-    with pytest.raises(Called):
-        s.evict(**args)
+    for kw in ({}, dict(acc=torch.zeros((9, HKV, 128))), dict(block_table=torch.zeros((B + 2, 2), dtype=torch.int32))):
+        with pytest.raises(Called):
+            s.evict(**dict(args, **kw))
     for kw in (dict(acc=plane[:6]), dict(acc=torch.zeros((B, HKV, 256))), dict(block_table=table.long()), dict(block_table=table[:, :1]),
+               dict(block_table=torch.zeros((B, 3), dtype=torch.int32)), dict(acc=torch.zeros((9, HKV, 256))),
                dict(block_table=table[:2])):
         with pytest.raises(ValueError):
             s.evict(**dict(args, **kw))
