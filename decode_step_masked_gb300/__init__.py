@@ -37,7 +37,7 @@ EXPORTS = ("ftd_init", "ftd_cache_ptrs", "ftd_decode_mha", "ftd_decode_mha_curre
            "ftd_decode_mha_host", "ftd_get_error", "ftd_destroy", "ftd_status_str", "ftd_last_error",
            "ftd_kernel_launches", "ftd_decode_mha_noalloc", "ftd_debug_stall_next",
            "ftd_debug_late_lengths", "ftd_debug_kernel", "ftd_decode_mha_proj", "ftd_set_rope", "ftd_rope_qkv", "ftd_enable_scores",
-           "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha")
+           "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha", "ftd_norm_rope_qkv", "ftd_build_tables")
 
 
 class FtdConfig(ctypes.Structure):
@@ -109,6 +109,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ftd_set_rope.restype = I
     lib.ftd_rope_qkv.argtypes = [P] * 4 + [ctypes.c_int64] * 2 + [P] * 2 + [ctypes.c_int64] + [P] * 4
     lib.ftd_rope_qkv.restype = I
+    lib.ftd_norm_rope_qkv.argtypes = ([P] * 4 + [ctypes.c_int64] * 2 + [P] * 3 + [ctypes.c_float] * 2 + [P, ctypes.c_int64] +
+                                      [P] * 8)
+    lib.ftd_norm_rope_qkv.restype = I
+    lib.ftd_build_tables.argtypes = [P] * 11 + [ctypes.c_int64, P]
+    lib.ftd_build_tables.restype = I
     lib.ftd_enable_scores.argtypes = [P, P]
     lib.ftd_enable_scores.restype = I
     lib.ftd_decode_mha_scored.argtypes = [P] * 16
@@ -189,6 +194,19 @@ def ftd_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_token
                  stream) -> int:
     return load_library().ftd_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out, k_out,
                                        v_out, stream)
+
+
+def ftd_norm_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, q_weight, k_weight, eps, weight_offset, positions, n_tokens,
+                      q_out, k_out, v_out, slots, k_cache, v_cache, scales, stream) -> int:
+    return load_library().ftd_norm_rope_qkv(ctx, q, k, v, q_stride, kv_stride, qkv_bias, q_weight, k_weight, eps,
+                                            weight_offset, positions, n_tokens, q_out, k_out, v_out, slots, k_cache,
+                                            v_cache, scales, stream)
+
+
+def ftd_build_tables(ctx, old_lens, new_lens, served, block_table, free_pages, n_free, n_free_out, offsets, slots, positions,
+                     max_tokens, stream) -> int:
+    return load_library().ftd_build_tables(ctx, old_lens, new_lens, served, block_table, free_pages, n_free, n_free_out,
+                                           offsets, slots, positions, max_tokens, stream)
 
 
 def ftd_enable_scores(ctx, stream) -> int:
@@ -327,6 +345,7 @@ class DecodeStep:
         self.device = torch.cuda.current_device()
         self._widths = (n_q_heads * head_dim, n_kv_heads * head_dim, head_dim)
         self._qkv_bytes = 4 if qkv_dtype == "f32" else 2
+        self._cache_bytes = {"f32": 4, "f16": 2, "bf16": 2, "i8": 1}[cache_dtype]
         self._int32 = torch.int32
         self._axes = 0
         self._float32 = torch.float32
@@ -489,6 +508,72 @@ class DecodeStep:
         st = ftd_rope_qkv(self.ctx, q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), qs, ks,
                           None if bias is None else bias.data_ptr(), positions.data_ptr(), n, q_out.data_ptr(),
                           k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), s)
+        if st:
+            check(st)
+
+    def _check_norm_rope(self, n, q_weight, k_weight, slots, k_cache, v_cache, scales):
+        """Raise for what the pointers of the norms and of a fill cannot show."""
+        d, eb = self._widths[2], self._qkv_bytes
+        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if t is not None:
+                _expect(name, t, d, itemsize=eb)
+        if slots is not None:
+            _expect("slots", slots, n, dtype=self._int32)
+            for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+                if t is not None:
+                    _expect(name, t, self._rows * d, itemsize=self._cache_bytes, tail=self._plane_tail + (d,))
+            if scales is not None:
+                _expect("scales", scales, 2 * self._rows, dtype=self._float32, tail=self._plane_tail)
+
+    def norm_rope(self, q, k, v, positions, q_out, k_out=None, v_out=None, bias=None, q_weight=None, k_weight=None, eps=1e-6,
+                  weight_offset=0.0, slots=None, k_cache=None, v_cache=None, scales=None, stream: Optional[int] = None):
+        """``rope`` with norms of the query and key heads ahead of the rotation: x / sqrt(mean(x^2) + eps) *
+        (weight + weight_offset), weights of head_dim elements (None: no norm).  With ``slots`` (int32 per
+        token, as ``tables`` makes them; negative: none) keys and values go straight into the cache (None: the
+        pool's), rounded or quantised as the step appends them, and k_out and v_out stay None."""
+        qw, kw, d = self._widths
+        eb = self._qkv_bytes
+        n = q.numel() // qw
+        bq, bk = n * qw * eb, n * kw * eb
+        if (q.nbytes != bq or k.nbytes != bk or q_out.nbytes != bq or positions.nbytes != 4 * n * self._axes
+                or positions.dtype is not self._int32 or not positions.is_contiguous() or not q_out.is_contiguous()
+                or bias is not None and (bias.nbytes != (qw + 2 * kw) * eb or not bias.is_contiguous())
+                or k_out is not None and (k_out.nbytes != bk or not k_out.is_contiguous())
+                or v is not None and v.nbytes != bk or v_out is not None and (v_out.nbytes != bk or not v_out.is_contiguous())):
+            self._check_rope(n, q, k, v, positions, q_out, k_out, v_out, bias)
+        if (q_weight is not None and (q_weight.nbytes != d * eb or not q_weight.is_contiguous())
+                or k_weight is not None and (k_weight.nbytes != d * eb or not k_weight.is_contiguous()) or slots is not None):
+            self._check_norm_rope(n, q_weight, k_weight, slots, k_cache, v_cache, scales)
+        s = _current_stream(self.device) if stream is None else stream
+        qs = 0 if q.is_contiguous() else _row_stride(q, qw, d)
+        ks = 0 if k.is_contiguous() else _row_stride(k, kw, d)
+        if v is not None and ((0 if v.is_contiguous() else _row_stride(v, kw, d)) or kw) != (ks or kw) and n > 1:
+            raise ValueError("k and v must share one row stride")
+        st = ftd_norm_rope_qkv(self.ctx, q.data_ptr(), k.data_ptr(), _ptr(v), qs, ks, _ptr(bias), _ptr(q_weight),
+                               _ptr(k_weight), eps, weight_offset, positions.data_ptr(), n, q_out.data_ptr(), _ptr(k_out),
+                               _ptr(v_out), _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(scales), s)
+        if st:
+            check(st)
+
+    def tables(self, old_lens, new_lens, served, block_table=None, free_pages=None, n_free=None, n_free_out=None, offsets=None,
+               slots=None, positions=None, stream: Optional[int] = None):
+        """Bring every slot from old_lens to new_lens cached rows: pages from and to the free list (a stack of
+        n_free pages; paged contexts), ``served`` the lengths that were granted (may be either list), ``offsets``
+        int32 [B + 1] of the new tokens packed slot by slot, and their ``slots`` and ``positions`` (int32, one length)."""
+        self._check_planes((old_lens, new_lens, served), table=block_table)
+        if free_pages is not None:
+            _expect("free_pages", free_pages, self.cfg.num_pages, dtype=self._int32)
+        for name, t, n in (("n_free", n_free, 1), ("n_free_out", n_free_out, 1), ("offsets", offsets, self.cfg.max_batch + 1),
+                           ("slots", slots, 0), ("positions", positions, 0)):
+            if t is not None:
+                _expect(name, t, n, dtype=self._int32, tail=t.shape)
+        if slots is not None and positions is not None and slots.numel() != positions.numel():
+            raise ValueError(f"slots holds {slots.numel()} tokens, positions {positions.numel()}")
+        n = slots.numel() if slots is not None else positions.numel() if positions is not None else 0
+        s = _current_stream(self.device) if stream is None else stream
+        st = ftd_build_tables(self.ctx, old_lens.data_ptr(), new_lens.data_ptr(), served.data_ptr(), _ptr(block_table),
+                              _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(offsets), _ptr(slots), _ptr(positions),
+                              n, s)
         if st:
             check(st)
 

@@ -370,6 +370,7 @@ struct ftd_ctx {
     uint32_t* counters = nullptr;
     size_t n_counters = 0;
     uint32_t* err = nullptr;
+    uint32_t* tab_count = nullptr;  // ftd_build_tables: blocks that have read
     void* st_q = nullptr;
     void* st_k = nullptr;
     void* st_v = nullptr;
@@ -526,6 +527,7 @@ ftd_status ftd_init(const ftd_config* cfg, void* stream, ftd_ctx** out) {
     const bool proj = c.proj_dim > 0;
     const size_t n_pcnt = proj ? static_cast<size_t>(plan.nblk) * plan.mtiles : 0;
     const size_t o_pcnt = carve(n_pcnt * sizeof(uint32_t));
+    const size_t o_tcnt = carve(sizeof(uint32_t));
     const size_t zero_end = off;  // caches, scales, counters and the error word start at zero
     const size_t o_ws = carve(ws_bytes);
     const size_t plane_bytes = proj ? static_cast<size_t>(plan.tokens) * Hq * D * 2 : 0;
@@ -547,6 +549,7 @@ ftd_status ftd_init(const ftd_config* cfg, void* stream, ftd_ctx** out) {
     ctx->scales = scale_bytes ? reinterpret_cast<float*>(base + o_s) : nullptr;
     ctx->counters = reinterpret_cast<uint32_t*>(base + o_cnt);
     ctx->err = reinterpret_cast<uint32_t*>(base + o_err);
+    ctx->tab_count = reinterpret_cast<uint32_t*>(base + o_tcnt);
     ctx->ws = reinterpret_cast<float*>(base + o_ws);
     ctx->st_q = base + o_q;
     ctx->st_k = base + o_kn;
@@ -1215,35 +1218,32 @@ ftd_status ftd_set_rope(ftd_ctx* ctx, const ftd_rope_config* cfg) {
     return FTD_OK;
 }
 
-ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride, int64_t kv_stride,
-                        const void* qkv_bias, const int32_t* positions, int64_t n_tokens, void* q_out, void* k_out,
-                        void* v_out, void* stream) {
-    g_last_error.clear();
-    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: ctx is NULL");
-    if (!ctx->rope_set) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: ftd_set_rope first");
+// What ftd_rope_qkv and ftd_norm_rope_qkv check alike: sizes, strides (0 becomes dense rows), alignment, overlaps;
+// vec becomes the widest access that every row, pointer and run of pairs allows.  to_cache: keys and values go to
+// the caches, not to k_out and v_out.  weights: two more arrays of head_dim elements, or NULL.
+namespace {
+ftd_status check_rope(const ftd_ctx* ctx, const char* what, const void* q, const void* k, const void* v, int64_t& q_stride,
+                      int64_t& kv_stride, const void* qkv_bias, const int32_t* positions, int64_t n_tokens, const void* q_out,
+                      const void* k_out, const void* v_out, bool to_cache, const void* const weights[2], int& vec) {
     const ftd_config& c = ctx->cfg;
-    if (n_tokens < 0 || n_tokens > (static_cast<int64_t>(1) << 31) - 1)
-        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: n_tokens %lld", static_cast<long long>(n_tokens));
-    if (n_tokens == 0) return FTD_OK;
-    if (!q || !k || !positions || !q_out || !k_out || (v == nullptr) != (v_out == nullptr))
-        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: q, k, positions, q_out and k_out must be non-NULL, v and v_out both or neither");
+    if (!q || !k || !positions || !q_out || (!to_cache && (!k_out || (v == nullptr) != (v_out == nullptr))))
+        return fail(FTD_ERR_INVALID_ARG, "%s: q, k, positions, q_out and k_out must be non-NULL, v and v_out both or neither", what);
     const int64_t qw = static_cast<int64_t>(c.n_q_heads) * c.head_dim, kw = static_cast<int64_t>(c.n_kv_heads) * c.head_dim;
     if (q_stride == 0) q_stride = qw;
     if (kv_stride == 0) kv_stride = kw;
     if (q_stride < qw || kv_stride < kw || q_stride > (static_cast<int64_t>(1) << 31) || kv_stride > (static_cast<int64_t>(1) << 31))
-        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: strides %lld, %lld below a row of %lld, %lld elements (or above 2^31)",
+        return fail(FTD_ERR_INVALID_ARG, "%s: strides %lld, %lld below a row of %lld, %lld elements (or above 2^31)", what,
                     static_cast<long long>(q_stride), static_cast<long long>(kv_stride), static_cast<long long>(qw),
                     static_cast<long long>(kw));
     const int eb = elem_bytes(c.qkv_dtype);
-    const void* ptrs[] = {q, k, v, qkv_bias, q_out, k_out, v_out};
-    // the widest access that every row, pointer and pair of runs allows
-    int vec = 16 / eb;
+    const void* ptrs[] = {q, k, v, qkv_bias, q_out, k_out, v_out, weights[0], weights[1]};
+    vec = 16 / eb;
     while (vec > 1 && (q_stride % vec != 0 || kv_stride % vec != 0 || (ctx->rope.R / 2) % vec != 0)) vec >>= 1;
     for (const void* p : ptrs) {
-        if (!aligned(p, eb)) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: pointers must be aligned to their element");
+        if (!aligned(p, eb)) return fail(FTD_ERR_INVALID_ARG, "%s: pointers must be aligned to their element", what);
         while (vec > 1 && !aligned(p, static_cast<uintptr_t>(vec * eb))) vec >>= 1;
     }
-    if (!aligned(positions, 4)) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: positions must be 4-byte aligned");
+    if (!aligned(positions, 4)) return fail(FTD_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", what);
     // An output may be its own input (same rows); any other overlap would be read after it was written.
     const size_t n = static_cast<size_t>(n_tokens);
     struct Span { const void* p; size_t bytes; int64_t stride, width; };
@@ -1256,15 +1256,37 @@ ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* 
         for (int i = 0; i < 3; ++i) {
             if (!in[i].p || !overlaps(in[i].p, in[i].bytes, out[o].p, out[o].bytes)) continue;
             if (!(i == o && in[i].p == out[o].p && (in[i].stride == in[i].width || n == 1)))
-                return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: an output may only be its own dense input, or apart from every input");
+                return fail(FTD_ERR_INVALID_ARG, "%s: an output may only be its own dense input, or apart from every input", what);
         }
         for (int i = 0; i < o; ++i)
             if (out[i].p && overlaps(out[i].p, out[i].bytes, out[o].p, out[o].bytes))
-                return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: outputs overlap");
+                return fail(FTD_ERR_INVALID_ARG, "%s: outputs overlap", what);
         if (overlaps(positions, n * ctx->rope.axes * 4, out[o].p, out[o].bytes) ||
             (qkv_bias && overlaps(qkv_bias, static_cast<size_t>(qw + 2 * kw) * eb, out[o].p, out[o].bytes)))
-            return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: an output overlaps positions or the bias");
+            return fail(FTD_ERR_INVALID_ARG, "%s: an output overlaps positions or the bias", what);
+        for (int i = 0; i < 2; ++i)
+            if (weights[i] && overlaps(weights[i], static_cast<size_t>(c.head_dim) * eb, out[o].p, out[o].bytes))
+                return fail(FTD_ERR_INVALID_ARG, "%s: an output overlaps the norms' weights", what);
     }
+    return FTD_OK;
+}
+}  // namespace
+
+ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride, int64_t kv_stride,
+                        const void* qkv_bias, const int32_t* positions, int64_t n_tokens, void* q_out, void* k_out,
+                        void* v_out, void* stream) {
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: ctx is NULL");
+    if (!ctx->rope_set) return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: ftd_set_rope first");
+    const ftd_config& c = ctx->cfg;
+    if (n_tokens < 0 || n_tokens > (static_cast<int64_t>(1) << 31) - 1)
+        return fail(FTD_ERR_INVALID_ARG, "ftd_rope_qkv: n_tokens %lld", static_cast<long long>(n_tokens));
+    if (n_tokens == 0) return FTD_OK;
+    int vec = 1;
+    const void* const none[2] = {nullptr, nullptr};
+    const ftd_status st = check_rope(ctx, "ftd_rope_qkv", q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out,
+                                     k_out, v_out, false, none, vec);
+    if (st != FTD_OK) return st;
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
     ftd::RopeParams r = ctx->rope;
@@ -1287,6 +1309,170 @@ ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* 
     r.heads = c.n_q_heads + c.n_kv_heads * (move_v ? 2 : 1);
     const cudaError_t e = ftd::launch_rope(r, vec, ctx->grid, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rotary kernel launch");
+    g_launches.fetch_add(1);
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return FTD_OK;
+}
+
+ftd_status ftd_norm_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride, int64_t kv_stride,
+                             const void* qkv_bias, const void* q_weight, const void* k_weight, float eps, float weight_offset,
+                             const int32_t* positions, int64_t n_tokens, void* q_out, void* k_out, void* v_out,
+                             const int32_t* slots, void* k_cache, void* v_cache, float* scales, void* stream) {
+    static const char* const what = "ftd_norm_rope_qkv";
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "%s: ctx is NULL", what);
+    if (!ctx->rope_set) return fail(FTD_ERR_INVALID_ARG, "%s: ftd_set_rope first", what);
+    const ftd_config& c = ctx->cfg;
+    if (n_tokens < 0 || n_tokens > (static_cast<int64_t>(1) << 31) - 1)
+        return fail(FTD_ERR_INVALID_ARG, "%s: n_tokens %lld", what, static_cast<long long>(n_tokens));
+    if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(weight_offset))
+        return fail(FTD_ERR_INVALID_ARG, "%s: eps must be finite and >= 0, weight_offset finite", what);
+    if (n_tokens == 0) return FTD_OK;
+    const bool i8 = c.cache_dtype == FTD_I8;
+    if (slots) {
+        if (k_out || v_out) return fail(FTD_ERR_INVALID_ARG, "%s: with slots, keys and values go to the caches (k_out and v_out NULL)", what);
+        if (!v) return fail(FTD_ERR_INVALID_ARG, "%s: with slots, v must be non-NULL", what);
+        if (!k_cache) k_cache = ctx->k_cache;
+        if (!v_cache) v_cache = ctx->v_cache;
+        if (i8 && !scales) scales = ctx->scales;
+        if (!aligned(slots, 4)) return fail(FTD_ERR_INVALID_ARG, "%s: slots must be 4-byte aligned", what);
+        if (!aligned16(k_cache) || !aligned16(v_cache) || (i8 && !aligned16(scales)))
+            return fail(FTD_ERR_INVALID_ARG, "%s: caches and scales must be 16-byte aligned", what);
+    } else if (k_cache || v_cache || scales) {
+        return fail(FTD_ERR_INVALID_ARG, "%s: caches and scales go with slots", what);
+    }
+    int vec = 1;
+    const void* const weights[2] = {q_weight, k_weight};
+    const ftd_status st = check_rope(ctx, what, q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out, k_out, v_out,
+                                     slots != nullptr, weights, vec);
+    if (st != FTD_OK) return st;
+    if (slots) {
+        // the caches against everything that is read, q_out, and each other
+        const size_t n = static_cast<size_t>(n_tokens), eb = elem_bytes(c.qkv_dtype);
+        const size_t qw = static_cast<size_t>(c.n_q_heads) * c.head_dim, kw = static_cast<size_t>(c.n_kv_heads) * c.head_dim;
+        const size_t kv = ((n - 1) * kv_stride + kw) * eb, cache = ctx->rows * c.head_dim * elem_bytes(c.cache_dtype);
+        struct Span { const void* p; size_t bytes; };
+        const Span written[] = {{k_cache, cache}, {v_cache, cache}, {i8 ? scales : nullptr, 2 * ctx->rows * sizeof(float)}};
+        const Span others[] = {{q, ((n - 1) * q_stride + qw) * eb}, {k, kv}, {v, kv}, {qkv_bias, (qw + 2 * kw) * eb},
+                               {q_weight, c.head_dim * eb}, {k_weight, c.head_dim * eb}, {positions, n * ctx->rope.axes * 4},
+                               {slots, n * 4}, {q_out, n * qw * eb}};
+        for (int i = 0; i < 3; ++i) {
+            if (!written[i].p) continue;
+            for (const Span& o : others)
+                if (o.p && overlaps(written[i].p, written[i].bytes, o.p, o.bytes))
+                    return fail(FTD_ERR_INVALID_ARG, "%s: a cache overlaps an input or q_out", what);
+            for (int j = 0; j < i; ++j)
+                if (written[j].p && overlaps(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+                    return fail(FTD_ERR_INVALID_ARG, "%s: the caches and scales overlap", what);
+        }
+        if (overlaps(slots, n * 4, q_out, n * qw * eb)) return fail(FTD_ERR_INVALID_ARG, "%s: q_out overlaps slots", what);
+    }
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    ftd::NormRopeParams r{};
+    static_cast<ftd::RopeParams&>(r) = ctx->rope;
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.bias = qkv_bias;
+    r.qo = q_out;
+    r.ko = k_out;
+    r.vo = v_out;
+    r.pos = positions;
+    r.n = n_tokens;
+    r.q_stride = q_stride;
+    r.kv_stride = kv_stride;
+    r.Hq = c.n_q_heads;
+    r.Hkv = c.n_kv_heads;
+    r.dt = static_cast<int>(c.qkv_dtype);
+    r.qw = q_weight;
+    r.kw = k_weight;
+    r.eps = eps;
+    r.offset = weight_offset;
+    r.slots = slots;
+    r.k_cache = static_cast<unsigned char*>(k_cache);
+    r.v_cache = static_cast<unsigned char*>(v_cache);
+    r.k_scales = slots && i8 ? scales : nullptr;
+    r.v_scales = slots && i8 ? scales + ctx->rows : nullptr;
+    r.err = ctx->err;
+    r.n_slots = static_cast<int>(ctx->rows / c.n_kv_heads);
+    r.unit = ctx->paged ? c.page_size : c.max_len;
+    r.cache_dt = static_cast<int>(c.cache_dtype);
+    // values in place and without a bias are done already
+    const bool move_v = v && (slots || v != v_out || qkv_bias);
+    r.heads = c.n_q_heads + c.n_kv_heads * (move_v ? 2 : 1);
+    const cudaError_t e = ftd::launch_norm_rope(r, vec, ctx->grid, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotary kernel launch");
+    g_launches.fetch_add(1);
+    ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return FTD_OK;
+}
+
+ftd_status ftd_build_tables(ftd_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, int32_t* served, int32_t* block_table,
+                            int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, int32_t* offsets, int32_t* slots,
+                            int32_t* positions, int64_t max_tokens, void* stream) {
+    static const char* const what = "ftd_build_tables";
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "%s: ctx is NULL", what);
+    const ftd_config& c = ctx->cfg;
+    if (!old_lens || !new_lens || !served)
+        return fail(FTD_ERR_INVALID_ARG, "%s: old_lens, new_lens and served must be non-NULL", what);
+    if (ctx->paged && (!block_table || !free_pages || !n_free))
+        return fail(FTD_ERR_INVALID_ARG, "%s: a paged context needs block_table, free_pages and n_free", what);
+    if (!ctx->paged && (block_table || free_pages || n_free || n_free_out))
+        return fail(FTD_ERR_INVALID_ARG, "%s: a contiguous context has no pages", what);
+    if (!n_free_out) n_free_out = const_cast<int32_t*>(n_free);
+    if (max_tokens < 0 || max_tokens > (static_cast<int64_t>(1) << 31) - 1)
+        return fail(FTD_ERR_INVALID_ARG, "%s: max_tokens %lld", what, static_cast<long long>(max_tokens));
+    const size_t B = static_cast<size_t>(c.max_batch), m = static_cast<size_t>(max_tokens) * 4;
+    struct Span { const void* p; size_t bytes; };
+    const Span in[] = {{old_lens, B * 4}, {new_lens, B * 4}, {n_free, 4}};
+    const Span out[] = {{served, B * 4},
+                        {n_free_out, 4},
+                        {block_table, B * ctx->pages_per_seq * 4},
+                        {free_pages, static_cast<size_t>(c.num_pages) * 4},
+                        {offsets, (B + 1) * 4},
+                        {slots, m},
+                        {positions, m}};
+    for (const Span& s : in)
+        if (!aligned(s.p, 4)) return fail(FTD_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", what);
+    for (int o = 0; o < 7; ++o) {
+        if (!aligned(out[o].p, 4)) return fail(FTD_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", what);
+        if (!out[o].p) continue;
+        for (int i = 0; i < 3; ++i) {
+            // updated in place: the lengths by served, n_free by n_free_out
+            if (in[i].p == out[o].p && (i < 2 ? o == 0 : o == 1)) continue;
+            if (in[i].p && overlaps(in[i].p, in[i].bytes, out[o].p, out[o].bytes))
+                return fail(FTD_ERR_INVALID_ARG, "%s: an output overlaps an input (only served may be old_lens or new_lens, and n_free_out n_free)", what);
+        }
+        for (int i = 0; i < o; ++i)
+            if (out[i].p && overlaps(out[i].p, out[i].bytes, out[o].p, out[o].bytes))
+                return fail(FTD_ERR_INVALID_ARG, "%s: outputs overlap", what);
+    }
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    ftd::TablesParams t{};
+    t.old_lens = old_lens;
+    t.new_lens = new_lens;
+    t.served = served;
+    t.block_table = block_table;
+    t.free_pages = free_pages;
+    t.n_free = n_free;
+    t.n_free_out = n_free_out;
+    t.offsets = offsets;
+    t.slots = max_tokens ? slots : nullptr;
+    t.positions = max_tokens ? positions : nullptr;
+    t.count = ctx->tab_count;
+    t.err = ctx->err;
+    t.cap = max_tokens;
+    t.B = c.max_batch;
+    t.Lmax = c.max_len;
+    t.per = ctx->pages_per_seq;
+    t.page_shift = page_shift_of(ctx);
+    t.num_pages = c.num_pages;
+    t.vec = aligned16(slots) && aligned16(positions);
+    const cudaError_t e = ftd::launch_tables(t, ctx->grid, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tables kernel launch");
     g_launches.fetch_add(1);
     ctx->last_stream = static_cast<cudaStream_t>(stream);
     return FTD_OK;

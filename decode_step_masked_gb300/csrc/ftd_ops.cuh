@@ -1,6 +1,6 @@
 // ftd_ops.cuh -- parameters and launchers of the operators around the decode step:
-// rotary positions (ftd_rope.cu), the accumulated attention weights (ftd_weights.cu)
-// and the eviction by them (ftd_evict.cu).
+// rotary positions (ftd_rope.cu), with head norms (ftd_norm_rope.cu), block tables (ftd_tables.cu),
+// the accumulated attention weights (ftd_weights.cu) and the eviction by them (ftd_evict.cu).
 #pragma once
 
 #include "ftd_common.cuh"
@@ -50,6 +50,43 @@ struct RopeParams {
 };
 // vec: elements per access (up to 16 bytes); every pointer and stride aligned to it, R / 2 a multiple of it.
 cudaError_t launch_rope(RopeParams p, int vec, int sms, cudaStream_t stream);
+
+// Head norms and rotary positions in one pass (ftd_norm_rope.cu); heads: Hq + Hkv, and Hkv more with values.
+constexpr int kCacheI8 = 3;  // cache types: kF32, kF16, kBF16, and INT8
+struct NormRopeParams : RopeParams {
+    const void* qw;  // [D] dt weights of the query and key norms, nullptr: no norm
+    const void* kw;
+    float eps, offset;
+    const int32_t* slots;  // [n] cache slot of a token (negative: none); nullptr: keys and values go to ko, vo
+    unsigned char* k_cache;
+    unsigned char* v_cache;
+    float* k_scales;  // INT8
+    float* v_scales;
+    uint32_t* err;
+    int n_slots, unit;  // slots of the cache, and of one unit (a sequence's rows, or a page)
+    int cache_dt;
+};
+cudaError_t launch_norm_rope(NormRopeParams p, int vec, int sms, cudaStream_t stream);
+
+// Block tables and slot maps (ftd_tables.cu).
+struct TablesParams {
+    const int32_t* old_lens;  // [B]
+    const int32_t* new_lens;
+    int32_t* served;          // [B], may be either
+    int32_t* block_table;     // [B][per], nullptr: contiguous cache
+    int32_t* free_pages;      // [num_pages]
+    const int32_t* n_free;
+    int32_t* n_free_out;      // may be n_free
+    int32_t* offsets;         // [B + 1] or nullptr
+    int32_t* slots;           // [cap] or nullptr
+    int32_t* positions;       // [cap] or nullptr
+    uint32_t* count;          // blocks that have read; zero between calls
+    uint32_t* err;
+    long long cap;
+    int B, Lmax, per, page_shift, num_pages;
+    int vec;                  // slots and positions allow 16-byte stores
+};
+cudaError_t launch_tables(TablesParams p, int sms, cudaStream_t stream);
 
 struct WeightsParams {
     const float* scores;  // as DecodeParams::scores / stats

@@ -26,6 +26,7 @@
 
 #include "ftd_internal.cuh"
 #include "ftd_ops.cuh"
+#include "ftd_rope.cuh"
 
 namespace ftd {
 namespace {
@@ -33,38 +34,6 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTile = 16;         // most tokens of a tile
 constexpr int kRopeTileItems = 5120;  // most items of a large call's tile
-
-template <typename T>
-__device__ __forceinline__ float to_f(T x) {
-    if constexpr (std::is_same_v<T, float>) return x;
-    else if constexpr (std::is_same_v<T, __half>) return __half2float(x);
-    else return __bfloat162float(x);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float x) {
-    if constexpr (std::is_same_v<T, float>) return x;
-    else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(x);
-    else return __float2bfloat16_rn(x);
-}
-
-// VEC consecutive elements, as one access of 2 to 16 bytes.
-template <typename T, int VEC>
-struct Chunk {
-    static constexpr int BYTES = VEC * static_cast<int>(sizeof(T));
-    using W = std::conditional_t<BYTES == 16, uint4,
-                                 std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, T>>>;
-    alignas(BYTES) T e[VEC];
-    __device__ __forceinline__ void load(const T* p) { *reinterpret_cast<W*>(e) = *reinterpret_cast<const W*>(p); }
-    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<W*>(p) = *reinterpret_cast<const W*>(e); }
-};
-
-// Place of pair p's value in a token's table: the quads of an item's pairs lie a whole
-// row of items apart, so the threads of a quarter-warp read consecutive 16-byte words.
-template <int VEC>
-__device__ __forceinline__ int table_at(int pair, int items) {
-    if constexpr (VEC < 4) return pair;
-    return (((pair % VEC) >> 2) * items + pair / VEC) * 4 + (pair & 3);
-}
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
@@ -96,11 +65,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
             const int tok = i / half, pair = i - tok * half;
             const int pos = __ldcg(p.pos + static_cast<long long>(axis[pair]) * p.n + t0 + tok);
-            const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(pos)) * step[pair];
-            // half turns in [-1, 1): the wrapped angle over pi
-            const float x = __ll2float_rn(static_cast<long long>(turn)) * 1.0842021724855044e-19f;  // 2^-63
             float s, c;
-            sincospif(x, &s, &c);
+            turn_sincos(pos, step[pair], &s, &c);
             cs[buf][tok][table_at<VEC>(pair, items)] = c;
             sn[buf][tok][table_at<VEC>(pair, items)] = s;
         }
@@ -136,14 +102,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 }
                 turns = turns && i < turning;
                 int ea, eb;  // first elements of the item's two chunks
-                if (p.adjacent || !turns) {
-                    // neighbours; (halves) the elements behind the rotary part, or a value head's
-                    ea = 2 * i * VEC;
-                    eb = ea + VEC;
-                } else {
-                    ea = i * VEC;
-                    eb = half + i * VEC;
-                }
+                unit_at<VEC>(i, turning, half, p.adjacent || !turns, ea, eb);
                 tk[u] = tok;
                 it[u] = turns ? i : -1;
                 a[u].load(src + ea);
@@ -186,24 +145,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                                 *reinterpret_cast<const float4*>(&sn[buf][tk[u]][(h * items + it[u]) * 4]);
                         }
                     }
-                    if (p.adjacent) {
-                        // pair e: elements 2e and 2e + 1 of the item's 2 VEC
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            float& y0 = 2 * e < VEC ? xa[(2 * e) % VEC] : xb[(2 * e) % VEC];
-                            float& y1 = 2 * e + 1 < VEC ? xa[(2 * e + 1) % VEC] : xb[(2 * e + 1) % VEC];
-                            const float u0 = y0, u1 = y1;
-                            y0 = u0 * c[e] - u1 * s[e];
-                            y1 = u1 * c[e] + u0 * s[e];
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float u0 = xa[e], u1 = xb[e];
-                            xa[e] = u0 * c[e] - u1 * s[e];
-                            xb[e] = u1 * c[e] + u0 * s[e];
-                        }
-                    }
+                    turn_pairs<VEC>(xa, xb, c, s, p.adjacent);
                 }
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
@@ -236,20 +178,11 @@ cudaError_t launch_rope(RopeParams p, int vec, int sms, cudaStream_t stream) {
     // 22.1 / 37.6 -> 9.9 / 19.2 / 33.3 us; 40 + 2 x 40 fp32 heads, 200 / 600 / 1001 tokens 8.4 / 13.1 / 19.9 -> 7.5 / 10.1 / 20.3).
     // Calls with fewer tiles than SMs: their heads over enough blocks to reach every SM (at least
     // 8 heads each).
-    const int per_token = p.heads * (p.D / (2 * vec));
-    p.tile = kRopeTile;
-    while (p.tile > 1 && (p.tile * per_token > kRopeTileItems || p.n < 4LL * p.tile * sms)) p.tile >>= 1;
+    // (tiles against fewer tokens: 64 + 2 x 8 bf16 heads, 1200 / 2400 / 4000 tokens 11.2 / 22.1 / 37.6 -> 9.9 / 19.2 /
+    // 33.3 us; 40 + 2 x 40 fp32 heads, 200 / 600 / 1001 tokens 8.4 / 13.1 / 19.9 -> 7.5 / 10.1 / 20.3)
+    plan_rope(p, p.heads * (p.D / (2 * vec)), kRopeTile, kRopeTileItems, sms);
     const long long tiles = (p.n + p.tile - 1) / p.tile;
-    long long split = tiles >= sms ? 1 : sms / tiles;
-    p.heads_per_block = static_cast<int>((p.heads + split - 1) / split);
-    if (p.heads_per_block < 8) p.heads_per_block = p.heads < 8 ? p.heads : 8;
-    if (p.heads_per_block > 4096) p.heads_per_block = 4096;
     const int gy = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
-    // ceil(2^32 / H): hh / H as the high half of a product, exact for hh < tile * H <= 16 * 2^12
-    for (int last = 0; last < 2; ++last) {
-        const uint32_t h = static_cast<uint32_t>(last ? p.heads - (gy - 1) * p.heads_per_block : p.heads_per_block);
-        p.div_h[last] = h == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + h - 1) / h);
-    }
     const long long cap = static_cast<long long>(sms) * 8;
     const dim3 grid(static_cast<unsigned>(tiles < cap ? tiles : cap), static_cast<unsigned>(gy));
     void* args[] = {&p};

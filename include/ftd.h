@@ -329,7 +329,8 @@ ftd_status ftd_debug_late_lengths(const int32_t* src, int32_t* dst, int n, int d
 ftd_status ftd_debug_kernel(ftd_ctx* ctx, int entry, int* block_rows, int* tensor_cores);
 
 /*
- * Operators around the step: rotary positions before it, the step that also
+ * Operators around the step: rotary positions before it, alone or with norms of
+ * the heads, block tables and slot maps from request lengths, the step that also
  * accumulates attention weights, the eviction by those weights, and cross
  * attention.  They take the context's shapes, types and caches, follow the
  * conventions above, launch on the caller's stream without allocating or
@@ -386,6 +387,66 @@ ftd_status ftd_set_rope(ftd_ctx* ctx, const ftd_rope_config* cfg);
 ftd_status ftd_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,
                         int64_t kv_stride, const void* qkv_bias, const int32_t* positions, int64_t n_tokens,
                         void* q_out, void* k_out, void* v_out, void* stream);
+
+/*
+ * ftd_norm_rope_qkv -- ftd_rope_qkv with norms of the query and key heads ahead of the
+ * rotation, and with keys and values that may go straight into the cache.  For a query or
+ * key head x = in + bias whose kind has a weight w:
+ *   y_e = x_e / sqrt(mean over the head of x^2 + eps) * (w_e + weight_offset),
+ * then y turns as in ftd_rope_qkv (ftd_set_rope first); fp32 throughout, one rounding.
+ *   q, k, v, q_stride, kv_stride, qkv_bias, positions, n_tokens, q_out : as in ftd_rope_qkv.
+ *   q_weight, k_weight : device [D], qkv dtype, or NULL (no norm of that kind of head).
+ *   eps       : finite, >= 0.   weight_offset : 0, or 1 for weights kept around zero.
+ *   slots     : NULL: keys and values go to k_out, v_out as in ftd_rope_qkv, and the three
+ *               cache arguments are NULL.  Else device int32 [n_tokens], a token's place in
+ *               the cache: b * Lmax + position, on a paged context page * page_size + offset
+ *               (as ftd_build_tables makes them); negative: the token's keys and values go
+ *               nowhere.  v is needed, k_out and v_out are NULL.  Two tokens of one call must
+ *               not name one slot.
+ *   k_cache, v_cache, scales : as in ftd_decode_mha / _paged (NULL: the pool).  Rows are
+ *               rounded once from fp32 to the cache type; INT8 rows are codes and a scale
+ *               as ftd_decode_mha appends them.  Only the named rows are written.
+ * A slot past the cache's end writes nothing and raises FTD_ERR_BAD_PAGE.  Every row is the one
+ * that the step would append, where qkv and cache type are one.  Launches one kernel.
+ */
+ftd_status ftd_norm_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride, int64_t kv_stride,
+                             const void* qkv_bias, const void* q_weight, const void* k_weight, float eps, float weight_offset,
+                             const int32_t* positions, int64_t n_tokens, void* q_out, void* k_out, void* v_out,
+                             const int32_t* slots, void* k_cache, void* v_cache, float* scales, void* stream);
+
+/*
+ * ftd_build_tables -- block tables and slot maps from request lengths: brings every slot
+ * from old_lens[b] to new_lens[b] cached rows (negative: inactive, no rows), by the pages
+ * of a free list, and says where the rows between go.
+ *   old_lens, new_lens : device int32 [B].  A slot grows, shrinks (an eviction, rejected
+ *               tokens), begins (old <= 0) or ends (new <= 0).
+ *   served    : device int32 [B], may be either list: new_lens[b], or old_lens[b] where the
+ *               slot was not served: a length above Lmax (FTD_ERR_SEQ_OVERFLOW), or too few
+ *               pages left.  The latter is no error; the slot keeps its pages and can ask
+ *               again.  Slots are served in order: once one has to wait, so do all later
+ *               ones that ask for pages.
+ *   block_table : device int32 [B][ceil(Lmax / page_size)]: the first ceil(old_lens[b] /
+ *               page_size) entries of a slot are its pages; entries for its new rows are
+ *               written, no others.
+ *   free_pages, n_free : device int32 [num_pages] and [1]: a stack, its top at n_free - 1.
+ *               Entries that slots give back are pushed in (slot, entry) order, then those
+ *               asked for are popped in that order, so pages given back are used again first.
+ *   n_free_out : device int32 [1], NULL or n_free: in place.
+ *   offsets   : device int32 [B + 1] or NULL: new tokens of the slots before b, packed.
+ *   slots     : device int32 [max_tokens] or NULL: for each new token, in packed order, its
+ *               place in the cache as ftd_norm_rope_qkv takes it; -1 from offsets[B] on.
+ *   positions : device int32 [max_tokens] or NULL: its position; 0 from offsets[B] on.
+ *               More than max_tokens new tokens raise FTD_ERR_SEQ_OVERFLOW, and those past
+ *               it are left out of both lists.
+ * On a contiguous context block_table, free_pages, n_free and n_free_out are NULL.  A page
+ * outside [0, num_pages) that changes hands or holds a new token raises FTD_ERR_BAD_PAGE (its
+ * tokens get -1), and so do an n_free outside [0, num_pages] and pages given back that the
+ * list has no room for.  Other overlaps of outputs are refused.  Launches one kernel, whose
+ * result does not depend on the order of anything.
+ */
+ftd_status ftd_build_tables(ftd_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, int32_t* served, int32_t* block_table,
+                            int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, int32_t* offsets, int32_t* slots,
+                            int32_t* positions, int64_t max_tokens, void* stream);
 
 /*
  * ftd_enable_scores -- allocate the workspace of ftd_decode_mha_scored and
