@@ -37,7 +37,8 @@ EXPORTS = ("ftd_init", "ftd_cache_ptrs", "ftd_decode_mha", "ftd_decode_mha_curre
            "ftd_decode_mha_host", "ftd_get_error", "ftd_destroy", "ftd_status_str", "ftd_last_error",
            "ftd_kernel_launches", "ftd_decode_mha_noalloc", "ftd_debug_stall_next",
            "ftd_debug_late_lengths", "ftd_debug_kernel", "ftd_decode_mha_proj", "ftd_set_rope", "ftd_rope_qkv", "ftd_enable_scores",
-           "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha", "ftd_norm_rope_qkv", "ftd_build_tables")
+           "ftd_decode_mha_scored", "ftd_cache_evict", "ftd_cross_mha", "ftd_norm_rope_qkv", "ftd_build_tables",
+           "ftd_enable_prefix", "ftd_decode_mha_prefix")
 
 
 class FtdConfig(ctypes.Structure):
@@ -114,6 +115,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ftd_norm_rope_qkv.restype = I
     lib.ftd_build_tables.argtypes = [P] * 11 + [ctypes.c_int64, P]
     lib.ftd_build_tables.restype = I
+    lib.ftd_enable_prefix.argtypes = [P, P]
+    lib.ftd_enable_prefix.restype = I
+    lib.ftd_decode_mha_prefix.argtypes = [P] * 14 + [ctypes.c_int64] + [P] * 3
+    lib.ftd_decode_mha_prefix.restype = I
     lib.ftd_enable_scores.argtypes = [P, P]
     lib.ftd_enable_scores.restype = I
     lib.ftd_decode_mha_scored.argtypes = [P] * 16
@@ -207,6 +212,17 @@ def ftd_build_tables(ctx, old_lens, new_lens, served, block_table, free_pages, n
                      max_tokens, stream) -> int:
     return load_library().ftd_build_tables(ctx, old_lens, new_lens, served, block_table, free_pages, n_free, n_free_out,
                                            offsets, slots, positions, max_tokens, stream)
+
+
+def ftd_enable_prefix(ctx, stream) -> int:
+    return load_library().ftd_enable_prefix(ctx, stream)
+
+
+def ftd_decode_mha_prefix(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, k_prefix, v_prefix,
+                          prefix_scales, prefix_table, prefix_rows, prefix_lens, out, stream) -> int:
+    return load_library().ftd_decode_mha_prefix(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens,
+                                                scales, k_prefix, v_prefix, prefix_scales, prefix_table, prefix_rows,
+                                                prefix_lens, out, stream)
 
 
 def ftd_enable_scores(ctx, stream) -> int:
@@ -574,6 +590,47 @@ class DecodeStep:
         st = ftd_build_tables(self.ctx, old_lens.data_ptr(), new_lens.data_ptr(), served.data_ptr(), _ptr(block_table),
                               _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(offsets), _ptr(slots), _ptr(positions),
                               n, s)
+        if st:
+            check(st)
+
+    def enable_prefix(self, stream: Optional[int] = None):
+        """Allocate what ``prefix`` needs."""
+        check(ftd_enable_prefix(self.ctx, _current_stream(self.device) if stream is None else stream))
+
+    def _prefix_rows(self, k_prefix, v_prefix, prefix_scales, prefix_table):
+        """Rows of the prefix by its tensors, which have to agree."""
+        d, hkv = self._widths[2], self.cfg.n_kv_heads
+        if self.cfg.page_size:
+            if prefix_table is None:
+                return 0
+            _expect("prefix_table", prefix_table, 0, dtype=self._int32, tail=prefix_table.shape)
+            return prefix_table.numel() * self.cfg.page_size
+        if k_prefix is None or v_prefix is None:
+            if k_prefix is not v_prefix:
+                raise ValueError("k_prefix and v_prefix come together")
+            return 0
+        rows = k_prefix.numel() // (hkv * d)
+        for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+            if t.numel() != rows * hkv * d or t.element_size() != self._cache_bytes or not t.is_contiguous() or (
+                    t.dim() > 1 and (t.shape[-1] != d or t.dim() > 2 and t.shape[-2] != rows)):
+                raise ValueError(f"{name} has to be a contiguous [{hkv}, rows, {d}] of the cache type, one shape for both")
+        if prefix_scales is not None:
+            _expect("prefix_scales", prefix_scales, 2 * hkv * rows, dtype=self._float32, tail=(hkv, rows))
+        return rows
+
+    def prefix(self, q, k_new, v_new, seq_lens, prefix_lens, out, k_prefix=None, v_prefix=None, prefix_scales=None,
+               prefix_table=None, bias=None, k_cache=None, v_cache=None, scales=None, block_table=None,
+               stream: Optional[int] = None):
+        """The step of slots that share a prefix: slot b sees its first prefix_lens[b] rows and its own.  The prefix
+        is [n_kv_heads, rows, head_dim] (INT8: and scales [2, n_kv_heads, rows]), or the pool's pages that
+        ``prefix_table`` names.  After ``enable_prefix``."""
+        self._check_planes((seq_lens, prefix_lens), table=block_table)
+        rows = self._prefix_rows(k_prefix, v_prefix, prefix_scales, prefix_table)
+        s = _current_stream(self.device) if stream is None else stream
+        st = ftd_decode_mha_prefix(self.ctx, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _ptr(bias), _ptr(k_cache),
+                                   _ptr(v_cache), _ptr(block_table), seq_lens.data_ptr(), _ptr(scales), _ptr(k_prefix),
+                                   _ptr(v_prefix), _ptr(prefix_scales), _ptr(prefix_table), rows, prefix_lens.data_ptr(),
+                                   out.data_ptr(), s)
         if st:
             check(st)
 

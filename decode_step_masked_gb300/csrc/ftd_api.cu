@@ -25,6 +25,7 @@
 #include "ftd_decode_wide_tc.cuh"
 #include "ftd_ops.cuh"
 #include "ftd_out_proj.cuh"
+#include "ftd_prefix.cuh"
 
 namespace {
 
@@ -415,6 +416,13 @@ struct ftd_ctx {
     int2* moves = nullptr;
     int2* local_moves = nullptr;
     uint32_t* evict_count = nullptr;
+    // ftd_enable_prefix: kernel and workspace of ftd_decode_mha_prefix
+    void* pre_pool = nullptr;
+    ftd::PrefixKernel pre{};
+    float* pre_own = nullptr;     // [B][T][Hq][D] the step's fp32 output
+    float2* pre_ml = nullptr;     // and its rows' statistics
+    float* pre_ws = nullptr;      // partials over the prefix
+    int2* pre_info = nullptr;
     // ftd_set_rope
     bool rope_set = false;
     ftd::RopeParams rope{};
@@ -624,7 +632,7 @@ static cudaError_t launch_overlapped(const void* fn, int grid, int threads, int 
 static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
                                 const void* bias, void* k_cache, void* v_cache, const int32_t* block_table,
                                 const int32_t* seq_lens, float* scales, void* out, cudaStream_t stream,
-                                bool proj = false, int mode = ftd::kStep) {
+                                bool proj = false, int mode = ftd::kStep, float2* stats = nullptr) {
     if (!k_cache) k_cache = ctx->k_cache;
     if (!v_cache) v_cache = ctx->v_cache;
     const bool i8 = ctx->cfg.cache_dtype == FTD_I8;
@@ -660,7 +668,8 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     p.nhb = ctx->nhb;
     p.qkv_dtype = static_cast<int>(c.qkv_dtype);
     p.qscale = ctx->qscale;
-    p.out_dtype = static_cast<int>(c.out_dtype);
+    p.out_dtype = stats ? ftd::kF32 : static_cast<int>(c.out_dtype);
+    p.stats = stats;
     p.window = c.window;
     p.nq = ctx->nq;
     p.block_table = ctx->paged ? block_table : nullptr;
@@ -915,6 +924,7 @@ void ftd_destroy(ftd_ctx* ctx) {
             }
     }
     cudaDeviceSynchronize();
+    cudaFree(ctx->pre_pool);
     cudaFree(ctx->sc_pool);
     cudaFree(ctx->pool);
     delete ctx;
@@ -1475,6 +1485,132 @@ ftd_status ftd_build_tables(ftd_ctx* ctx, const int32_t* old_lens, const int32_t
     if (e != cudaSuccess) return cuda_fail(e, "tables kernel launch");
     g_launches.fetch_add(1);
     ctx->last_stream = static_cast<cudaStream_t>(stream);
+    return FTD_OK;
+}
+
+ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
+    static const char* const what = "ftd_enable_prefix";
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "%s: ctx is NULL", what);
+    if (ctx->pre_pool) return FTD_OK;
+    const ftd_config& c = ctx->cfg;
+    if (c.window > 0) return fail(FTD_ERR_INVALID_ARG, "%s: a shared prefix and a sliding window exclude each other", what);
+    const size_t B = c.max_batch, T = ctx->nq, Hq = c.n_q_heads, Hkv = c.n_kv_heads, D = c.head_dim;
+    const size_t R = B * T * (Hq / Hkv);
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    const ftd::PrefixKernel k = ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
+    const size_t blocks = (R + k.block_rows - 1) / k.block_rows;
+    if (R > 65536 || blocks > ftd::kMaxRowBlocks)
+        return fail(FTD_ERR_UNSUPPORTED, "%s: %zu query rows per kv head, at most 65536", what, R);
+    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (shared prefix)");
+    size_t off = 0;
+    auto carve = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    };
+    const size_t o_own = carve(B * T * Hq * D * sizeof(float)), o_ml = carve(Hkv * R * sizeof(float2));
+    const size_t o_info = carve(Hkv * blocks * sizeof(int2));
+    const size_t o_ws = carve((Hkv * blocks + ctx->grid) * ftd::prefix_slot_floats(k.block_rows, c.head_dim) * sizeof(float));
+    void* pool = nullptr;
+    e = cudaMalloc(&pool, off);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "cudaMalloc of the prefix workspace");
+    }
+    unsigned char* base = static_cast<unsigned char*>(pool);
+    ctx->pre_pool = pool;
+    ctx->pre = k;
+    ctx->pre_own = reinterpret_cast<float*>(base + o_own);
+    ctx->pre_ml = reinterpret_cast<float2*>(base + o_ml);
+    ctx->pre_info = reinterpret_cast<int2*>(base + o_info);
+    ctx->pre_ws = reinterpret_cast<float*>(base + o_ws);
+    (void)stream;
+    return FTD_OK;
+}
+
+ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new, const void* qkv_bias,
+                                 void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
+                                 float* scales, const void* k_prefix, const void* v_prefix, const float* prefix_scales,
+                                 const int32_t* prefix_table, int64_t prefix_rows, const int32_t* prefix_lens, void* out,
+                                 void* stream) {
+    static const char* const what = "ftd_decode_mha_prefix";
+    g_last_error.clear();
+    if (!ctx) return fail(FTD_ERR_INVALID_ARG, "%s: ctx is NULL", what);
+    if (!ctx->pre_pool) return fail(FTD_ERR_INVALID_ARG, "%s: ftd_enable_prefix first", what);
+    const ftd_config& c = ctx->cfg;
+    const bool i8 = c.cache_dtype == FTD_I8;
+    ftd_status st = check_table(ctx, block_table, what);
+    if (st != FTD_OK) return st;
+    if (prefix_rows < 0 || prefix_rows * c.n_kv_heads >= (static_cast<int64_t>(1) << 31) || prefix_rows >= (static_cast<int64_t>(1) << 31))
+        return fail(FTD_ERR_INVALID_ARG, "%s: prefix_rows %lld", what, static_cast<long long>(prefix_rows));
+    if (!prefix_lens || !aligned(prefix_lens, 4) || !out || !aligned16(out))
+        return fail(FTD_ERR_INVALID_ARG, "%s: prefix_lens (4-byte aligned) and out (16-byte aligned) must be non-NULL", what);
+    if (ctx->paged) {
+        if (k_prefix || v_prefix || prefix_scales)
+            return fail(FTD_ERR_INVALID_ARG, "%s: on a paged context the prefix lies in the pool's pages (k_prefix, v_prefix and prefix_scales NULL)", what);
+        if (prefix_rows > 0 && (!prefix_table || !aligned(prefix_table, 4)))
+            return fail(FTD_ERR_INVALID_ARG, "%s: a paged context needs a 4-byte aligned prefix_table", what);
+    } else {
+        if (prefix_table) return fail(FTD_ERR_INVALID_ARG, "%s: a contiguous context takes no prefix_table", what);
+        if (prefix_rows > 0 && (!k_prefix || !v_prefix || (i8 && !prefix_scales)))
+            return fail(FTD_ERR_INVALID_ARG, "%s: k_prefix and v_prefix (INT8: and prefix_scales) must be non-NULL", what);
+        if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned(prefix_scales, 4))
+            return fail(FTD_ERR_INVALID_ARG, "%s: k_prefix and v_prefix must be 16-byte aligned", what);
+    }
+    DeviceScope dev(ctx->device);
+    if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // The slots' own rows by the step's kernel, into the workspace, beside the prefix (nothing to share: straight to out).
+    if (prefix_rows == 0)
+        return launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, out, s);
+    st = launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, ctx->pre_own, s, false,
+                       ftd::kStep, ctx->pre_ml);
+    if (st != FTD_OK) return st;
+    ftd::PrefixParams p{};
+    p.q = q;
+    p.bias = qkv_bias;
+    p.k = static_cast<const unsigned char*>(ctx->paged ? (k_cache ? k_cache : ctx->k_cache) : k_prefix);
+    p.v = static_cast<const unsigned char*>(ctx->paged ? (v_cache ? v_cache : ctx->v_cache) : v_prefix);
+    const float* sc = ctx->paged ? (scales ? scales : ctx->scales) : prefix_scales;
+    p.k_scales = i8 ? sc : nullptr;
+    p.v_scales = i8 ? sc + (ctx->paged ? ctx->rows : static_cast<size_t>(prefix_rows) * c.n_kv_heads) : nullptr;
+    p.table = ctx->paged ? prefix_table : nullptr;
+    p.prefix_lens = prefix_lens;
+    p.seq_lens = seq_lens;
+    p.ws = ctx->pre_ws;
+    p.seg_info = ctx->pre_info;
+    p.err = ctx->err;
+    p.own_o = ctx->pre_own;
+    p.own_ml = ctx->pre_ml;
+    p.out = out;
+    p.out_dtype = static_cast<int>(c.out_dtype);
+    p.B = c.max_batch;
+    p.T = ctx->nq;
+    p.Hq = c.n_q_heads;
+    p.Hkv = c.n_kv_heads;
+    p.group = c.n_q_heads / c.n_kv_heads;
+    p.D = c.head_dim;
+    p.Lmax = c.max_len;
+    p.P = static_cast<int>(prefix_rows);
+    p.R = p.B * p.T * p.group;
+    p.block_rows = ctx->pre.block_rows;
+    p.row_blocks = (p.R + p.block_rows - 1) / p.block_rows;
+    p.workers = ctx->grid;
+    p.qkv_dtype = static_cast<int>(c.qkv_dtype);
+    p.qscale = ctx->qscale;
+    p.page_shift = page_shift_of(ctx);
+    p.num_pages = c.num_pages;
+    p.wait_cycles = ctx->wait_cycles;
+    void* args[] = {&p};
+    cudaError_t e = launch_overlapped(ctx->pre.fn, ctx->grid, ctx->pre.threads, ctx->pre.smem, args, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
+    g_launches.fetch_add(1);
+    e = ftd::launch_prefix_join(p, ctx->pre.split, s);
+    if (e != cudaSuccess) return cuda_fail(e, "join kernel launch");
+    g_launches.fetch_add(1);
     return FTD_OK;
 }
 

@@ -73,6 +73,8 @@ struct DecodeParams {
     void* proj_hi;          // nullptr: no projection
     void* proj_lo;
     int proj_dt;
+    // kStep with stats: each query row's (m, 1 / sum of 2^(s - m)) beside its output, laid out as for kScored,
+    // for the join with a shared prefix (ftd_prefix.cu).
     // kScored: the scores of query row qi of (b, kv head) at [((b * Hkv + kvh) * nq * group + qi) * Lmax + position],
     // in the log2 domain, and the row's (reference m, 1 / sum of 2^(s - m)).  There qscale is the
     // power of two below the softmax scale and the scores are multiplied by the rest, sscale: a
@@ -103,16 +105,23 @@ __device__ __forceinline__ int cached_rows(int L) {
     return L;
 }
 // Scale of an INT8 row from its largest magnitude (0: 1).  The step divides by 127; the scored
-// step multiplies by the fp32 value of 1 / 127, within an ulp of that.
+// step and the step beside a shared prefix multiply by the fp32 value of 1 / 127, within an ulp of that.
 template <int MODE>
-__device__ __forceinline__ float i8_row_scale(float amax) {
+__device__ __forceinline__ float i8_row_scale(const DecodeParams& p, float amax) {
     if (amax == 0.f) return 1.f;
-    if constexpr (MODE == kScored) return amax * (1.f / 127.f);
+    if (MODE == kScored || (MODE == kStep && p.stats)) return amax * (1.f / 127.f);
     return __fdiv_rn(amax, 127.f);
 }
-// kScored: index of the score and statistics row of query row qi of (b, kvh).
+// Index of the score (kScored) and statistics row of query row qi of (b, kvh).
 __device__ __forceinline__ size_t score_row(const DecodeParams& p, int b, int kvh, int qi) {
     return (static_cast<size_t>(b) * p.Hkv + kvh) * (p.nq * p.group) + qi;
+}
+
+// Whether a row's softmax statistics are stored: by the scored step always, by the step when asked to.
+template <int MODE>
+__device__ __forceinline__ bool keeps_stats(const DecodeParams& p) {
+    if constexpr (MODE == kStep) return p.stats != nullptr;
+    return MODE == kScored;
 }
 
 // First visible position of a slot with L cached tokens (the window start).

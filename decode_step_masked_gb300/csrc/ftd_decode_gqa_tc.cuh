@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             amax = fmaxf(amax, fabsf(x[e]));
                         }
                         amax = warp_max(amax);
-                        const float qs = i8_row_scale<MODE>(amax);
+                        const float qs = i8_row_scale<MODE>(p, amax);
                         uint32_t w = 0u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -1279,6 +1279,8 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         for (int jj = 0; jj < GH; ++jj)
                             if (c0 + jj < QB) {
                                 store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r, o[jj] / lt[jj]);
+                                if (keeps_stats<MODE>(p) && r == 0)
+                                    p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] = make_float2(m[jj], 1.f / lt[jj]);
                             }
                         }
                     } else {
@@ -1373,10 +1375,9 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                 if (c0 + jj < QB && (BOXES > 1 || r < D)) {
                                     store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r,
                                                Ac[jj] / Ls_[jj]);
-                                    if constexpr (MODE == kScored)
-                                        if (r == 0)
-                                            p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] =
-                                                make_float2(Mx[jj], 1.f / Ls_[jj]);
+                                    if (keeps_stats<MODE>(p) && r == 0)
+                                        p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] =
+                                            make_float2(Mx[jj], 1.f / Ls_[jj]);
                                 }
                             if (leader) p.counters[segg] = 0u;
                         }

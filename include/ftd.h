@@ -331,8 +331,8 @@ ftd_status ftd_debug_kernel(ftd_ctx* ctx, int entry, int* block_rows, int* tenso
 /*
  * Operators around the step: rotary positions before it, alone or with norms of
  * the heads, block tables and slot maps from request lengths, the step that also
- * accumulates attention weights, the eviction by those weights, and cross
- * attention.  They take the context's shapes, types and caches, follow the
+ * accumulates attention weights, the eviction by those weights, cross attention, and
+ * the step of slots that share a prefix.  They take the context's shapes, types and caches, follow the
  * conventions above, launch on the caller's stream without allocating or
  * synchronising, and may be captured into a graph (after one call of
  * ftd_enable_scores, and of ftd_cross_mha, outside the capture).  Calls on one
@@ -537,6 +537,47 @@ ftd_status ftd_cache_evict(ftd_ctx* ctx, void* k_cache, void* v_cache, float* sc
  */
 ftd_status ftd_cross_mha(ftd_ctx* ctx, const void* q, const void* q_bias, const void* k_mem, const void* v_mem,
                          const int32_t* mem_lens, const float* scales, void* out, void* stream);
+
+/*
+ * ftd_enable_prefix -- allocate the workspace of ftd_decode_mha_prefix: an fp32 copy of
+ * out, two numbers per query row, and one partial block per SM and per kv head and block of query
+ * rows.  One cudaMalloc, freed by ftd_destroy.  A second call does nothing.  UNSUPPORTED
+ * above 65536 query rows per kv head (B * T * Hq / Hkv), INVALID_ARG with a window.
+ */
+ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
+
+/*
+ * ftd_decode_mha_prefix -- the step of ftd_decode_mha (of ftd_decode_mha_paged on a paged
+ * context) for slots that share a long prefix, as the samples of one question or the chats
+ * behind one system prompt do: slot b's tokens attend to the first prefix_lens[b] rows
+ * of the prefix and to the slot's own rows, those of its cache and the new ones,
+ *   out[b][j][h] = softmax over both of scale * q'[b][j][h] . K, times V.
+ * The prefix is read once for all slots: with B slots its products are matrix products
+ * with B * T * Hq / Hkv rows, which fp16 and bf16 caches make on the tensor cores.
+ *   k_prefix, v_prefix : device [Hkv][prefix_rows][D] of the cache dtype, 16-byte aligned, read
+ *               only; INT8 with prefix_scales, device fp32 [2][Hkv][prefix_rows].  On a
+ *               paged context NULL: the prefix lies in pages of the pool, and
+ *   prefix_table : device int32 [ceil(prefix_rows / page_size)] names them (NULL on a
+ *               contiguous context).  No slot's block table may have them in reach of a
+ *               new row.
+ *   prefix_rows : rows of the prefix, >= 0; 0: ftd_decode_mha's call.
+ *   prefix_lens : device int32 [B].  A slot that shares nothing has 0 (or less); one above
+ *               prefix_rows sees prefix_rows and raises FTD_ERR_SEQ_OVERFLOW.
+ * seq_lens counts the slot's own rows: 0 as long as it has only the prefix.  Keys carry their
+ * positions already, so the slot's own rows start wherever the caller turned them to.
+ * Rows of the prefix from the longest prefix_lens on may hold anything; rows that some slot
+ * sees hold finite values.
+ * Other arguments, out, the appended rows (an INT8 row's scale as in ftd_decode_mha_scored) and
+ * the sticky errors as in ftd_decode_mha; a page of the prefix outside [0, num_pages) raises
+ * FTD_ERR_BAD_PAGE, and what the slots see of it is undefined.  Where out is a 16-bit type and q fits the cache's (one 16-bit type, no bias), the tensor
+ * cores take q and the weights over the prefix rounded to that type; else each as a pair of
+ * numbers of it (about 16 mantissa bits with bf16).  Launches three kernels.
+ */
+ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new, const void* qkv_bias,
+                                 void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
+                                 float* scales, const void* k_prefix, const void* v_prefix, const float* prefix_scales,
+                                 const int32_t* prefix_table, int64_t prefix_rows, const int32_t* prefix_lens, void* out,
+                                 void* stream);
 
 /* Size of the fixed device array that ftd_decode_mha_noalloc uses as scratch. */
 #define FTD_NOALLOC_SCRATCH_BYTES (8u << 20)
