@@ -26,6 +26,7 @@
 #include "ftd_ops.cuh"
 #include "ftd_out_proj.cuh"
 #include "ftd_prefix.cuh"
+#include "ftd_prefix_tc.cuh"
 
 namespace {
 
@@ -418,7 +419,13 @@ struct ftd_ctx {
     uint32_t* evict_count = nullptr;
     // ftd_enable_prefix: kernel and workspace of ftd_decode_mha_prefix
     void* pre_pool = nullptr;
-    ftd::PrefixKernel pre{};
+    ftd::PrefixKernel pre[2];     // [1]: q and the weights as pairs (the same on CUDA cores)
+    bool pre_tc = false;
+    CUtensorMap tmpk;
+    CUtensorMap tmpv;
+    const void* tm_pk_base = nullptr;
+    const void* tm_pv_base = nullptr;
+    size_t tm_p_rows = 0;
     float* pre_own = nullptr;     // [B][T][Hq][D] the step's fp32 output
     float2* pre_ml = nullptr;     // and its rows' statistics
     float* pre_ws = nullptr;      // partials over the prefix
@@ -1499,12 +1506,22 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     const size_t R = B * T * (Hq / Hkv);
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
-    const ftd::PrefixKernel k = ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
-    const size_t blocks = (R + k.block_rows - 1) / k.block_rows;
-    if (R > 65536 || blocks > ftd::kMaxRowBlocks)
-        return fail(FTD_ERR_UNSUPPORTED, "%s: %zu query rows per kv head, at most 65536", what, R);
-    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (shared prefix)");
+    // fp16 and bf16 caches on the tensor cores
+    const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
+    const bool tc = half && c.kernel != FTD_KERNEL_CUDA_CORE && encode_tiled();
+    if (R > 32768) return fail(FTD_ERR_UNSUPPORTED, "%s: %zu query rows per kv head, at most 32768", what, R);
+    ftd::PrefixKernel k[2];
+    size_t blocks = 0, ws = 0;
+    for (int i = 0; i < 2; ++i) {
+        k[i] = tc ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i == 1)
+                  : ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
+        const size_t n = (R + k[i].block_rows - 1) / k[i].block_rows;
+        const size_t floats = (Hkv * n + ctx->grid) * ftd::prefix_slot_floats(k[i].slot_rows, c.head_dim);
+        if (n > blocks) blocks = n;
+        if (floats > ws) ws = floats;
+        const cudaError_t e = cudaFuncSetAttribute(k[i].fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k[i].smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (shared prefix)");
+    }
     size_t off = 0;
     auto carve = [&](size_t bytes) {
         const size_t o = off;
@@ -1513,16 +1530,18 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     };
     const size_t o_own = carve(B * T * Hq * D * sizeof(float)), o_ml = carve(Hkv * R * sizeof(float2));
     const size_t o_info = carve(Hkv * blocks * sizeof(int2));
-    const size_t o_ws = carve((Hkv * blocks + ctx->grid) * ftd::prefix_slot_floats(k.block_rows, c.head_dim) * sizeof(float));
+    const size_t o_ws = carve(ws * sizeof(float));
     void* pool = nullptr;
-    e = cudaMalloc(&pool, off);
+    const cudaError_t e = cudaMalloc(&pool, off);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail(e, "cudaMalloc of the prefix workspace");
     }
     unsigned char* base = static_cast<unsigned char*>(pool);
     ctx->pre_pool = pool;
-    ctx->pre = k;
+    ctx->pre[0] = k[0];
+    ctx->pre[1] = k[1];
+    ctx->pre_tc = tc;
     ctx->pre_own = reinterpret_cast<float*>(base + o_own);
     ctx->pre_ml = reinterpret_cast<float2*>(base + o_ml);
     ctx->pre_info = reinterpret_cast<int2*>(base + o_info);
@@ -1563,6 +1582,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool stall = ctx->stall_calls > 0;  // (the step's launch takes one)
     // The slots' own rows by the step's kernel, into the workspace, beside the prefix (nothing to share: straight to out).
     if (prefix_rows == 0)
         return launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, out, s);
@@ -1596,7 +1616,12 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.Lmax = c.max_len;
     p.P = static_cast<int>(prefix_rows);
     p.R = p.B * p.T * p.group;
-    p.block_rows = ctx->pre.block_rows;
+    // q and the weights in one 16-bit number each where q is one and out keeps no more, else in two
+    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 || qkv_bias || c.qkv_dtype != c.cache_dtype];
+    p.block_rows = k.block_rows;
+    p.slot_rows = k.slot_rows;
+    p.split = k.split;
+    p.stall = stall;
     p.row_blocks = (p.R + p.block_rows - 1) / p.block_rows;
     p.workers = ctx->grid;
     p.qkv_dtype = static_cast<int>(c.qkv_dtype);
@@ -1604,11 +1629,27 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.page_shift = page_shift_of(ctx);
     p.num_pages = c.num_pages;
     p.wait_cycles = ctx->wait_cycles;
-    void* args[] = {&p};
-    cudaError_t e = launch_overlapped(ctx->pre.fn, ctx->grid, ctx->pre.threads, ctx->pre.smem, args, s);
+    cudaError_t e;
+    if (ctx->pre_tc) {
+        const size_t rows = ctx->paged ? ctx->rows : static_cast<size_t>(prefix_rows) * c.n_kv_heads;
+        if (ctx->tm_pk_base != p.k || ctx->tm_pv_base != p.v || ctx->tm_p_rows != rows) {
+            ctx->tm_p_rows = 0;
+            if (!encode_cache_map(&ctx->tmpk, const_cast<unsigned char*>(p.k), c.cache_dtype, rows, c.head_dim) ||
+                !encode_cache_map(&ctx->tmpv, const_cast<unsigned char*>(p.v), c.cache_dtype, rows, c.head_dim))
+                return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the prefix");
+            ctx->tm_pk_base = p.k;
+            ctx->tm_pv_base = p.v;
+            ctx->tm_p_rows = rows;
+        }
+        void* args[] = {&ctx->tmpk, &ctx->tmpv, &p};
+        e = launch_overlapped(k.fn, ctx->grid, k.threads, k.smem, args, s);
+    } else {
+        void* args[] = {&p};
+        e = launch_overlapped(k.fn, ctx->grid, k.threads, k.smem, args, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
     g_launches.fetch_add(1);
-    e = ftd::launch_prefix_join(p, ctx->pre.split, s);
+    e = ftd::launch_prefix_join(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "join kernel launch");
     g_launches.fetch_add(1);
     return FTD_OK;

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kCcThreads, 1) prefix_cc_kernel(const PrefixPa
 // and leave as rows.
 constexpr int kJoinRows = 32, kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p, bool split) {
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p) {
     constexpr int N = D / 8;  // outputs of a thread
     __shared__ float acc_s[kJoinRows][D + 1];
     __shared__ float M_s[kJoinRows], S_s[kJoinRows];
@@ -276,10 +276,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
     grid_dep_wait();
     grid_dep_launch();
     const int rb = row0 / p.block_rows;
-    const bool twice = prefix_twice(p.R, p.block_rows, rb, split);
-    const int half = p.block_rows / 2, r = row0 - rb * p.block_rows + lane;
+    const bool twice = prefix_twice(p, rb);
+    const int half = p.slot_rows / 2, r = row0 - rb * p.block_rows + lane;
     const int2 range = __ldcg(p.seg_info + h * p.row_blocks + rb);
-    const size_t stride = prefix_slot_floats(p.block_rows, D);
+    const size_t stride = prefix_slot_floats(p.slot_rows, D);
     const float* slot = p.ws + static_cast<size_t>(h * p.row_blocks + rb + range.x) * stride;
     const int n = r < p.block_rows ? (range.y - range.x + 1) * (twice ? 2 : 1) : 0;
     float M = kNone, S = 0.f, acc[N];
@@ -288,10 +288,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
 #pragma unroll 2
     for (int k = 0; k < n; ++k) {
         const float* s = slot + (twice ? k >> 1 : k) * stride + (twice ? r + (k & 1) * half : r);
-        const float mk = __ldcg(s), lk = __ldcg(s + p.block_rows);
+        const float mk = __ldcg(s), lk = __ldcg(s + p.slot_rows);
         float o[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = __ldcg(s + (2 + d0 + e) * p.block_rows);
+        for (int e = 0; e < N; ++e) o[e] = __ldcg(s + (2 + d0 + e) * p.slot_rows);
         if (lk == 0.f && mk <= kNone) continue;  // a piece that the row saw nothing of
         const float mn = fmaxf(M, mk), a = exp2f(M - mn), f = exp2f(mk - mn);
         S = S * a + lk * f;
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
 template <typename CT, int D>
 PrefixKernel pick_cc(int R) {
     if (R <= 32)
-        return {reinterpret_cast<const void*>(&prefix_cc_kernel<CT, D, 16>), CcLayout<CT, D, 16>::SMEM, kCcThreads, 16, false};
-    return {reinterpret_cast<const void*>(&prefix_cc_kernel<CT, D, 64>), CcLayout<CT, D, 64>::SMEM, kCcThreads, 64, false};
+        return {reinterpret_cast<const void*>(&prefix_cc_kernel<CT, D, 16>), CcLayout<CT, D, 16>::SMEM, kCcThreads, 16, 16, false};
+    return {reinterpret_cast<const void*>(&prefix_cc_kernel<CT, D, 64>), CcLayout<CT, D, 64>::SMEM, kCcThreads, 64, 64, false};
 }
 
 }  // namespace
@@ -345,10 +345,10 @@ PrefixKernel select_prefix_cc(int cache_dt, int D, int R) {
     }
 }
 
-cudaError_t launch_prefix_join(PrefixParams p, bool split, cudaStream_t stream) {
+cudaError_t launch_prefix_join(PrefixParams p, cudaStream_t stream) {
     const int per = p.block_rows < kJoinRows ? p.block_rows : kJoinRows;  // rows of a block
     const dim3 grid(static_cast<unsigned>((p.R + per - 1) / per) * static_cast<unsigned>(p.Hkv));
-    void* args[] = {&p, &split};
+    void* args[] = {&p};
     const void* fn = p.D == 64 ? reinterpret_cast<const void*>(&prefix_join_kernel<64>)
                                : reinterpret_cast<const void*>(&prefix_join_kernel<128>);
     return launch_pdl(fn, grid, kJoinThreads, 0, args, stream);

@@ -46,6 +46,9 @@ struct PrefixParams {
     int P;                // rows of the prefix's buffer
     int R;                // query rows of a kv head: B * T * group
     int row_blocks, block_rows;  // row blocks of a kv head, and rows of a block
+    int slot_rows;        // query rows of a partial slot
+    bool split;           // the kernel runs two streams of half a slot's rows (prefix_twice)
+    int stall;            // test hook: block 0's first copy never comes (see ftd_debug_stall_next)
     int workers;          // blocks of the grid
     int qkv_dtype;
     float qscale;         // softmax scale * log2(e)
@@ -53,15 +56,15 @@ struct PrefixParams {
     long long wait_cycles;
 };
 
-// A partial slot of the workspace: m of the block's rows, their l, then D rows of outputs with the query rows side by
-// side, as a thread that owns a query row writes them and as the join reads them.  A block of at most half the
-// rows (in the tensor-core kernel) is held twice: each half of the rows is one of the block's two streams.
-__host__ __device__ inline size_t prefix_slot_floats(int block_rows, int D) {
-    return static_cast<size_t>(block_rows) * (2 + D);
+// A partial slot of the workspace, of slot_rows rows: their m, their l, then D rows of outputs with the query rows
+// side by side, as a thread that owns a query row writes them and as the join reads them.  A block of at most half a
+// slot's rows (in the tensor-core kernel) is held twice: each half of the slot is one of the block's two streams.
+__host__ __device__ inline size_t prefix_slot_floats(int slot_rows, int D) {
+    return static_cast<size_t>(slot_rows) * (2 + D);
 }
-// Whether row block rb is held twice (split: the kernel runs two streams of half a block's rows).
-__host__ __device__ inline bool prefix_twice(int R, int block_rows, int rb, bool split) {
-    return split && R - rb * block_rows <= block_rows / 2;
+// Whether row block rb is held twice.
+__device__ __forceinline__ bool prefix_twice(const PrefixParams& p, int rb) {
+    return p.split && 2 * min(p.block_rows, p.R - rb * p.block_rows) <= p.slot_rows;
 }
 
 // Cache row (of D elements) of position t of kv head h; -1 for a page outside the pool.
@@ -173,12 +176,13 @@ struct PrefixKernel {
     const void* fn;
     int smem, threads;
     int block_rows;  // query rows of a block
-    bool split;      // two streams of half a block's rows (prefix_twice)
+    int slot_rows;   // and of a partial slot
+    bool split;      // two streams of half a slot's rows (prefix_twice)
 };
 // The CUDA-core kernel: cache type, head dimension, query rows of a kv head.
 PrefixKernel select_prefix_cc(int cache_dt, int D, int R);
 
 // Joins every row's parts into out.
-cudaError_t launch_prefix_join(PrefixParams p, bool split, cudaStream_t stream);
+cudaError_t launch_prefix_join(PrefixParams p, cudaStream_t stream);
 
 }  // namespace ftd

@@ -542,7 +542,7 @@ ftd_status ftd_cross_mha(ftd_ctx* ctx, const void* q, const void* q_bias, const 
  * ftd_enable_prefix -- allocate the workspace of ftd_decode_mha_prefix: an fp32 copy of
  * out, two numbers per query row, and one partial block per SM and per kv head and block of query
  * rows.  One cudaMalloc, freed by ftd_destroy.  A second call does nothing.  UNSUPPORTED
- * above 65536 query rows per kv head (B * T * Hq / Hkv), INVALID_ARG with a window.
+ * above 32768 query rows per kv head (B * T * Hq / Hkv), INVALID_ARG with a window.
  */
 ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
 

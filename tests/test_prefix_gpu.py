@@ -86,7 +86,7 @@ def expect(w, inp, k_after, v_after, scales_after, single):
     return out, tol
 
 
-def run(w, inp, out_dtype="f32", page=0, cuda_core=False, bias=True, step=None, status=ftd.FTD_OK, calls=1):
+def run(w, inp, out_dtype="f32", page=0, cuda_core=False, bias=True, step=None, status=ftd.FTD_OK, calls=1, values=True):
     import torch
     T, lens, P = w.q_len, inp["seq_lens"], inp["k_prefix"].shape[1]
     arrs = {"k": inp["k_cache"], "v": inp["v_cache"]}
@@ -133,6 +133,8 @@ def run(w, inp, out_dtype="f32", page=0, cuda_core=False, bias=True, step=None, 
     torch.cuda.synchronize()
     assert ftd.ftd_kernel_launches() == before + 3 * calls
     assert step.get_error() == status
+    if not values:
+        return
     got = out.double().cpu().numpy()
     ka, va = host(kc, arrs["k"]), host(vc, arrs["v"])
     sa = None if t_sc is None else t_sc.cpu().numpy()
@@ -360,3 +362,17 @@ def test_refusals():
     assert ftd.ftd_kernel_launches() == n
     for s in (flat, paged, windowed, many):
         s.close()
+
+
+@pytest.mark.parametrize("cache,out", [("bf16", "bf16"), ("bf16", "f32"), ("i8", "f16")])
+def test_waits_that_run_out(cache, out):
+    """A withheld copy: the bounded waits give up, the error is reported, and the next call is right."""
+    qkv = "f16" if cache == "i8" else cache
+    w, inp = case(cache, qkv, 4, 16, 2, 128, 64, [3, 9, 0, 30], 700, [700] * 4, bias=None)
+    step = make_step(w, out_dtype=out, wait_limit_us=2000)
+    step.enable_prefix()
+    run(w, inp, out_dtype=out, step=step)
+    assert ftd.ftd_debug_stall_next(step.ctx, 1) == ftd.FTD_OK
+    run(w, inp, out_dtype=out, step=step, status=ftd.FTD_ERR_DEVICE_TIMEOUT, values=False)
+    run(w, inp, out_dtype=out, step=step)
+    step.close()
