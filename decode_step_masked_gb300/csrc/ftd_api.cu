@@ -421,6 +421,9 @@ struct ftd_ctx {
     void* pre_pool = nullptr;
     ftd::PrefixKernel pre[2];     // [1]: q and the weights as pairs (the same on CUDA cores)
     bool pre_tc = false;
+    bool pre_own_rows = false;    // the prefix's kernel takes the slots' own rows too
+    float* pre_own_ws = nullptr;  // their partials
+    int2* pre_own_info = nullptr;
     CUtensorMap tmpk;
     CUtensorMap tmpv;
     const void* tm_pk_base = nullptr;
@@ -636,6 +639,22 @@ static cudaError_t launch_overlapped(const void* fn, int grid, int threads, int 
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// The tensor maps of the caches, encoded again when the caches change.
+static ftd_status cache_maps(ftd_ctx* ctx, void* k_cache, void* v_cache) {
+    const ftd_config& c = ctx->cfg;
+    if (ctx->tm_k_base != k_cache) {
+        if (!encode_cache_map(&ctx->tmk, k_cache, c.cache_dtype, ctx->rows, c.head_dim))
+            return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for k_cache");
+        ctx->tm_k_base = k_cache;
+    }
+    if (ctx->tm_v_base != v_cache) {
+        if (!encode_cache_map(&ctx->tmv, v_cache, c.cache_dtype, ctx->rows, c.head_dim))
+            return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for v_cache");
+        ctx->tm_v_base = v_cache;
+    }
+    return FTD_OK;
+}
+
 static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
                                 const void* bias, void* k_cache, void* v_cache, const int32_t* block_table,
                                 const int32_t* seq_lens, float* scales, void* out, cudaStream_t stream,
@@ -710,17 +729,8 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
 
     cudaError_t e;
     if (tki.fn) {
-        const size_t rows = ctx->rows;
-        if (ctx->tm_k_base != k_cache) {
-            if (!encode_cache_map(&ctx->tmk, k_cache, c.cache_dtype, rows, c.head_dim))
-                return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for k_cache");
-            ctx->tm_k_base = k_cache;
-        }
-        if (ctx->tm_v_base != v_cache) {
-            if (!encode_cache_map(&ctx->tmv, v_cache, c.cache_dtype, rows, c.head_dim))
-                return fail(FTD_ERR_CUDA, "cuTensorMapEncodeTiled failed for v_cache");
-            ctx->tm_v_base = v_cache;
-        }
+        const ftd_status mst = cache_maps(ctx, k_cache, v_cache);
+        if (mst != FTD_OK) return mst;
         p.nhb = tcc.nhb;
         p.qblk = tcc.qblk;
         void* args[] = {&ctx->tmk, &ctx->tmv, &p};
@@ -1528,7 +1538,12 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
         off = align_up(off + bytes, 256);
         return o;
     };
-    const size_t o_own = carve(B * T * Hq * D * sizeof(float)), o_ml = carve(Hkv * R * sizeof(float2));
+    // Few query rows per slot: the prefix's kernel takes the own rows too (partials in place of the step's output).
+    const int per = static_cast<int>(T * (Hq / Hkv));
+    const bool own = tc && per <= ftd::kMostOwnRows;
+    const size_t o_own = carve(own ? 0 : B * T * Hq * D * sizeof(float)), o_ml = carve(own ? 0 : Hkv * R * sizeof(float2));
+    const size_t o_ows = carve(own ? (B * Hkv + 2 * ctx->grid) * ftd::own_slot_floats(per, c.head_dim) * sizeof(float) : 0);
+    const size_t o_oinfo = carve(own ? B * Hkv * sizeof(int2) : 0);
     const size_t o_info = carve(Hkv * blocks * sizeof(int2));
     const size_t o_ws = carve(ws * sizeof(float));
     void* pool = nullptr;
@@ -1542,6 +1557,9 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     ctx->pre[0] = k[0];
     ctx->pre[1] = k[1];
     ctx->pre_tc = tc;
+    ctx->pre_own_rows = own;
+    ctx->pre_own_ws = reinterpret_cast<float*>(base + o_ows);
+    ctx->pre_own_info = reinterpret_cast<int2*>(base + o_oinfo);
     ctx->pre_own = reinterpret_cast<float*>(base + o_own);
     ctx->pre_ml = reinterpret_cast<float2*>(base + o_ml);
     ctx->pre_info = reinterpret_cast<int2*>(base + o_info);
@@ -1582,12 +1600,22 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool stall = ctx->stall_calls > 0;  // (the step's launch takes one)
-    // The slots' own rows by the step's kernel, into the workspace, beside the prefix (nothing to share: straight to out).
-    if (prefix_rows == 0)
+    if (prefix_rows == 0)  // nothing to share: straight to out
         return launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, out, s);
-    st = launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, ctx->pre_own, s, false,
-                       ftd::kStep, ctx->pre_ml);
+    const bool stall = ctx->stall_calls > 0;
+    if (ctx->pre_own_rows) {
+        if (!k_cache) k_cache = ctx->k_cache;
+        if (!v_cache) v_cache = ctx->v_cache;
+        char msg[160];
+        st = ftd::check_pointers(c, q, k_new, v_new, qkv_bias, seq_lens, k_cache, v_cache, nullptr, out, msg, sizeof msg);
+        if (st != FTD_OK) return fail(st, "%s", msg);
+        st = cache_maps(ctx, k_cache, v_cache);
+        if (stall) --ctx->stall_calls;
+    } else {
+        // the slots' own rows by the step's kernel, into the workspace, beside the prefix
+        st = launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, ctx->pre_own, s, false,
+                           ftd::kStep, ctx->pre_ml);
+    }
     if (st != FTD_OK) return st;
     ftd::PrefixParams p{};
     p.q = q;
@@ -1603,6 +1631,15 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.ws = ctx->pre_ws;
     p.seg_info = ctx->pre_info;
     p.err = ctx->err;
+    p.own = ctx->pre_own_rows;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.k_cache = static_cast<unsigned char*>(k_cache);
+    p.v_cache = static_cast<unsigned char*>(v_cache);
+    p.block_table = ctx->paged ? block_table : nullptr;
+    p.pages_per_seq = ctx->pages_per_seq;
+    p.own_ws = ctx->pre_own_ws;
+    p.own_info = ctx->pre_own_info;
     p.own_o = ctx->pre_own;
     p.own_ml = ctx->pre_ml;
     p.out = out;
@@ -1641,7 +1678,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
             ctx->tm_pv_base = p.v;
             ctx->tm_p_rows = rows;
         }
-        void* args[] = {&ctx->tmpk, &ctx->tmpv, &p};
+        void* args[] = {&ctx->tmpk, &ctx->tmpv, &ctx->tmk, &ctx->tmv, &p};
         e = launch_overlapped(k.fn, ctx->grid, k.threads, k.smem, args, s);
     } else {
         void* args[] = {&p};
@@ -1652,6 +1689,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     e = ftd::launch_prefix_join(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "join kernel launch");
     g_launches.fetch_add(1);
+    ctx->last_stream = s;
     return FTD_OK;
 }
 

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kCcThreads, 1) prefix_cc_kernel(const PrefixPa
     // and everything before the step has ended (its blocks wait for that before they let this grid start).
     build_prefix_plan(p, first, kCcTile);
     const PrefixSplit sp(p, first);
-    if (blockIdx.x == 0) write_seg_info(p, first, sp);
+    if (blockIdx.x == 0) write_seg_info(p, first, sp, threadIdx.x, kCcThreads);
     const int w = blockIdx.x;
     long long u = sp.begin(w);
     const long long end = sp.begin(w + 1);
@@ -314,14 +314,34 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
         const size_t at = prefix_q_row(p, h, row) * D + d;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (L >= 0 && L <= p.Lmax - p.T) {
-            const int per = p.T * p.group;
-            const float2 own = __ldcg(p.own_ml + (static_cast<size_t>(b) * p.Hkv + h) * per + (row - b * per));
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(p.own_o + at));
-            // a part without weight leaves the other as it is
-            const float m0 = M_s[rr], mn = fmaxf(own.x, m0), lo = exp2f(own.x - mn) / own.y, f = S_s[rr] == 0.f ? 0.f : exp2f(m0 - mn);
-            const float inv = 1.f / (lo + S_s[rr] * f), a = lo * inv, c = f * inv;
-            x = make_float4(o.x * a + acc_s[rr][d] * c, o.y * a + acc_s[rr][d + 1] * c, o.z * a + acc_s[rr][d + 2] * c,
-                            o.w * a + acc_s[rr][d + 3] * c);
+            const int per = p.T * p.group, r_own = row - b * per;
+            float M = M_s[rr], S = S_s[rr];
+            x = make_float4(acc_s[rr][d], acc_s[rr][d + 1], acc_s[rr][d + 2], acc_s[rr][d + 3]);
+            // a part without weight leaves the sums as they are
+            auto add = [&](float m, float l, float o_l, const float4& o) {
+                const float mn = fmaxf(M, m), f = exp2f(m - mn) * o_l, a = S == 0.f ? 0.f : exp2f(M - mn);
+                S = S * a + exp2f(m - mn) * l;
+                x = make_float4(x.x * a + o.x * f, x.y * a + o.y * f, x.z * a + o.z * f, x.w * a + o.w * f);
+                M = mn;
+            };
+            if (p.own) {
+                const int2 v = __ldcg(p.own_info + static_cast<size_t>(b) * p.Hkv + h);
+                const size_t step = own_slot_floats(per, D);
+                const float* s = p.own_ws + (static_cast<size_t>(b) * p.Hkv + h + v.x) * step;
+#pragma unroll 2
+                for (int k = v.x; k <= v.y; ++k, s += step) {
+                    const float m = __ldcg(s + r_own), l = __ldcg(s + per + r_own);
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(s + own_out_at(per) + r_own * D + d));
+                    if (l == 0.f && m <= kNone) continue;  // tokens that came later than the row
+                    add(m, l, 1.f, o);
+                }
+            } else {
+                const float2 own = __ldcg(p.own_ml + (static_cast<size_t>(b) * p.Hkv + h) * per + r_own);
+                const float l = 1.f / own.y;
+                add(own.x, l, l, __ldcg(reinterpret_cast<const float4*>(p.own_o + at)));
+            }
+            const float inv = 1.f / S;
+            x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
         }
         st_out4(p.out, at, x.x, x.y, x.z, x.w, p.out_dtype);
     }

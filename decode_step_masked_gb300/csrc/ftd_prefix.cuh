@@ -37,8 +37,18 @@ struct PrefixParams {
     float* ws;            // partials
     int2* seg_info;       // [Hkv * row blocks] first and last block that hold a piece of the segment
     uint32_t* err;
-    // join
-    const float* own_o;   // [B][T][Hq][D]: the step's fp32 output over the slot's own rows
+    // The slots' own rows, where the prefix's kernel takes them too (own): a segment is one slot and kv head.
+    bool own;
+    const void* k_new;    // [B][T][Hkv][D] qkv dtype
+    const void* v_new;
+    unsigned char* k_cache;  // contiguous [B][Hkv][Lmax][D], or pages through block_table
+    unsigned char* v_cache;
+    const int32_t* block_table;
+    int pages_per_seq;
+    float* own_ws;        // their partials
+    int2* own_info;       // [B * Hkv] first and last worker of a segment
+    // and where the decode step's kernel took them before:
+    const float* own_o;   // [B][T][Hq][D]: its fp32 output
     const float2* own_ml; // [B][Hkv][T * group] (m, 1 / l)
     void* out;            // [B][T][Hq][D] out_dtype
     int out_dtype;
@@ -62,6 +72,11 @@ struct PrefixParams {
 __host__ __device__ inline size_t prefix_slot_floats(int slot_rows, int D) {
     return static_cast<size_t>(slot_rows) * (2 + D);
 }
+// A partial slot of own rows: m and l of the slot's query rows, then their outputs, D each.
+__host__ __device__ inline int own_out_at(int rows) { return (2 * rows + 3) / 4 * 4; }
+__host__ __device__ inline size_t own_slot_floats(int rows, int D) { return static_cast<size_t>(own_out_at(rows)) + static_cast<size_t>(rows) * D; }
+// Most query rows of a slot's kv head (T * group) that the prefix's kernel takes the own rows of.
+constexpr int kMostOwnRows = 32;
 // Whether row block rb is held twice.
 __device__ __forceinline__ bool prefix_twice(const PrefixParams& p, int rb) {
     return p.split && 2 * min(p.block_rows, p.R - rb * p.block_rows) <= p.slot_rows;
@@ -155,10 +170,10 @@ __device__ __forceinline__ PrefixCursor prefix_locate(long long u, const int* fi
     return c;
 }
 
-// Which blocks hold pieces of each segment, for the join; by all threads of the grid's first block.
-__device__ __forceinline__ void write_seg_info(const PrefixParams& p, const int* first, const PrefixSplit& sp) {
+// Which blocks hold pieces of each segment, for the join; by threads t, t + step, .. of the grid's first block.
+__device__ __forceinline__ void write_seg_info(const PrefixParams& p, const int* first, const PrefixSplit& sp, int t, int step = 32) {
     const int per = first[p.row_blocks];
-    for (int s = threadIdx.x; s < p.Hkv * p.row_blocks; s += blockDim.x) {
+    for (int s = t; s < p.Hkv * p.row_blocks; s += step) {
         const int h = s / p.row_blocks, rb = s - h * p.row_blocks;
         const long long u0 = static_cast<long long>(h) * per + first[rb], u1 = static_cast<long long>(h) * per + first[rb + 1];
         p.seg_info[s] = u0 < u1 ? make_int2(sp.holder(u0), sp.holder(u1 - 1)) : make_int2(0, -1);
