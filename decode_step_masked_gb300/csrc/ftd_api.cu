@@ -419,7 +419,7 @@ struct ftd_ctx {
     uint32_t* evict_count = nullptr;
     // ftd_enable_prefix: kernel and workspace of ftd_decode_mha_prefix
     void* pre_pool = nullptr;
-    ftd::PrefixKernel pre[2];     // [1]: q and the weights as pairs (the same on CUDA cores)
+    ftd::PrefixKernel pre[3];     // [pairs] of select_prefix_tc (all alike on CUDA cores)
     bool pre_tc = false;
     bool pre_own_rows = false;    // the prefix's kernel takes the slots' own rows too
     float* pre_own_ws = nullptr;  // their partials
@@ -1520,10 +1520,10 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
     const bool tc = half && c.kernel != FTD_KERNEL_CUDA_CORE && encode_tiled();
     if (R > 32768) return fail(FTD_ERR_UNSUPPORTED, "%s: %zu query rows per kv head, at most 32768", what, R);
-    ftd::PrefixKernel k[2];
+    ftd::PrefixKernel k[3];
     size_t blocks = 0, ws = 0;
-    for (int i = 0; i < 2; ++i) {
-        k[i] = tc ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i == 1)
+    for (int i = 0; i < 3; ++i) {
+        k[i] = tc ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i)
                   : ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
         const size_t n = (R + k[i].block_rows - 1) / k[i].block_rows;
         const size_t floats = (Hkv * n + ctx->grid) * ftd::prefix_slot_floats(k[i].slot_rows, c.head_dim);
@@ -1554,8 +1554,7 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     }
     unsigned char* base = static_cast<unsigned char*>(pool);
     ctx->pre_pool = pool;
-    ctx->pre[0] = k[0];
-    ctx->pre[1] = k[1];
+    for (int i = 0; i < 3; ++i) ctx->pre[i] = k[i];
     ctx->pre_tc = tc;
     ctx->pre_own_rows = own;
     ctx->pre_own_ws = reinterpret_cast<float*>(base + o_ows);
@@ -1653,8 +1652,8 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.Lmax = c.max_len;
     p.P = static_cast<int>(prefix_rows);
     p.R = p.B * p.T * p.group;
-    // q and the weights in one 16-bit number each where q is one and out keeps no more, else in two
-    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 || qkv_bias || c.qkv_dtype != c.cache_dtype];
+    // q as one 16-bit number where it is one, the weights where out keeps no more; else as two
+    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 ? 2 : qkv_bias || c.qkv_dtype != c.cache_dtype ? 1 : 0];
     p.block_rows = k.block_rows;
     p.slot_rows = k.slot_rows;
     p.split = k.split;

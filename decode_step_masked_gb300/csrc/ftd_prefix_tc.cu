@@ -25,9 +25,9 @@
 // m and rescales its row of O; the product of the tile before has ended by then, since the score product
 // behind it has.
 //
-// PAIR: q and the weights as pairs of 16-bit numbers, hi and lo, two products each (about 16 mantissa bits with
-// bf16, 22 with fp16): for fp32 out, and where q is no 16-bit number of the cache's type (a bias, another
-// type).  Both streams then share one row block of 128.
+// PQ, PP: q and the weights as pairs of 16-bit numbers, hi and lo, two products each (about 16 mantissa bits with
+// bf16, 22 with fp16): q where it is no 16-bit number of the cache's type (a bias, another type) and
+// for fp32 out, the weights for fp32 out.  With PQ both streams share one row block of 128.
 //
 // Roles (384 threads, one block an SM): warp 0 copies K and V tiles (TMA, a ring of whole tiles), then writes for the
 // join which blocks hold what; warps 1 and 3 issue the products, each of one stream (one warp for both was busy all the
@@ -59,7 +59,9 @@ struct Share {
 template <int D>
 struct Layout {
     static constexpr int TILE = D / 64 * KB;
-    static constexpr int NSLOT = D == 128 ? 5 : 8;
+    // K slots, then V slots: a K tile is free when its scores are made, a V tile, which waits for the softmax, later
+    // (one ring of five, in which a K tile's place can be that of an earlier V tile, kept the next scores waiting)
+    static constexpr int NK = D == 128 ? 2 : 4, NV = D == 128 ? 3 : 4, NSLOT = NK + NV;
     // Two streams' q, or hi and lo of one; on own rows two buffers a stream.  It lies before the ring: a product over
     // a few own rows reads 128 all the same, what lies behind them (its rows of S are never looked at).
     static constexpr int OFF_RING = 2 * TILE;
@@ -232,10 +234,10 @@ static __device__ __noinline__ void copy_q(const PrefixParams& p, unsigned char*
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
-template <typename CT, int D, bool PAIR>
+template <typename CT, int D, bool PQ>
 __device__ __forceinline__ void put_q(const PrefixParams& p, unsigned char* dst, int box_rows, int lo_at, int h, int b0, int r_begin, int rows,
                                       int w, int ws) {
-    if constexpr (!PAIR) copy_q<D>(p, dst, box_rows, h, b0, r_begin, rows, w, ws);
+    if constexpr (!PQ) copy_q<D>(p, dst, box_rows, h, b0, r_begin, rows, w, ws);
     else wide::with_qkv_type(p.qkv_dtype, [&](auto tag) { put_q_as<CT, decltype(tag), D>(p, dst, box_rows, lo_at, h, b0, r_begin, rows, w, ws); });
 }
 
@@ -329,15 +331,11 @@ static __device__ __noinline__ void mask_scores(uint32_t ts, int lim) {
     wide::tmem_st_wait();
 }
 
-// A tile whose scores are in TMEM at ts: the weights of this thread's row, which sees the first `lim` of its columns (none:
-// <= 0), over them.  Columns from `edge` on belong to nobody and may hold anything.  live: the row is one; chained: its row of O, at to, holds earlier tiles.  ml: running reference and sum.
-template <typename CT, int D, bool PAIR>
-static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int lim, int edge, bool live, bool chained, float2 ml, float qscale) {
+// The weights of a tile in two passes over its scores: the largest, then the weights against the reference that it leaves.
+template <typename CT, int D, bool PP>
+static __device__ __noinline__ float2 weigh_tile(uint32_t ts, uint32_t to, bool sees, bool chained, float2 ml, float qscale) {
     constexpr unsigned FULL = 0xffffffffu;
     float m = ml.x, l = ml.y;
-    const bool sees = live && lim > 0;
-    const bool masked = live && lim < TK && (lim > 0 || edge < TK);
-    if (__any_sync(FULL, masked)) mask_scores(ts, masked ? lim : TK);
     // the largest score, and what it does to the reference
     float t[4];
     {
@@ -378,7 +376,7 @@ static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int li
 #pragma unroll 1
     for (int c = 0; c < TK / 32; ++c) {
         land_scores(v);
-        uint32_t hi[16], lo[PAIR ? 16 : 1];
+        uint32_t hi[16], lo[PP ? 16 : 1];
         float x[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
@@ -391,12 +389,12 @@ static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int li
             b = wide::ex2(b);
             if (e & 2) acc1 = add2(acc1, pack2(a, b));
             else acc0 = add2(acc0, pack2(a, b));
-            if constexpr (PAIR) wide::split_pair<CT>(a, b, hi[e / 2], lo[e / 2]);
+            if constexpr (PP) wide::split_pair<CT>(a, b, hi[e / 2], lo[e / 2]);
             else hi[e / 2] = pack_ct<CT>(a, b);
         }
         // 32 keys' weights: 16 columns, or 16 of hi and 16 of lo, over scores that have been read
-        tc::tmem_st16(ts + (PAIR ? 32 : 16) * c, hi);
-        if constexpr (PAIR) tc::tmem_st16(ts + 32 * c + 16, lo);
+        tc::tmem_st16(ts + (PP ? 32 : 16) * c, hi);
+        if constexpr (PP) tc::tmem_st16(ts + 32 * c + 16, lo);
     }
     float a, b;
     unpack2(add2(acc0, acc1), a, b);
@@ -405,26 +403,78 @@ static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int li
     return make_float2(m, l + (a + b));
 }
 
+// A tile whose scores are in TMEM at ts: the weights of this thread's row, which sees the first `lim` of its columns (none:
+// <= 0), over them.  Columns from `edge` on belong to nobody and may hold anything.  live: the row is one; chained: its row of O, at to, holds earlier tiles.  ml: running reference and sum.
+template <typename CT, int D, bool PP>
+static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int lim, int edge, bool live, bool chained, float2 ml, float qscale) {
+    constexpr unsigned FULL = 0xffffffffu;
+    const bool sees = live && lim > 0;
+    const bool masked = live && lim < TK && (lim > 0 || edge < TK);
+    if (__any_sync(FULL, masked)) mask_scores(ts, masked ? lim : TK);
+    if constexpr (!PP) {
+        if (chained) {
+            // One pass: the weights against the reference as it is, kept until the largest score is known to allow it (1500
+            // against 1050 cycles a tile).
+            const float ref = sees ? -ml.x : -INFINITY;
+            const uint64_t sc2 = pack2(qscale, qscale), m2 = pack2(ref, ref);
+            uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
+            uint32_t hi[TK / 2], v[32];
+            float t0 = -INFINITY, t1 = -INFINITY;
+            fetch_scores(ts, v);
+#pragma unroll
+            for (int c = 0; c < TK / 32; ++c) {
+                land_scores(v);
+                float x[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
+                if (c + 1 < TK / 32) fetch_scores(ts + 32 * (c + 1), v);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    if (e & 2) t1 = fmaxf(t1, fmaxf(x[e], x[e + 1]));
+                    else t0 = fmaxf(t0, fmaxf(x[e], x[e + 1]));
+                    float a, b;
+                    unpack2(fma2(pack2(x[e], x[e + 1]), sc2, m2), a, b);
+                    a = wide::ex2(a);
+                    b = wide::ex2(b);
+                    if (e & 2) acc1 = add2(acc1, pack2(a, b));
+                    else acc0 = add2(acc0, pack2(a, b));
+                    hi[16 * c + e / 2] = pack_ct<CT>(a, b);
+                }
+            }
+            if (!__any_sync(FULL, sees && fmaxf(t0, t1) * qscale > ml.x + tc::kRescaleLog2)) {
+#pragma unroll
+                for (int c = 0; c < TK / 32; ++c) tc::tmem_st16(ts + 16 * c, hi + 16 * c);
+                float a, b;
+                unpack2(add2(acc0, acc1), a, b);
+                wide::tmem_st_wait();
+                tc::tc_fence_before();
+                return make_float2(ml.x, ml.y + (a + b));
+            }
+        }
+    }
+    return weigh_tile<CT, D, PP>(ts, to, sees, chained, ml, qscale);
+}
+
 // The scores' products: q at qa (lo half lo_at behind, boxes box_at apart, in 16-byte units), K at ka.  One thread.
-template <int D, bool PAIR>
+template <int D, bool PQ>
 static __device__ __noinline__ void issue_scores(uint32_t ts, uint64_t qa, uint64_t ka, uint32_t lo_at, uint32_t box_at, uint32_t id) {
     tc::tc_fence_after();
 #pragma unroll
     for (int kq = 0; kq < D / 16; ++kq) {
         const uint64_t k = ka + (((kq >> 2) * KB + (kq & 3) * 32) >> 4), q = qa + (kq >> 2) * box_at + (kq & 3) * 2;
         tc::mma_f16(ts, q, k, id, kq > 0);
-        if constexpr (PAIR) tc::mma_f16(ts, q + lo_at, k, id, true);
+        if constexpr (PQ) tc::mma_f16(ts, q + lo_at, k, id, true);
     }
 }
 
 // The weights (TMEM at tp) times V at vb into O at to, which begins (fresh) or goes on.  One thread.
-template <int D, bool PAIR>
+template <int D, bool PP>
 static __device__ __noinline__ void issue_values(uint32_t to, uint32_t tp, uint64_t vb, bool fresh, uint32_t id) {
     tc::tc_fence_after();
 #pragma unroll
     for (int kq = 0; kq < TK / 16; ++kq) {
         const uint64_t v = vb + (kq * 2048 >> 4);
-        if constexpr (PAIR) {  // chunks of 32 keys: 16 columns of hi, 16 of lo
+        if constexpr (PP) {  // chunks of 32 keys: 16 columns of hi, 16 of lo
             const uint32_t c = tp + (kq >> 1) * 32 + (kq & 1) * 8;
             tc::mma_f16_ta(to, c, v, id, !fresh || kq > 0);
             tc::mma_f16_ta(to, c + 16, v, id, true);
@@ -520,13 +570,13 @@ struct OwnSplit {
     __device__ int holder(long long u) const { return static_cast<int>(((u + 1) * V - 1) / U); }
 };
 
-template <typename CT, int D, bool PAIR>
+template <typename CT, int D, bool PQ, bool PP>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ CUtensorMap tmk_own, const __grid_constant__ CUtensorMap tmv_own,
                      const __grid_constant__ PrefixParams p) {
     using LY = Layout<D>;
-    constexpr int NSLOT = LY::NSLOT, TILE = LY::TILE, BOXES = D / 64;
+    constexpr int NK = LY::NK, NV = LY::NV, NSLOT = LY::NSLOT, TILE = LY::TILE, BOXES = D / 64;
     constexpr bool BF = std::is_same_v<CT, __nv_bfloat16>;
     constexpr unsigned FULL = 0xffffffffu;
     enum : int {
@@ -616,35 +666,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tiles of stream s in a piece, and the piece's tile that is its j-th
     auto tiles_of = [](const Piece& x, int s) { return x.twice ? (x.nt - s + 1) / 2 : x.nt; };
     auto tile_of = [](const Piece& x, int s, int j) { return x.twice ? 2 * j + s : j; };
-    // Ring order.  Prefix: K and V of the piece's tiles in turn.  Own rows: K and V of stream 0's i-th tile, then of stream 1's.
+    // Tiles are counted in the order of the copies: a piece's tiles in turn; on own rows stream 0's i-th tile, then stream 1's.
+    // K and V slot of tile t, and the parity of its round
+    auto k_slot = [](int t) { return t % NK; };
+    auto k_par = [](int t) { return (t / NK) & 1; };
+    auto v_slot = [](int t) { return NK + t % NV; };
+    auto v_par = [](int t) { return (t / NV) & 1; };
     auto wait = [&](int b, int parity) {
         if (__all_sync(FULL, mbar_try_wait(bar(b), parity))) return true;
         return wait_on(bar(b), parity, p.err, abort_flag, p.wait_cycles);
     };
 
-    int issued = 0;  // producer: tiles copied (or withheld)
+    int issued = 0;  // producer: K and V tiles copied (or withheld)
     const bool withhold = p.stall && blockIdx.x == 0;  // test hook: block 0's first copy never comes
     if (works && warp == 0) {
         // ------------------------------------------------ TMA producer
         bool ok = true;
-        auto copy = [&](const CUtensorMap* map, long long row) -> bool {
-            const int slot = issued % NSLOT;
-            if (issued >= NSLOT && !wait(kEmpty + slot, ((issued / NSLOT) - 1) & 1)) return false;
+        auto copy = [&](const CUtensorMap* mk, const CUtensorMap* mv, long long row) -> bool {
             if (row < 0) {
                 if (lane == 0) atomicOr(p.err, kErrBadPage);
                 row = 0;
             }
-            if (!(withhold && issued == 0) && elect_one()) {
-                const uint32_t dst = smem_addr(ring + slot * TILE);
-                mbar_arrive_expect_tx(bar(kFull + slot), TILE);
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+                const int t = issued >> 1, slot = v ? v_slot(t) : k_slot(t);
+                if (t >= (v ? NV : NK) && !wait(kEmpty + slot, (v ? v_par(t) : k_par(t)) ^ 1)) return false;
+                if (!(withhold && issued == 0) && elect_one()) {
+                    const uint32_t dst = smem_addr(ring + slot * TILE);
+                    mbar_arrive_expect_tx(bar(kFull + slot), TILE);
 #pragma unroll
-                for (int b = 0; b < BOXES; ++b) tma_load(dst + b * KB, map, 64 * b, static_cast<int>(row), bar(kFull + slot));
+                    for (int b = 0; b < BOXES; ++b) tma_load(dst + b * KB, v ? mv : mk, 64 * b, static_cast<int>(row), bar(kFull + slot));
+                }
+                __syncwarp();
+                ++issued;
             }
-            __syncwarp();
-            ++issued;
             return true;
         };
-#pragma unroll 1
         for (int ph = 0; ph < 2 && ok; ++ph) {
             if ((ph == 0) != own_first) {
 #pragma unroll 1
@@ -653,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = 0; i < x.nt && ok; ++i) {
                         const long long row = prefix_row(p, x.c.h, (x.c.tile + i) * TK);
-                        ok = copy(&tmk, row) && copy(&tmv, row);
+                        ok = copy(&tmk, &tmv, row);
                     }
                     u += x.nt;
                 }
@@ -667,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int s = 0; s < 2; ++s) {
                         if (i >= own_n[s] || !ok) continue;
                         const long long row = own_row(p, k[s].b, k[s].h, k[s].tile * TK);
-                        ok = copy(&tmk_own, row) && copy(&tmv_own, row);
+                        ok = copy(&tmk_own, &tmv_own, row);
                         if (i + 1 < own_n[s]) k[s].next(p, lane);
                     }
                 }
@@ -680,36 +737,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq0 = tc::smem_desc_sw128(smem_addr(smem), 16, 1024);
         const uint64_t dk0 = tc::smem_desc_sw128(smem_addr(ring), 16, 1024);
         const uint64_t dv0 = tc::smem_desc_sw128(smem_addr(ring), KB, 1024);
-        int items = 0, starts = 0;  // tiles of the ring that the pieces before took; starts waited for
+        int tiles = 0, starts = 0;  // tiles of the pieces before; starts waited for
         int np = 0, turns = 0;      // products P.V issued; steps taken
         bool ok = true;
-        auto tile_ready = [&](int item) { return wait(kReady + item % NSLOT, (item / NSLOT) & 1) && wait(kFull + item % NSLOT, (item / NSLOT) & 1); };
+        auto tile_ready = [&](int slot, int parity) { return wait(kReady + slot, parity) && wait(kFull + slot, parity); };
         // a slot is free when both streams are through with it; a tile of one stream counts twice
         auto release = [&](int slot, bool both) {
             tc::mma_commit(bar(kEmpty + slot));
             if (!both) tc::mma_commit(bar(kEmpty + slot));
         };
-        // One step: the weights times V of ring item v (none: < 0) once they are there, then the scores with K of item k
+        // One step: the weights times V of tile v (none: < 0) once they are there, then the scores with K of tile k
         // (none: < 0).  The tiles are waited for before the weights, so nothing comes between the two products.
         // fresh, end: O begins and is complete with this product; both: the other stream takes the tiles too.
         // The streams take turns, so that one's softmax falls under the other's products: without, both come at once, and both
         // wait for twice the products (4250 against 3000 cycles a step).
         auto step = [&](int v, bool fresh, bool end, int k, uint32_t q_at, uint32_t lo_at, uint32_t box_at, bool both) -> bool {
-            if (v >= 0 && !tile_ready(v)) return false;
-            if (k >= 0 && !tile_ready(k)) return false;
+            if (v >= 0 && !tile_ready(v_slot(v), v_par(v))) return false;
+            if (k >= 0 && !tile_ready(k_slot(k), k_par(k))) return false;
             if (v >= 0 && !wait(kPFull + s, np++ & 1)) return false;
             if (s + turns > 0 && !wait(kTurn + s, (turns + s - 1) & 1)) return false;
             ++turns;
             if (elect_one()) {
                 if (v >= 0) {
-                    const int slot = v % NSLOT;
-                    issue_values<D, PAIR>(tmem + 2 * TK + s * TK, tmem + s * TK, dv0 + static_cast<uint32_t>(slot * (TILE >> 4)), fresh, id_o);
+                    const int slot = v_slot(v);
+                    issue_values<D, PP>(tmem + 2 * TK + s * TK, tmem + s * TK, dv0 + static_cast<uint32_t>(slot * (TILE >> 4)), fresh, id_o);
                     release(slot, both);
                     if (end) tc::mma_commit(bar(kOFull + s));
                 }
                 if (k >= 0) {
-                    const int slot = k % NSLOT;
-                    issue_scores<D, PAIR>(tmem + s * TK, dq0 + (q_at >> 4), dk0 + static_cast<uint32_t>(slot * (TILE >> 4)), lo_at >> 4, box_at >> 4, id_s);
+                    const int slot = k_slot(k);
+                    issue_scores<D, PQ>(tmem + s * TK, dq0 + (q_at >> 4), dk0 + static_cast<uint32_t>(slot * (TILE >> 4)), lo_at >> 4, box_at >> 4, id_s);
                     tc::mma_commit(bar(kSFull + s));
                     release(slot, both);
                 }
@@ -731,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int most = tiles_of(x, 0);
 #pragma unroll 1
                     for (int j = -1; j < most && ok; ++j)
-                        ok = step(j < 0 || j >= n ? -1 : items + 2 * tile_of(x, s, j) + 1, j == 0, j + 1 == n,
-                                  j + 1 < n ? items + 2 * tile_of(x, s, j + 1) : -1, PAIR ? 0 : s * TILE, TILE, KB, !x.twice);
-                    items += 2 * x.nt;
+                        ok = step(j < 0 || j >= n ? -1 : tiles + tile_of(x, s, j), j == 0, j + 1 == n, j + 1 < n ? tiles + tile_of(x, s, j + 1) : -1,
+                                  PQ ? 0 : s * TILE, TILE, KB, !x.twice);
+                    tiles += x.nt;
                     u += x.nt;
                 }
             } else if (owns) {
@@ -750,11 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool has = i >= 0 && i < n, end = has && (k.tile + 1 == k.nt || i + 1 == n);  // of the piece of tile i
                     if (has && i + 1 < n) k.next(p, lane);
                     if (end) buf ^= 1;
-                    ok = step(has ? items + 4 * i + 2 * s + 1 : -1, fresh, end, i + 1 < n ? items + 4 * (i + 1) + 2 * s : -1,
+                    ok = step(has ? tiles + 2 * i + s : -1, fresh, end, i + 1 < n ? tiles + 2 * (i + 1) + s : -1,
                               s * TILE + buf * LY::OWN_BUF, LY::OWN_LO, LY::OWN_BOX, false);
                     if (has) fresh = end;
                 }
-                items += 2 * (own_n[0] + own_n[1]);
+                tiles += own_n[0] + own_n[1];
             }
         }
         // one last commit: it completes once every product issued above has
@@ -764,16 +821,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ tiles that are not whole
         int items = 0;
         bool ok = true;
-        auto landed = [&]() { return wait(kFull + items % NSLOT, (items / NSLOT) & 1); };
+        auto slot_of = [&]() { return items & 1 ? v_slot(items >> 1) : k_slot(items >> 1); };
+        auto landed = [&]() { return wait(kFull + slot_of(), items & 1 ? v_par(items >> 1) : k_par(items >> 1)); };
         auto pass = [&](bool written) {
             if (written) fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kReady + items % NSLOT));
+            if (lane == 0) mbar_arrive(bar(kReady + slot_of()));
             ++items;
         };
         // rows from `from` on of the V tile that is there become zeros
         auto zero_rows = [&](int from) {
-            unsigned char* tile = ring + (items % NSLOT) * TILE + from * 128;
+            unsigned char* tile = ring + slot_of() * TILE + from * 128;
             const int nz = (TK - from) * 8;
 #pragma unroll 4
             for (int i = lane; i < nz; i += 32) {
@@ -825,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int v = 0; v < 2 && ok; ++v) {
                             ok = landed();
                             if (!ok) break;
-                            unsigned char* tile = ring + (items % NSLOT) * TILE;
+                            unsigned char* tile = ring + slot_of() * TILE;
                             unsigned char* cache = v ? p.v_cache : p.k_cache;
 #pragma unroll 1
                             for (int j = lane; j < n; j += 32) {
@@ -870,9 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     {
                         // q: neighbouring lanes take neighbouring 16 bytes of a row (a pair's q is made by both streams, half
                         // of the rows each)
-                        const int r0 = quarter * 32 + (PAIR ? 16 * s : 0);
-                        put_q<CT, D, PAIR>(p, smem + (PAIR ? 0 : s * TILE), TK, TILE, x.c.h, x.c.rb * p.block_rows + (x.twice ? 0 : s * TK), r0,
-                                           PAIR ? 16 : 32, 0, 1);
+                        const int r0 = quarter * 32 + (PQ ? 16 * s : 0);
+                        put_q<CT, D, PQ>(p, smem + (PQ ? 0 : s * TILE), TK, TILE, x.c.h, x.c.rb * p.block_rows + (x.twice ? 0 : s * TK), r0,
+                                           PQ ? 16 : 32, 0, 1);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kStart));
@@ -885,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         ++ns;
                         tc::tc_fence_after();
-                        ml = take_tile<CT, D, PAIR>(ts, to, seen - (x.c.tile + tile_of(x, s, j)) * TK, most - (x.c.tile + tile_of(x, s, j)) * TK, true, j > 0, ml, p.qscale);
+                        ml = take_tile<CT, D, PP>(ts, to, seen - (x.c.tile + tile_of(x, s, j)) * TK, most - (x.c.tile + tile_of(x, s, j)) * TK, true, j > 0, ml, p.qscale);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kPFull + s));
                     }
@@ -908,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc::tc_fence_before();
                     }
-                    if (PAIR) ok = wait(kOFull + (s ^ 1), no[s ^ 1] & 1);  // the q that both streams share is free
+                    if (PQ) ok = wait(kOFull + (s ^ 1), no[s ^ 1] & 1);  // the q that both streams share is free
                     ++no[s ^ 1];
                     u += x.nt;
                 }
@@ -920,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n > 0) k.locate(p, coarse, share.own_at[s], lane);
                 // the q of a segment into buffer `buf`, by the warps from q0 on
                 auto fetch_q = [&](const OwnWalk& at, int buf, int q0) {
-                    put_q<CT, D, PAIR>(p, smem + s * TILE + buf * LY::OWN_BUF, kMostOwnRows, LY::OWN_LO, at.h, at.b * rows, 0, rows,
+                    put_q<CT, D, PQ>(p, smem + s * TILE + buf * LY::OWN_BUF, kMostOwnRows, LY::OWN_LO, at.h, at.b * rows, 0, rows,
                                        quarter - q0, 4 - q0);
                     fence_proxy_async_smem();
                 };
@@ -954,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         ++ns;
                         tc::tc_fence_after();
-                        ml = take_tile<CT, D, PAIR>(ts, to, k.L + tok + 1 - k.tile * TK, k.L + p.T - k.tile * TK, live, !fresh, ml, p.qscale);
+                        ml = take_tile<CT, D, PP>(ts, to, k.L + tok + 1 - k.tile * TK, k.L + p.T - k.tile * TK, live, !fresh, ml, p.qscale);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kPFull + s));
                     }
@@ -1039,8 +1097,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*abort_flag && warp == 0 && lane == 0) {
         // a bounded wait ran out: wait (long drain limit) for the copies in flight
 #pragma unroll 1
-        for (int i = max(0, issued - NSLOT); i < issued; ++i)
-            if (!(withhold && i == 0)) mbar_wait_bounded(bar(kFull + i % NSLOT), (i / NSLOT) & 1, p.err, kDrainLimitCycles);
+        for (int i = max(0, issued - 2 * NV); i < issued; ++i) {
+            const int t = i >> 1;
+            if (!(i & 1) && t + NK < (issued + 1) / 2) continue;  // (a K slot that was filled again since)
+            if (!(withhold && i == 0))
+                mbar_wait_bounded(bar(kFull + ((i & 1) ? v_slot(t) : k_slot(t))), (i & 1) ? v_par(t) : k_par(t), p.err, kDrainLimitCycles);
+        }
     }
     if (warp == 1) {
         if (lane == 0 && works) mbar_wait_bounded(bar(kDrain), 0u, p.err, kDrainLimitCycles);
@@ -1052,17 +1114,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename CT, int D>
-PrefixKernel pick(bool pair) {
+PrefixKernel pick(int pairs) {
     using LY = Layout<D>;
-    if (pair) return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, true>), LY::SMEM, kThreads, TK, 2 * TK, true};
-    return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, false>), LY::SMEM, kThreads, 2 * TK, 2 * TK, true};
+    if (pairs == 2) return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, true, true>), LY::SMEM, kThreads, TK, 2 * TK, true};
+    if (pairs == 1) return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, true, false>), LY::SMEM, kThreads, TK, 2 * TK, true};
+    return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, false, false>), LY::SMEM, kThreads, 2 * TK, 2 * TK, true};
 }
 
 }  // namespace ptc
 
-PrefixKernel select_prefix_tc(bool bf16, int D, bool pair) {
-    if (bf16) return D == 64 ? ptc::pick<__nv_bfloat16, 64>(pair) : ptc::pick<__nv_bfloat16, 128>(pair);
-    return D == 64 ? ptc::pick<__half, 64>(pair) : ptc::pick<__half, 128>(pair);
+PrefixKernel select_prefix_tc(bool bf16, int D, int pairs) {
+    if (bf16) return D == 64 ? ptc::pick<__nv_bfloat16, 64>(pairs) : ptc::pick<__nv_bfloat16, 128>(pairs);
+    return D == 64 ? ptc::pick<__half, 64>(pairs) : ptc::pick<__half, 128>(pairs);
 }
 
 }  // namespace ftd

@@ -4,6 +4,6 @@
 #include "ftd_prefix.cuh"
 
 namespace ftd {
-// Cache type, head dimension, and whether q and the weights are kept as pairs.
-PrefixKernel select_prefix_tc(bool bf16, int D, bool pair);
+// Cache type, head dimension, and what is kept as pairs of 16-bit numbers: 0 nothing, 1 q, 2 q and the weights.
+PrefixKernel select_prefix_tc(bool bf16, int D, int pairs);
 }  // namespace ftd

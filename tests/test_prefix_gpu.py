@@ -146,7 +146,7 @@ def run(w, inp, out_dtype="f32", page=0, cuda_core=False, bias=True, step=None, 
     if own:
         step.close()
     inp = inp if use else dict(inp, bias=None)
-    single = out_dtype != "f32" and not use and w.qkv_dtype == w.cache_dtype and not cuda_core and w.cache_dtype != "f32"
+    single = out_dtype != "f32" and not cuda_core and w.cache_dtype != "f32"  # weights of one 16-bit number
     want, tol = expect(w, inp, ka, va, sa, single)
     if out_dtype != "f32":
         tol = tol + np.abs(want) * ref.HALF_STEP[out_dtype] * (1 + 2.0 ** -7) + (2.0 ** -25 if out_dtype == "f16" else 0.0)
