@@ -1538,9 +1538,14 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
         off = align_up(off + bytes, 256);
         return o;
     };
-    // Few query rows per slot: the prefix's kernel takes the own rows too (partials in place of the step's output).
+    // The prefix's kernel takes the own rows too (partials in place of the step's output) where a slot has 4 to 32 query rows and
+    // short contexts, or where there is little of them.  Own rows with it / by the step's kernel, us: 64 slots of 1 to
+    // 1023 rows, 8 kv heads of 128 behind 8192, with 1 / 2 / 4 / 8 / 32 query rows 118 / 111 / 104 / 107 / 178 against 93 / 96 /
+    // 110 / 115 / 262; 16 slots of 7000 to 8000 rows, 8 query rows 153 against 137; 4 / 8 / 16 slots of 17 to
+    // 190 rows, 32 heads 46 / 54 / 62 against 57 / 55 / 57.
     const int per = static_cast<int>(T * (Hq / Hkv));
-    const bool own = tc && per <= ftd::kMostOwnRows;
+    const size_t own_tiles = B * Hkv * ((static_cast<size_t>(c.max_len) + 127) / 128);
+    const bool own = tc && per <= ftd::kMostOwnRows && ((per >= 4 && c.max_len <= 4096) || own_tiles <= static_cast<size_t>(4 * ctx->grid));
     const size_t o_own = carve(own ? 0 : B * T * Hq * D * sizeof(float)), o_ml = carve(own ? 0 : Hkv * R * sizeof(float2));
     const size_t o_ows = carve(own ? (B * Hkv + 2 * ctx->grid) * ftd::own_slot_floats(per, c.head_dim) * sizeof(float) : 0);
     const size_t o_oinfo = carve(own ? B * Hkv * sizeof(int2) : 0);

@@ -139,13 +139,21 @@ __device__ __forceinline__ void build_prefix_plan(const PrefixParams& p, int* fi
     __syncthreads();
 }
 
+// First of the tiles of worker w, of W that share U equally: floor(w U / W), by divisions of 32 bits where U has no more.
+__device__ __forceinline__ long long equal_share(long long U, int W, int w) {
+    if (w >= W) return U;
+    if (U >= (1LL << 31)) return w * U / W;
+    const uint32_t u = static_cast<uint32_t>(U), n = static_cast<uint32_t>(W), q = u / n;
+    return static_cast<long long>(w) * q + static_cast<uint32_t>(w) * (u - q * n) / n;  // (w, u mod W < W <= 2^12)
+}
+
 // Equal contiguous ranges of U tiles over W blocks.
 struct PrefixSplit {
     long long U;
     int W;
     __device__ PrefixSplit(const PrefixParams& p, const int* first)
         : U(static_cast<long long>(p.Hkv) * first[p.row_blocks]), W(static_cast<int>(min(static_cast<long long>(p.workers), max(U, 1LL)))) {}
-    __device__ long long begin(int w) const { return w >= W ? U : w * U / W; }
+    __device__ long long begin(int w) const { return equal_share(U, W, w); }
     __device__ int holder(long long u) const { return static_cast<int>(((u + 1) * W - 1) / U); }
 };
 
@@ -156,7 +164,7 @@ struct PrefixCursor {
 __device__ __forceinline__ PrefixCursor prefix_locate(long long u, const int* first, int row_blocks) {
     const int per = first[row_blocks];
     PrefixCursor c;
-    c.h = static_cast<int>(u / per);
+    c.h = u < (1LL << 31) ? static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(per)) : static_cast<int>(u / per);
     const int rem = static_cast<int>(u - static_cast<long long>(c.h) * per);
     int lo = 0, hi = row_blocks - 1;  // largest rb with first[rb] <= rem
     while (lo < hi) {

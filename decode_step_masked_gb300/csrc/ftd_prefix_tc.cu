@@ -455,31 +455,55 @@ static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int li
     return weigh_tile<CT, D, PP>(ts, to, sees, chained, ml, qscale);
 }
 
+// The products take their operands as uniform registers.  What is the same for the whole warp is handed round once, so that
+// the compiler knows it to be, and descriptors are built from their low halves (the high ones are all alike: rows 1 KB apart
+// in groups of eight, 128-byte swizzle): 65 cycles from one product to the next, 115 with every operand moved over.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+
+// D (TMEM) (+)= A (shared memory) . B (shared memory)
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(add), "n"(kDescHigh)
+        : "memory");
+}
+// D (TMEM) (+)= A (TMEM) . B (shared memory)
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(add), "n"(kDescHigh)
+        : "memory");
+}
+
 // The scores' products: q at qa (lo half lo_at behind, boxes box_at apart, in 16-byte units), K at ka.  One thread.
 template <int D, bool PQ>
-static __device__ __noinline__ void issue_scores(uint32_t ts, uint64_t qa, uint64_t ka, uint32_t lo_at, uint32_t box_at, uint32_t id) {
+__device__ __forceinline__ void issue_scores(uint32_t ts, uint32_t qa, uint32_t ka, uint32_t lo_at, uint32_t box_at, uint32_t id) {
     tc::tc_fence_after();
 #pragma unroll
     for (int kq = 0; kq < D / 16; ++kq) {
-        const uint64_t k = ka + (((kq >> 2) * KB + (kq & 3) * 32) >> 4), q = qa + (kq >> 2) * box_at + (kq & 3) * 2;
-        tc::mma_f16(ts, q, k, id, kq > 0);
-        if constexpr (PQ) tc::mma_f16(ts, q + lo_at, k, id, true);
+        const uint32_t k = ka + (((kq >> 2) * KB + (kq & 3) * 32) >> 4), q = qa + (kq >> 2) * box_at + (kq & 3) * 2;
+        product_ss(ts, q, k, id, kq > 0);
+        if constexpr (PQ) product_ss(ts, q + lo_at, k, id, 1u);
     }
 }
 
-// The weights (TMEM at tp) times V at vb into O at to, which begins (fresh) or goes on.  One thread.
+// The weights (TMEM at tp) times V at vb into O at to, which begins (more 0) or goes on.  One thread.
 template <int D, bool PP>
-static __device__ __noinline__ void issue_values(uint32_t to, uint32_t tp, uint64_t vb, bool fresh, uint32_t id) {
+__device__ __forceinline__ void issue_values(uint32_t to, uint32_t tp, uint32_t vb, uint32_t more, uint32_t id) {
     tc::tc_fence_after();
 #pragma unroll
     for (int kq = 0; kq < TK / 16; ++kq) {
-        const uint64_t v = vb + (kq * 2048 >> 4);
+        const uint32_t v = vb + (kq * 2048 >> 4);
         if constexpr (PP) {  // chunks of 32 keys: 16 columns of hi, 16 of lo
             const uint32_t c = tp + (kq >> 1) * 32 + (kq & 1) * 8;
-            tc::mma_f16_ta(to, c, v, id, !fresh || kq > 0);
-            tc::mma_f16_ta(to, c + 16, v, id, true);
+            product_ts(to, c, v, id, kq > 0 ? 1u : more);
+            product_ts(to, c + 16, v, id, 1u);
         } else {
-            tc::mma_f16_ta(to, tp + kq * 8, v, id, !fresh || kq > 0);
+            product_ts(to, tp + kq * 8, v, id, kq > 0 ? 1u : more);
         }
     }
 }
@@ -565,7 +589,7 @@ struct OwnSplit {
     __device__ OwnSplit(const PrefixParams& p, const int* coarse)
         : U(p.own ? static_cast<long long>(p.Hkv) * coarse[(p.B + 31) / 32] : 0),
           V(static_cast<int>(min(2LL * p.workers, max(U, 1LL)))) {}
-    __device__ long long begin(int v) const { return v >= V ? U : v * U / V; }
+    __device__ long long begin(int v) const { return equal_share(U, V, v); }
     __device__ int tiles(int v) const { return static_cast<int>(begin(v + 1) - begin(v)); }
     __device__ int holder(long long u) const { return static_cast<int>(((u + 1) * V - 1) / U); }
 };
@@ -734,15 +758,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ products of one stream
         const int s = warp >> 1;
         const uint32_t id_s = tc::instr_desc(BF, TK, TK, false), id_o = tc::instr_desc(BF, TK, D, false, true);
-        const uint64_t dq0 = tc::smem_desc_sw128(smem_addr(smem), 16, 1024);
-        const uint64_t dk0 = tc::smem_desc_sw128(smem_addr(ring), 16, 1024);
-        const uint64_t dv0 = tc::smem_desc_sw128(smem_addr(ring), KB, 1024);
+        const uint32_t dq0 = desc_low(smem_addr(smem), 16), dk0 = desc_low(smem_addr(ring), 16), dv0 = desc_low(smem_addr(ring), KB);
+        const uint32_t ts = uniform(tmem + s * TK), to = ts + 2 * TK;
         int tiles = 0, starts = 0;  // tiles of the pieces before; starts waited for
         int np = 0, turns = 0;      // products P.V issued; steps taken
         bool ok = true;
         auto tile_ready = [&](int slot, int parity) { return wait(kReady + slot, parity) && wait(kFull + slot, parity); };
         // a slot is free when both streams are through with it; a tile of one stream counts twice
-        auto release = [&](int slot, bool both) {
+        auto release = [&](uint32_t slot, bool both) {
             tc::mma_commit(bar(kEmpty + slot));
             if (!both) tc::mma_commit(bar(kEmpty + slot));
         };
@@ -757,18 +780,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (v >= 0 && !wait(kPFull + s, np++ & 1)) return false;
             if (s + turns > 0 && !wait(kTurn + s, (turns + s - 1) & 1)) return false;
             ++turns;
+            const uint32_t vs = uniform(v >= 0 ? v_slot(v) : 0), ks = uniform(k >= 0 ? k_slot(k) : 0), qa = uniform(dq0 + (q_at >> 4));
+            const uint32_t does = uniform((v >= 0) | (k >= 0) << 1 | end << 2 | both << 3 | !fresh << 4);
             if (elect_one()) {
-                if (v >= 0) {
-                    const int slot = v_slot(v);
-                    issue_values<D, PP>(tmem + 2 * TK + s * TK, tmem + s * TK, dv0 + static_cast<uint32_t>(slot * (TILE >> 4)), fresh, id_o);
-                    release(slot, both);
-                    if (end) tc::mma_commit(bar(kOFull + s));
+                if (does & 1) {
+                    issue_values<D, PP>(to, ts, dv0 + vs * (TILE >> 4), does >> 4, id_o);
+                    release(vs, does & 8);
+                    if (does & 4) tc::mma_commit(bar(kOFull + s));
                 }
-                if (k >= 0) {
-                    const int slot = k_slot(k);
-                    issue_scores<D, PQ>(tmem + s * TK, dq0 + (q_at >> 4), dk0 + static_cast<uint32_t>(slot * (TILE >> 4)), lo_at >> 4, box_at >> 4, id_s);
+                if (does & 2) {
+                    issue_scores<D, PQ>(ts, qa, dk0 + ks * (TILE >> 4), lo_at >> 4, box_at >> 4, id_s);
                     tc::mma_commit(bar(kSFull + s));
-                    release(slot, both);
+                    release(ks, does & 8);
                 }
                 mbar_arrive(bar(kTurn + (s ^ 1)));
             }
@@ -950,8 +973,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     // ---- the piece's partial ----
                     float* slot = p.ws + static_cast<size_t>(x.c.h * p.row_blocks + x.c.rb + w) * prefix_slot_floats(p.slot_rows, D) + s * TK + r;
+                    constexpr int SR = 2 * TK;  // p.slot_rows
                     __stcg(slot, ml.x);
-                    __stcg(slot + p.slot_rows, ml.y);
+                    __stcg(slot + SR, ml.y);
                     ok = wait(kOFull + s, no[s] & 1);
                     if (!ok) break;
                     ++no[s];
@@ -962,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float o[32];
                             wide::tmem_ld_rows<32>(to + 32 * c, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) __stcg(slot + static_cast<size_t>(2 + 32 * c + e) * p.slot_rows, o[e]);
+                            for (int e = 0; e < 32; ++e) __stcg(slot + (2 + 32 * c + e) * SR, o[e]);
                         }
                         tc::tc_fence_before();
                     }
@@ -982,6 +1006,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        quarter - q0, 4 - q0);
                     fence_proxy_async_smem();
                 };
+                auto fetch_next = [&](const OwnWalk& from, int to_buf) {
+                    OwnWalk nx = from;
+                    nx.next_segment(p, lane);
+                    fetch_q(nx, to_buf, 1);
+                };
                 if (n > 0) fetch_q(k, 0, 0);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kStart));
@@ -991,21 +1020,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < n; ++i) {
                     const bool end = k.tile + 1 == k.nt || i + 1 == n;
                     if (quarter > 0) {
-                        // no row of its own: the next segment's q, while the piece's first scores are made
-                        if (fresh && n - i > k.nt - k.tile) {
-                            OwnWalk nx = k;
-                            nx.next_segment(p, lane);
-                            // (the buffer's last reader was the piece before, whose scores are done when this piece's are)
-                            ok = wait(kSFull + s, ns & 1);
-                            if (!ok) break;
-                            fetch_q(nx, buf ^ 1, 1);
-                        } else {
-                            ok = wait(kSFull + s, ns & 1);
-                            if (!ok) break;
-                        }
+                        // no row of its own: the next segment's q, at the piece's first tile (the buffer's last reader was the piece
+                        // before, whose scores are done when this piece's are), behind its weights where another tile follows
+                        const bool next_q = fresh && n - i > k.nt - k.tile;
+                        ok = wait(kSFull + s, ns & 1);
+                        if (!ok) break;
                         ++ns;
+                        if (next_q && end) fetch_next(k, buf ^ 1);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kPFull + s));
+                        if (next_q && !end) fetch_next(k, buf ^ 1);
                     } else {
                         if (fresh) ml = make_float2(kNone, 0.f);
                         ok = wait(kSFull + s, ns & 1);

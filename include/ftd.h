@@ -572,8 +572,8 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  * FTD_ERR_BAD_PAGE, and what the slots see of it is undefined.
  * fp16 and bf16 caches: the tensor cores take the weights rounded to that type where out is a
  * 16-bit type, and q as it is where it is of the cache's type and has no bias; else each as a
- * pair of its numbers (about 16 mantissa bits with bf16), as ftd_decode_mha does.  Launches two
- * kernels where such a cache has at most 32 query rows per slot and kv head (T * Hq / Hkv), else three.
+ * pair of its numbers (about 16 mantissa bits with bf16), as ftd_decode_mha does.  Launches two or
+ * three kernels: the slots' own rows are taken beside the prefix or by the step's kernel.
  */
 ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new, const void* qkv_bias,
                                  void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
