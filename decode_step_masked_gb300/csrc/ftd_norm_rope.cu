@@ -10,8 +10,10 @@
 //
 // Bound: each head is read and written once; the norm's sum needs the whole head before the first
 // product, so a head stays in registers: D / 16 neighbouring lanes hold 16 elements each (eight
-// pairs) and exchange their sums in two or three shuffles.  A block takes a tile of tokens, forms
-// their cosines, sines and cache rows once in shared memory and applies them to all its heads.
+// pairs) and exchange their sums in two or three shuffles.  A lane keeps its head and walks the tokens,
+// its bias and weights in registers as fp32 (read anew for every token they cost half of the instructions, and
+// the kernel was bound by those: 169 us for the prompt below); the next token's loads go out before the present one is
+// worked on.  A block takes a tile of tokens and forms their cosines, sines and cache rows once in shared memory.
 #include <cuda_runtime.h>
 
 #include "ftd_internal.cuh"
@@ -21,9 +23,8 @@
 namespace ftd {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;   // most threads of a block
 constexpr int kNormTile = 16;         // most tokens of a tile
-constexpr int kNormTileItems = 5120;  // most units of a large call's tile
 
 // VEC fp32 values to elements i .. of an array of type dt (kF32, kF16, kBF16), rounded to nearest even.
 template <int VEC>
@@ -69,11 +70,10 @@ __device__ __forceinline__ void st_codes(unsigned char* base, long long i, const
 
 // LPH: lanes of a head (D / 16); VEC: elements per access.
 template <typename T, int LPH, int VEC>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int D = 16 * LPH;
     constexpr int NU = 8 / VEC;       // units of a lane: two runs of VEC elements, the pairs of one or neighbours
     constexpr int ITEMS = LPH * NU;   // units of a head
-    constexpr int U = NU == 1 ? 2 : 1;  // heads of a lane in flight
     __shared__ __align__(16) float cs[2][kNormTile][64], sn[2][kNormTile][64];
     __shared__ long long crow[2][kNormTile];  // cache row of head 0 of a token, -1: none
     __shared__ uint64_t step[64];
@@ -81,20 +81,63 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
     const int lane = threadIdx.x & 31, hl = lane & (LPH - 1);
     const int half = p.R >> 1;
     const int turning = half / VEC;   // units of a head that turn
-    const int h0 = blockIdx.y * p.heads_per_block;
-    const int H = min(p.heads_per_block, p.heads - h0);
-    for (int i = threadIdx.x; i < half; i += kNormThreads) {
+    for (int i = threadIdx.x; i < half; i += blockDim.x) {
         step[i] = p.step[i];
         axis[i] = p.axis[i];
     }
-    const uint32_t div = p.div_h[blockIdx.y == gridDim.y - 1];
+    // this lane's head (the last block's idle lanes follow the last head, without storing)
+    const int at = blockIdx.y * p.heads_per_block + static_cast<int>(threadIdx.x) / LPH;
+    const bool active = at < p.heads && static_cast<int>(threadIdx.x) / LPH < p.heads_per_block;
+    const int head = min(at, p.heads - 1);
+    const bool isq = head < p.Hq, isk = !isq && head < p.Hq + p.Hkv, turns = isq || isk;
+    const int kvh = head - p.Hq - (isk ? 0 : p.Hkv);
+    const bool neighbours = p.adjacent || !turns;
+    const T* src = isq ? static_cast<const T*>(p.q) + static_cast<long long>(head) * D
+                       : static_cast<const T*>(isk ? p.k : p.v) + static_cast<long long>(kvh) * D;
+    const long long stride = isq ? p.q_stride : p.kv_stride;
+    const void* weight = isq ? p.qw : isk ? p.kw : nullptr;
+    const bool to_cache = p.slots && !isq;
+    float bias[2 * NU][VEC], wt[2 * NU][VEC];
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+        int e2[2];
+        unit_at<VEC>(j * LPH + hl, turning, half, neighbours, e2[0], e2[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            Chunk<T, VEC> c;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) bias[2 * j + h][e] = wt[2 * j + h][e] = 0.f;
+            if (p.bias) {
+                c.load(static_cast<const T*>(p.bias) + static_cast<long long>(head) * D + e2[h]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) bias[2 * j + h][e] = to_f<T>(c.e[e]);
+            }
+            if (weight) {
+                c.load(static_cast<const T*>(weight) + e2[h]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) wt[2 * j + h][e] = to_f<T>(c.e[e]) + p.offset;
+            }
+        }
+    }
     int buf = 0;
     for (long long t0 = static_cast<long long>(blockIdx.x) * p.tile; t0 < p.n; t0 += static_cast<long long>(gridDim.x) * p.tile) {
         const int nt = static_cast<int>(min(static_cast<long long>(p.tile), p.n - t0));
-        for (int i = threadIdx.x; i < nt * half; i += kNormThreads) {
+        Chunk<T, VEC> x[2 * NU];
+        auto load = [&](int tok) {
+            const T* row = src + (t0 + tok) * stride;
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                int ea, eb;
+                unit_at<VEC>(j * LPH + hl, turning, half, neighbours, ea, eb);
+                x[2 * j].load(row + ea);
+                x[2 * j + 1].load(row + eb);
+            }
+        };
+        load(0);
+        for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
             const int tok = i / half, pair = i - tok * half;
             const int pos = __ldcg(p.pos + static_cast<long long>(axis[pair]) * p.n + t0 + tok);
             float s, c;
@@ -110,146 +153,100 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
             crow[buf][threadIdx.x] = r;
         }
         __syncthreads();  // (the other buffer is written only after every thread has passed here again)
-        const int total = nt * H * LPH;
-        // whole warps go round together: the sums are exchanged between lanes
-        for (int base = threadIdx.x - lane; base < total; base += U * kNormThreads) {
-            Chunk<T, VEC> x[U][2 * NU], bs[U][2 * NU], wt[U][2 * NU];
-            int tk[U], hd[U];
+#pragma unroll 1
+        for (int tok = 0; tok < nt; ++tok) {
+            float y[2 * NU][VEC];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int idx = base + u * kNormThreads + lane;
-                const int hh = min(idx, total - 1) / LPH;
-                const int tok = div ? static_cast<int>(__umulhi(static_cast<uint32_t>(hh), div)) : hh;  // hh / H
-                const int head = h0 + hh - tok * H;
-                tk[u] = idx < total ? tok : -1;
-                hd[u] = head;
-                const long long t = t0 + tok;
-                const T* src;
-                const void* w = nullptr;
-                if (head < p.Hq) {
-                    src = static_cast<const T*>(p.q) + t * p.q_stride + static_cast<long long>(head) * D;
-                    w = p.qw;
-                } else if (head < p.Hq + p.Hkv) {
-                    src = static_cast<const T*>(p.k) + t * p.kv_stride + static_cast<long long>(head - p.Hq) * D;
-                    w = p.kw;
-                } else {
-                    src = static_cast<const T*>(p.v) + t * p.kv_stride + static_cast<long long>(head - p.Hq - p.Hkv) * D;
-                }
+            for (int j = 0; j < 2 * NU; ++j)
 #pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    int ea, eb;
-                    unit_at<VEC>(j * LPH + hl, turning, half, p.adjacent || head >= p.Hq + p.Hkv, ea, eb);
-                    x[u][2 * j].load(src + ea);
-                    x[u][2 * j + 1].load(src + eb);
-                    if (p.bias) {
-                        const T* bp = static_cast<const T*>(p.bias) + static_cast<long long>(head) * D;
-                        bs[u][2 * j].load(bp + ea);
-                        bs[u][2 * j + 1].load(bp + eb);
-                    }
-                    if (w) {
-                        wt[u][2 * j].load(static_cast<const T*>(w) + ea);
-                        wt[u][2 * j + 1].load(static_cast<const T*>(w) + eb);
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int head = hd[u], tok = max(tk[u], 0);
-                const bool isq = head < p.Hq, isk = !isq && head < p.Hq + p.Hkv;
-                float y[2 * NU][VEC];
+                for (int e = 0; e < VEC; ++e) y[j][e] = to_f<T>(x[j].e[e]) + bias[j][e];
+            if (tok + 1 < nt) load(tok + 1);
+            if (weight) {  // (a head's lanes come here together, and so do all lanes of the mask)
                 float ss = 0.f;
 #pragma unroll
                 for (int j = 0; j < 2 * NU; ++j)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        y[j][e] = to_f<T>(x[u][j].e[e]);
-                        if (p.bias) y[j][e] += to_f<T>(bs[u][j].e[e]);
-                        ss = fmaf(y[j][e], y[j][e], ss);
-                    }
+                    for (int e = 0; e < VEC; ++e) ss = fmaf(y[j][e], y[j][e], ss);
+                const unsigned lanes = ((1u << LPH) - 1u) << (lane & ~(LPH - 1));
 #pragma unroll
-                for (int m = LPH / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                if ((isq && p.qw) || (isk && p.kw)) {
-                    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+                for (int m = LPH / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(lanes, ss, m);
+                const float r = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+                for (int j = 0; j < 2 * NU; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) y[j][e] = y[j][e] * r * wt[j][e];
+            }
+            if (turns) {
+#pragma unroll
+                for (int j = 0; j < NU; ++j) {
+                    const int unit = j * LPH + hl;
+                    if (unit >= turning) continue;
+                    float c[VEC], s[VEC];
+                    if constexpr (VEC < 4) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            c[e] = cs[buf][tok][unit * VEC + e];
+                            s[e] = sn[buf][tok][unit * VEC + e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int q4 = 0; q4 < VEC / 4; ++q4) {
+                            *reinterpret_cast<float4*>(c + 4 * q4) =
+                                *reinterpret_cast<const float4*>(&cs[buf][tok][(q4 * ITEMS + unit) * 4]);
+                            *reinterpret_cast<float4*>(s + 4 * q4) =
+                                *reinterpret_cast<const float4*>(&sn[buf][tok][(q4 * ITEMS + unit) * 4]);
+                        }
+                    }
+                    turn_pairs<VEC>(y[2 * j], y[2 * j + 1], c, s, p.adjacent);
+                }
+            }
+            // where the row goes
+            if (!to_cache) {
+                if (!active) continue;
+                const long long t = t0 + tok;
+                T* dst;
+                if (isq) dst = static_cast<T*>(p.qo) + (t * p.Hq + head) * D;
+                else dst = static_cast<T*>(isk ? p.ko : p.vo) + (t * p.Hkv + kvh) * D;
+#pragma unroll
+                for (int j = 0; j < NU; ++j) {
+                    int ea, eb;
+                    unit_at<VEC>(j * LPH + hl, turning, half, neighbours, ea, eb);
+                    Chunk<T, VEC> o;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[2 * j][e]);
+                    o.store(dst + ea);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[2 * j + 1][e]);
+                    o.store(dst + eb);
+                }
+            } else {
+                const long long r0 = crow[buf][tok];
+                const long long row = r0 + static_cast<long long>(kvh) * p.unit;
+                unsigned char* cache = isk ? p.k_cache : p.v_cache;
+                float amax = 0.f;
+                if (p.cache_dt == kCacheI8) {
 #pragma unroll
                     for (int j = 0; j < 2 * NU; ++j)
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) y[j][e] = y[j][e] * r * (to_f<T>(wt[u][j].e[e]) + p.offset);
+                        for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[j][e]));
+                    // (a head's lanes come here together, so only they take part)
+                    const unsigned lanes = ((1u << LPH) - 1u) << (lane & ~(LPH - 1));
+#pragma unroll
+                    for (int m = LPH / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, m));
                 }
-                if (isq || isk) {
+                if (!active || r0 < 0) continue;
+                const float scale = amax == 0.f ? 1.f : __fdiv_rn(amax, 127.f);
+                if (p.cache_dt == kCacheI8 && hl == 0) (isk ? p.k_scales : p.v_scales)[row] = scale;
 #pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        const int unit = j * LPH + hl;
-                        if (unit >= turning) continue;
-                        float c[VEC], s[VEC];
-                        if constexpr (VEC < 4) {
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) {
-                                c[e] = cs[buf][tok][unit * VEC + e];
-                                s[e] = sn[buf][tok][unit * VEC + e];
-                            }
-                        } else {
-#pragma unroll
-                            for (int q4 = 0; q4 < VEC / 4; ++q4) {
-                                *reinterpret_cast<float4*>(c + 4 * q4) =
-                                    *reinterpret_cast<const float4*>(&cs[buf][tok][(q4 * ITEMS + unit) * 4]);
-                                *reinterpret_cast<float4*>(s + 4 * q4) =
-                                    *reinterpret_cast<const float4*>(&sn[buf][tok][(q4 * ITEMS + unit) * 4]);
-                            }
-                        }
-                        turn_pairs<VEC>(y[2 * j], y[2 * j + 1], c, s, p.adjacent);
-                    }
-                }
-                // where the row goes
-                if (isq || !p.slots) {
-                    if (tk[u] < 0) continue;
-                    const long long t = t0 + tok;
-                    T* dst;
-                    if (isq) dst = static_cast<T*>(p.qo) + (t * p.Hq + head) * D;
-                    else if (isk) dst = static_cast<T*>(p.ko) + (t * p.Hkv + head - p.Hq) * D;
-                    else dst = static_cast<T*>(p.vo) + (t * p.Hkv + head - p.Hq - p.Hkv) * D;
-#pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        int ea, eb;
-                        unit_at<VEC>(j * LPH + hl, turning, half, p.adjacent || !(isq || isk), ea, eb);
-                        Chunk<T, VEC> o;
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[2 * j][e]);
-                        o.store(dst + ea);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[2 * j + 1][e]);
-                        o.store(dst + eb);
-                    }
-                } else {
-                    const int kvh = head - p.Hq - (isk ? 0 : p.Hkv);
-                    const long long r0 = crow[buf][tok];
-                    const long long row = r0 + static_cast<long long>(kvh) * p.unit;
-                    const bool live = tk[u] >= 0 && r0 >= 0;
-                    unsigned char* cache = isk ? p.k_cache : p.v_cache;
-                    float amax = 0.f;
+                for (int j = 0; j < NU; ++j) {
+                    int ea, eb;
+                    unit_at<VEC>(j * LPH + hl, turning, half, neighbours, ea, eb);
                     if (p.cache_dt == kCacheI8) {
-#pragma unroll
-                        for (int j = 0; j < 2 * NU; ++j)
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[j][e]));
-                        // (a head's lanes come here together, so only they take part)
-                        const unsigned lanes = ((1u << LPH) - 1u) << (lane & ~(LPH - 1));
-#pragma unroll
-                        for (int m = LPH / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, m));
-                    }
-                    if (!live) continue;
-                    const float scale = amax == 0.f ? 1.f : __fdiv_rn(amax, 127.f);
-                    if (p.cache_dt == kCacheI8 && hl == 0) (isk ? p.k_scales : p.v_scales)[row] = scale;
-#pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        int ea, eb;
-                        unit_at<VEC>(j * LPH + hl, turning, half, p.adjacent || !isk, ea, eb);
-                        if (p.cache_dt == kCacheI8) {
-                            st_codes<VEC>(cache, row * D + ea, y[2 * j], scale, amax == 0.f);
-                            st_codes<VEC>(cache, row * D + eb, y[2 * j + 1], scale, amax == 0.f);
-                        } else {
-                            st_vals<VEC>(cache, row * D + ea, y[2 * j], p.cache_dt);
-                            st_vals<VEC>(cache, row * D + eb, y[2 * j + 1], p.cache_dt);
-                        }
+                        st_codes<VEC>(cache, row * D + ea, y[2 * j], scale, amax == 0.f);
+                        st_codes<VEC>(cache, row * D + eb, y[2 * j + 1], scale, amax == 0.f);
+                    } else {
+                        st_vals<VEC>(cache, row * D + ea, y[2 * j], p.cache_dt);
+                        st_vals<VEC>(cache, row * D + eb, y[2 * j + 1], p.cache_dt);
                     }
                 }
             }
@@ -275,12 +272,18 @@ const void* pick(int D, int vec) {
 
 cudaError_t launch_norm_rope(NormRopeParams p, int vec, int sms, cudaStream_t stream) {
     const void* fn = p.dt == kF32 ? pick<float>(p.D, vec) : p.dt == kF16 ? pick<__half>(p.D, vec) : pick<__nv_bfloat16>(p.D, vec);
-    plan_rope(p, p.heads * (p.D / (2 * vec)), kNormTile, kNormTileItems, sms);
-    const long long tiles = (p.n + p.tile - 1) / p.tile, cap = static_cast<long long>(sms) * 8;
-    const int gy = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
+    // Heads of a block: as many as its threads take, evenly, whole warps of them; one warp's where there are few tokens.
+    const int lph = p.D / 16, per_warp = 32 / lph;
+    const int most = p.n * p.heads < static_cast<long long>(sms) * kNormThreads / lph ? per_warp : kNormThreads / lph;
+    const int gy = (p.heads + most - 1) / most;
+    p.heads_per_block = ((p.heads + gy - 1) / gy + per_warp - 1) / per_warp * per_warp;
+    // Tokens of a tile: fewer where that would leave an SM fewer than two blocks.  Blocks: about six an SM, which walk the tiles.
+    p.tile = kNormTile;
+    while (p.tile > 1 && (p.n + p.tile - 1) / p.tile * gy < 2LL * sms) p.tile >>= 1;
+    const long long tiles = (p.n + p.tile - 1) / p.tile, cap = (6LL * sms + gy - 1) / gy;
     const dim3 grid(static_cast<unsigned>(tiles < cap ? tiles : cap), static_cast<unsigned>(gy));
     void* args[] = {&p};
-    return launch_pdl(fn, grid, kNormThreads, 0, args, stream);
+    return launch_pdl(fn, grid, p.heads_per_block * lph, 0, args, stream);
 }
 
 }  // namespace ftd
