@@ -16,6 +16,8 @@
 // worked on.  A block takes a tile of tokens and forms their cosines, sines and cache rows once in shared memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "ftd_internal.cuh"
 #include "ftd_ops.cuh"
 #include "ftd_rope.cuh"
@@ -25,6 +27,73 @@ namespace {
 
 constexpr int kNormThreads = 256;   // most threads of a block
 constexpr int kNormTile = 16;         // most tokens of a tile
+
+// Two fp32 values that the packed forms take at once (a lane's arithmetic is most of its instructions).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ void add_to(float (&y)[VEC], const float (&b)[VEC]) {
+    if constexpr (VEC == 1) y[0] += b[0];
+    else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) unpack2(add2(pack2(y[e], y[e + 1]), pack2(b[e], b[e + 1])), y[e], y[e + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ uint64_t squares(const float (&y)[VEC], uint64_t sum) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+        const uint64_t v = pack2(y[e], VEC == 1 ? 0.f : y[(e + 1) % VEC]);
+        sum = fma2(v, v, sum);
+    }
+    return sum;
+}
+template <int VEC>
+__device__ __forceinline__ void weigh(float (&y)[VEC], float r, const float (&w)[VEC]) {
+    if constexpr (VEC == 1) y[0] = y[0] * r * w[0];
+    else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2)
+            unpack2(mul2(mul2(pack2(y[e], y[e + 1]), pack2(r, r)), pack2(w[e], w[e + 1])), y[e], y[e + 1]);
+    }
+}
+// (a, b) -> (a c - b s, b c + a s); sn holds s and, for the packed form, b's products take their sign in the last step
+template <int VEC>
+__device__ __forceinline__ void turn(float (&a)[VEC], float (&b)[VEC], const float (&c)[VEC], const float (&s)[VEC], bool adjacent) {
+    if (VEC == 1 || adjacent) {
+        turn_pairs<VEC>(a, b, c, s, adjacent);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC / 2 * 2; e += 2) {
+        const uint64_t c2 = pack2(c[e], c[e + 1]), s2 = pack2(s[e], s[e + 1]);
+        const uint64_t a2 = pack2(a[e], a[e + 1]), b2 = pack2(b[e], b[e + 1]);
+        float t0, t1;
+        unpack2(mul2(b2, s2), t0, t1);
+        unpack2(fma2(a2, s2, mul2(b2, c2)), b[e], b[e + 1]);
+        a[e] = fmaf(a[e], c[e], -t0);
+        a[e + 1] = fmaf(a[e + 1], c[e + 1], -t1);
+    }
+}
 
 // VEC fp32 values to elements i .. of an array of type dt (kF32, kF16, kBF16), rounded to nearest even.
 template <int VEC>
@@ -53,14 +122,38 @@ __device__ __forceinline__ void st_vals(void* base, long long i, const float (&x
     }
 }
 
-// VEC codes of a row with the given scale to bytes i ..
+__device__ __noinline__ uint32_t code_by_quotient(float x, float scale) {
+    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(__fdiv_rn(x, scale))))) & 0xffu;
+}
+
+// VEC codes rint(x / scale) of a row with the given scale (inv: its reciprocal) to bytes i ..  x inv differs from the
+// quotient by at most 127 * 2^-22, so it rounds to the same code unless it lies that near to a half; then, one value of
+// thousands, and for values that are no numbers, the quotients themselves are formed.  |x / scale| < 127.5, so the code is
+// the low byte of x inv + 1.5 * 2^23.
 template <int VEC>
-__device__ __forceinline__ void st_codes(unsigned char* base, long long i, const float (&x)[VEC], float scale, bool zero) {
-    uint32_t w[(VEC + 3) / 4] = {};
+__device__ __forceinline__ void st_codes(unsigned char* base, long long i, const float (&x)[VEC], float scale, float inv) {
+    constexpr float kShift = 12582912.f;
+    float m[VEC], off = 0.f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        const int code = zero ? 0 : max(-127, min(127, __float2int_rn(__fdiv_rn(x[e], scale))));
-        w[e / 4] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (e % 4));
+        m[e] = fmaf(x[e], inv, kShift);
+        const float d = fabsf(fmaf(x[e], inv, kShift - m[e]));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(off) : "f"(d));
+    }
+    uint32_t w[(VEC + 3) / 4] = {};
+    if (off < 0.4999f) {
+        if constexpr (VEC >= 4) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4)
+                w[e / 4] = __byte_perm(__byte_perm(__float_as_uint(m[e]), __float_as_uint(m[e + 1]), 0x0040),
+                                       __byte_perm(__float_as_uint(m[e + 2]), __float_as_uint(m[e + 3]), 0x0040), 0x5410);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[0] |= (__float_as_uint(m[e]) & 0xffu) << (8 * e);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e / 4] |= code_by_quotient(x[e], scale) << (8 * (e % 4));
     }
     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(base + i) = make_uint2(w[0], w[1]);
     else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(base + i) = w[0];
@@ -97,31 +190,30 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid
     const long long stride = isq ? p.q_stride : p.kv_stride;
     const void* weight = isq ? p.qw : isk ? p.kw : nullptr;
     const bool to_cache = p.slots && !isq;
+    int at_e[2 * NU];  // elements of the head where this lane's runs begin
+#pragma unroll
+    for (int j = 0; j < NU; ++j) unit_at<VEC>(j * LPH + hl, turning, half, neighbours, at_e[2 * j], at_e[2 * j + 1]);
     float bias[2 * NU][VEC], wt[2 * NU][VEC];
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
-        int e2[2];
-        unit_at<VEC>(j * LPH + hl, turning, half, neighbours, e2[0], e2[1]);
+    for (int j = 0; j < 2 * NU; ++j) {
+        Chunk<T, VEC> c;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Chunk<T, VEC> c;
+        for (int e = 0; e < VEC; ++e) bias[j][e] = wt[j][e] = 0.f;
+        if (p.bias) {
+            c.load(static_cast<const T*>(p.bias) + static_cast<long long>(head) * D + at_e[j]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) bias[2 * j + h][e] = wt[2 * j + h][e] = 0.f;
-            if (p.bias) {
-                c.load(static_cast<const T*>(p.bias) + static_cast<long long>(head) * D + e2[h]);
+            for (int e = 0; e < VEC; ++e) bias[j][e] = to_f<T>(c.e[e]);
+        }
+        if (weight) {
+            c.load(static_cast<const T*>(weight) + at_e[j]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) bias[2 * j + h][e] = to_f<T>(c.e[e]);
-            }
-            if (weight) {
-                c.load(static_cast<const T*>(weight) + e2[h]);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) wt[2 * j + h][e] = to_f<T>(c.e[e]) + p.offset;
-            }
+            for (int e = 0; e < VEC; ++e) wt[j][e] = to_f<T>(c.e[e]) + p.offset;
         }
     }
+    const int inv_half = half ? (65535 + half) / half : 0;  // i / half = (i * inv_half) >> 16 for i < 64 kNormTile
     int buf = 0;
     for (long long t0 = static_cast<long long>(blockIdx.x) * p.tile; t0 < p.n; t0 += static_cast<long long>(gridDim.x) * p.tile) {
         const int nt = static_cast<int>(min(static_cast<long long>(p.tile), p.n - t0));
@@ -129,16 +221,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid
         auto load = [&](int tok) {
             const T* row = src + (t0 + tok) * stride;
 #pragma unroll
-            for (int j = 0; j < NU; ++j) {
-                int ea, eb;
-                unit_at<VEC>(j * LPH + hl, turning, half, neighbours, ea, eb);
-                x[2 * j].load(row + ea);
-                x[2 * j + 1].load(row + eb);
-            }
+            for (int j = 0; j < 2 * NU; ++j) x[j].load(row + at_e[j]);
         };
         load(0);
         for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-            const int tok = i / half, pair = i - tok * half;
+            const int tok = (i * inv_half) >> 16, pair = i - tok * half;
             const int pos = __ldcg(p.pos + static_cast<long long>(axis[pair]) * p.n + t0 + tok);
             float s, c;
             turn_sincos(pos, step[pair], &s, &c);
@@ -159,22 +246,23 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < 2 * NU; ++j)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) y[j][e] = to_f<T>(x[j].e[e]) + bias[j][e];
+                for (int e = 0; e < VEC; ++e) y[j][e] = to_f<T>(x[j].e[e]);
+#pragma unroll
+            for (int j = 0; j < 2 * NU; ++j) add_to<VEC>(y[j], bias[j]);
             if (tok + 1 < nt) load(tok + 1);
             if (weight) {  // (a head's lanes come here together, and so do all lanes of the mask)
-                float ss = 0.f;
+                uint64_t two = 0;
 #pragma unroll
-                for (int j = 0; j < 2 * NU; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) ss = fmaf(y[j][e], y[j][e], ss);
+                for (int j = 0; j < 2 * NU; ++j) two = squares<VEC>(y[j], two);
+                float ss, other;
+                unpack2(two, ss, other);
+                ss += other;
                 const unsigned lanes = ((1u << LPH) - 1u) << (lane & ~(LPH - 1));
 #pragma unroll
                 for (int m = LPH / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(lanes, ss, m);
                 const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-                for (int j = 0; j < 2 * NU; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) y[j][e] = y[j][e] * r * wt[j][e];
+                for (int j = 0; j < 2 * NU; ++j) weigh<VEC>(y[j], r, wt[j]);
             }
             if (turns) {
 #pragma unroll
@@ -197,7 +285,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid
                                 *reinterpret_cast<const float4*>(&sn[buf][tok][(q4 * ITEMS + unit) * 4]);
                         }
                     }
-                    turn_pairs<VEC>(y[2 * j], y[2 * j + 1], c, s, p.adjacent);
+                    turn<VEC>(y[2 * j], y[2 * j + 1], c, s, p.adjacent);
                 }
             }
             // where the row goes
@@ -208,16 +296,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid
                 if (isq) dst = static_cast<T*>(p.qo) + (t * p.Hq + head) * D;
                 else dst = static_cast<T*>(isk ? p.ko : p.vo) + (t * p.Hkv + kvh) * D;
 #pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    int ea, eb;
-                    unit_at<VEC>(j * LPH + hl, turning, half, neighbours, ea, eb);
+                for (int j = 0; j < 2 * NU; ++j) {
                     Chunk<T, VEC> o;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[2 * j][e]);
-                    o.store(dst + ea);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[2 * j + 1][e]);
-                    o.store(dst + eb);
+                    for (int e = 0; e < VEC; ++e) o.e[e] = from_f<T>(y[j][e]);
+                    o.store(dst + at_e[j]);
                 }
             } else {
                 const long long r0 = crow[buf][tok];
@@ -236,18 +319,12 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const __grid
                 }
                 if (!active || r0 < 0) continue;
                 const float scale = amax == 0.f ? 1.f : __fdiv_rn(amax, 127.f);
+                const float inv = __frcp_rn(scale);
                 if (p.cache_dt == kCacheI8 && hl == 0) (isk ? p.k_scales : p.v_scales)[row] = scale;
 #pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    int ea, eb;
-                    unit_at<VEC>(j * LPH + hl, turning, half, neighbours, ea, eb);
-                    if (p.cache_dt == kCacheI8) {
-                        st_codes<VEC>(cache, row * D + ea, y[2 * j], scale, amax == 0.f);
-                        st_codes<VEC>(cache, row * D + eb, y[2 * j + 1], scale, amax == 0.f);
-                    } else {
-                        st_vals<VEC>(cache, row * D + ea, y[2 * j], p.cache_dt);
-                        st_vals<VEC>(cache, row * D + eb, y[2 * j + 1], p.cache_dt);
-                    }
+                for (int j = 0; j < 2 * NU; ++j) {
+                    if (p.cache_dt == kCacheI8) st_codes<VEC>(cache, row * D + at_e[j], y[j], scale, inv);
+                    else st_vals<VEC>(cache, row * D + at_e[j], y[j], p.cache_dt);
                 }
             }
         }
@@ -272,15 +349,23 @@ const void* pick(int D, int vec) {
 
 cudaError_t launch_norm_rope(NormRopeParams p, int vec, int sms, cudaStream_t stream) {
     const void* fn = p.dt == kF32 ? pick<float>(p.D, vec) : p.dt == kF16 ? pick<__half>(p.D, vec) : pick<__nv_bfloat16>(p.D, vec);
-    // Heads of a block: as many as its threads take, evenly, whole warps of them; one warp's where there are few tokens.
+    // Heads of a block: as many as its threads take, whole warps of them and evenly, so that few lanes idle (at most
+    // twice the blocks for that); one warp's where there are few tokens.
     const int lph = p.D / 16, per_warp = 32 / lph;
     const int most = p.n * p.heads < static_cast<long long>(sms) * kNormThreads / lph ? per_warp : kNormThreads / lph;
-    const int gy = (p.heads + most - 1) / most;
-    p.heads_per_block = ((p.heads + gy - 1) / gy + per_warp - 1) / per_warp * per_warp;
-    // Tokens of a tile: fewer where that would leave an SM fewer than two blocks.  Blocks: about six an SM, which walk the tiles.
+    int gy = (p.heads + most - 1) / most;
+    auto heads_of = [&](int g) { return ((p.heads + g - 1) / g + per_warp - 1) / per_warp * per_warp; };
+    for (int g = gy + 1, until = 2 * gy; g <= until; ++g)
+        if (g * heads_of(g) < gy * heads_of(gy)) gy = g;
+    p.heads_per_block = heads_of(gy);
+    gy = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
+    // Tokens of a tile: fewer where that would leave an SM fewer than two blocks.  As many blocks as are resident at once
+    // (two of 256 threads an SM) walk the tiles, each as many.
     p.tile = kNormTile;
     while (p.tile > 1 && (p.n + p.tile - 1) / p.tile * gy < 2LL * sms) p.tile >>= 1;
-    const long long tiles = (p.n + p.tile - 1) / p.tile, cap = (6LL * sms + gy - 1) / gy;
+    const long long tiles = (p.n + p.tile - 1) / p.tile;
+    const long long at_once = std::max(1LL, 6LL * kNormThreads / (p.heads_per_block * lph) * sms / gy);
+    const long long each = (tiles + at_once - 1) / at_once, cap = (tiles + each - 1) / each;
     const dim3 grid(static_cast<unsigned>(tiles < cap ? tiles : cap), static_cast<unsigned>(gy));
     void* args[] = {&p};
     return launch_pdl(fn, grid, p.heads_per_block * lph, 0, args, stream);
