@@ -31,27 +31,25 @@ namespace {
 constexpr int kTabThreads = kMaxBatch;  // one thread a slot in the scans
 constexpr int kTabTokens = 4;           // tokens of a thread at a time
 
-// Inclusive sum over the block's threads; total over all of them.  Two barriers.
-template <typename V>
-__device__ __forceinline__ V block_scan(V v, V* warp_sums, V& total) {
+// Inclusive sum over the block's threads; total over all of them.  One barrier; warp_sums is this scan's own.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const V y = __shfl_up_sync(0xffffffffu, v, m);
+        const long long y = __shfl_up_sync(0xffffffffu, v, m);
         if (lane >= m) v += y;
     }
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    V w = warp_sums[lane];
+    long long w = lane < static_cast<int>(blockDim.x) / 32 ? warp_sums[lane] : 0;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const V y = __shfl_up_sync(0xffffffffu, w, m);
+        const long long y = __shfl_up_sync(0xffffffffu, w, m);
         if (lane >= m) w += y;
     }
     total = __shfl_sync(0xffffffffu, w, 31);
-    const V before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);  // the warps before this one's
-    __syncthreads();
-    return v + (warp ? before : V(0));
+    const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);  // the warps before this one's
+    return v + (warp ? before : 0);
 }
 
 // Largest i of [0, n) with first[i] <= x, for first[0] <= x.
@@ -66,6 +64,61 @@ __device__ __forceinline__ int last_at_most(const V* first, int n, V x) {
     return lo;
 }
 
+// The map's elements, N neighbours to a thread.  A warp has a run of its own, so the slot and the page of the last round
+// mostly are this one's too.  page_of(s, e) is the page of entry e of slot s.
+template <int N, typename PageOf>
+__device__ __forceinline__ void write_map(const TablesParams& p, long long warp, long long warps, long long tokens, const int* start,
+                                          const long long* first, PageOf page_of) {
+    constexpr int kRound = 32 * N;
+    const int mask = (1 << p.page_shift) - 1;
+    const long long rounds = (p.cap + kRound - 1) / kRound, each = (rounds + warps - 1) / warps;
+    const long long end = min(p.cap, (warp + 1) * each * kRound);
+    int s = -1, entry = -1, page = 0;
+#pragma unroll 1
+    for (long long t0 = warp * each * kRound + (threadIdx.x & 31) * N; t0 < end; t0 += kRound) {
+        int at[N], ps[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const long long t = t0 + i;
+            at[i] = -1;
+            ps[i] = 0;
+            if (t >= tokens) continue;
+            if (s < 0 || first[s + 1] <= t) {
+                const int from = s + 1;  // (first[from] <= t)
+                s = from + last_at_most(first + from, p.B + 1 - from, t);
+                entry = -1;
+            }
+            const int pos = start[s] + static_cast<int>(t - first[s]);
+            ps[i] = pos;
+            if (!p.block_table) {
+                at[i] = s * p.Lmax + pos;
+            } else {
+                const int e = pos >> p.page_shift;
+                if (e != entry) {
+                    entry = e;
+                    page = page_of(s, e);
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicOr(p.err, kErrBadPage);
+                        page = -1;
+                    }
+                }
+                if (page >= 0) at[i] = (page << p.page_shift) + (pos & mask);
+            }
+        }
+        if (N == 4 && t0 + N <= p.cap) {
+            if (p.slots) *reinterpret_cast<int4*>(p.slots + t0) = make_int4(at[0], at[1 % N], at[2 % N], at[3 % N]);
+            if (p.positions) *reinterpret_cast<int4*>(p.positions + t0) = make_int4(ps[0], ps[1 % N], ps[2 % N], ps[3 % N]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (t0 + i >= p.cap) break;
+                if (p.slots) p.slots[t0 + i] = at[i];
+                if (p.positions) p.positions[t0 + i] = ps[i];
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams p) {
     __shared__ int asked[kMaxBatch];      // pages asked for by the slots before
     __shared__ int back[kMaxBatch];       // pages given back by the slots before
@@ -73,8 +126,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     __shared__ int want[kMaxBatch];       // and after it
     __shared__ int start[kMaxBatch];      // rows before the call
     __shared__ long long first[kMaxBatch + 1];  // new tokens of the slots before
-    __shared__ int sums[32], sums2[32];
-    __shared__ long long lsums[32];
+    __shared__ long long page_sums[32], token_sums[32];
     __shared__ int s_grow, s_last;
     const int b = threadIdx.x;
     grid_dep_wait();
@@ -84,26 +136,24 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     // ---- one thread a slot: pages asked for and given back ----
     const bool slot = b < p.B;
     const int old_raw = slot ? __ldcg(p.old_lens + b) : 0, new_raw = slot ? __ldcg(p.new_lens + b) : 0;
+    const int free_raw = p.block_table ? __ldcg(p.n_free) : 0;
     const bool fits = old_raw <= p.Lmax && new_raw <= p.Lmax;
     const int L0 = fits ? max(old_raw, 0) : 0, L1 = fits ? max(new_raw, 0) : 0;
     const int ps1 = (1 << p.page_shift) - 1;
     const int h = p.block_table ? static_cast<int>((static_cast<long long>(L0) + ps1) >> p.page_shift) : 0;
     int w = p.block_table ? static_cast<int>((static_cast<long long>(L1) + ps1) >> p.page_shift) : 0;
     const int grow = max(0, w - h), give = max(0, h - w);
-    int A, F;
-    const int a_end = block_scan(grow, sums, A), f_end = block_scan(give, sums2, F);
-    int n_free = 0;
-    bool bad = false;
-    if (p.block_table) {
-        const int raw = __ldcg(p.n_free);
-        n_free = min(max(raw, 0), p.num_pages);
-        bad = raw != n_free;
-    }
+    // (both sums in one scan: a slot's pages and a call's fit 31 bits)
+    long long both;
+    const long long ends = block_scan(static_cast<long long>(grow) << 32 | give, page_sums, both);
+    const int a_end = static_cast<int>(ends >> 32), f_end = static_cast<int>(ends), F = static_cast<int>(both);
+    const int n_free = min(max(free_raw, 0), p.num_pages);
+    const bool bad = free_raw != n_free;
     const bool served = fits && (grow == 0 || a_end <= static_cast<long long>(n_free) + F);
     if (grow > 0 && served) atomicMax(&s_grow, a_end);
     if (!served) w = h;
     long long tokens;
-    const long long t_end = block_scan<long long>(served ? max(0, L1 - L0) : 0, lsums, tokens);
+    const long long t_end = block_scan(served ? max(0, L1 - L0) : 0, token_sums, tokens);
     if (slot) {
         asked[b] = a_end - grow;
         back[b] = f_end - give;
@@ -114,7 +164,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     }
     if (b == 0) first[0] = 0;
     __syncthreads();
-    A = s_grow;
+    const int A = s_grow;
 
     // ---- what may be updated in place: by the last block to have read it ----
     if (b == 0) {
@@ -145,12 +195,16 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
         return __ldcg(p.block_table + static_cast<size_t>(s) * p.per + want[s] + (f - back[s]));
     };
     auto page_for = [&](int a) -> int { return a < F ? given(F - 1 - a) : __ldcg(p.free_pages + n_free - 1 - (a - F)); };
-    const long long tid = static_cast<long long>(blockIdx.x) * kTabThreads + b;
-    const long long threads = static_cast<long long>(gridDim.x) * kTabThreads;
+    auto page_of = [&](int s, int e) -> int {
+        return e < held[s] ? __ldcg(p.block_table + static_cast<size_t>(s) * p.per + e) : page_for(asked[s] + (e - held[s]));
+    };
+    const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + b;
+    const long long threads = static_cast<long long>(gridDim.x) * blockDim.x;
 
     // ---- pages that change hands ----
     if (p.block_table) {
-        for (long long a = tid; a < A; a += threads) {
+        // (the last threads first: the first ones have the map's first tokens)
+        for (long long a = threads - 1 - tid; a < A; a += threads) {
             const int page = page_for(static_cast<int>(a));
             const int s = last_at_most(asked, p.B, static_cast<int>(a));
             if (page < 0 || page >= p.num_pages) atomicOr(p.err, kErrBadPage);
@@ -166,63 +220,22 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
 
     // ---- the slot map: new tokens packed in slot order, -1 behind them ----
     if (!p.slots && !p.positions) return;
-    const bool vec = p.vec;
-    for (long long t0 = tid * kTabTokens; t0 < p.cap; t0 += threads * kTabTokens) {
-        int at[kTabTokens], ps[kTabTokens];
-        int s = 0, entry = -1, page = 0;
-        if (t0 < tokens) s = last_at_most(first, p.B + 1, t0);
-#pragma unroll
-        for (int i = 0; i < kTabTokens; ++i) {
-            const long long t = t0 + i;
-            at[i] = -1;
-            ps[i] = 0;
-            if (t >= tokens) continue;
-            while (first[s + 1] <= t) {
-                ++s;
-                entry = -1;
-            }
-            const int pos = start[s] + static_cast<int>(t - first[s]);
-            ps[i] = pos;
-            if (!p.block_table) {
-                at[i] = s * p.Lmax + pos;
-            } else {
-                const int e = pos >> p.page_shift;
-                if (e != entry) {
-                    entry = e;
-                    page = e < held[s] ? __ldcg(p.block_table + static_cast<size_t>(s) * p.per + e)
-                                       : page_for(asked[s] + (e - held[s]));
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicOr(p.err, kErrBadPage);
-                        page = -1;
-                    }
-                }
-                if (page >= 0) at[i] = (page << p.page_shift) + (pos & ps1);
-            }
-        }
-        if (vec && t0 + kTabTokens <= p.cap) {
-            if (p.slots) *reinterpret_cast<int4*>(p.slots + t0) = make_int4(at[0], at[1], at[2], at[3]);
-            if (p.positions) *reinterpret_cast<int4*>(p.positions + t0) = make_int4(ps[0], ps[1], ps[2], ps[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kTabTokens; ++i) {
-                if (t0 + i >= p.cap) break;
-                if (p.slots) p.slots[t0 + i] = at[i];
-                if (p.positions) p.positions[t0 + i] = ps[i];
-            }
-        }
-    }
+    if (p.vec && p.cap > threads) write_map<kTabTokens>(p, tid >> 5, threads >> 5, tokens, start, first, page_of);
+    else write_map<1>(p, tid >> 5, threads >> 5, tokens, start, first, page_of);
 }
 
 }  // namespace
 
 cudaError_t launch_tables(TablesParams p, int sms, cudaStream_t stream) {
-    // a block's threads take four tokens each; a call without maps, a few entries each
-    const long long per_block = static_cast<long long>(kTabThreads) * kTabTokens;
+    // A thread a slot, 256 at the least; as many blocks as give each thread four tokens (a call without maps: four
+    // entries), 1024 threads an SM at the most.
+    const int threads = p.B <= 256 ? 256 : p.B <= 512 ? 512 : kTabThreads;
+    const long long per_block = static_cast<long long>(threads) * kTabTokens, most = static_cast<long long>(sms) * (kTabThreads / threads);
     const long long items = p.slots || p.positions ? p.cap : static_cast<long long>(p.B) * p.per;
     const long long blocks = (items + per_block - 1) / per_block;
-    const dim3 grid(static_cast<unsigned>(blocks < 1 ? 1 : blocks < sms ? blocks : sms));
+    const dim3 grid(static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most));
     void* args[] = {&p};
-    return launch_pdl(reinterpret_cast<const void*>(&tables_kernel), grid, kTabThreads, 0, args, stream);
+    return launch_pdl(reinterpret_cast<const void*>(&tables_kernel), grid, threads, 0, args, stream);
 }
 
 }  // namespace ftd
