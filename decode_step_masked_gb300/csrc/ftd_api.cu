@@ -1585,7 +1585,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     const bool i8 = c.cache_dtype == FTD_I8;
     ftd_status st = check_table(ctx, block_table, what);
     if (st != FTD_OK) return st;
-    if (prefix_rows < 0 || prefix_rows * c.n_kv_heads >= (static_cast<int64_t>(1) << 31) || prefix_rows >= (static_cast<int64_t>(1) << 31))
+    if (prefix_rows < 0 || prefix_rows >= (static_cast<int64_t>(1) << 31) || prefix_rows * c.n_kv_heads >= (static_cast<int64_t>(1) << 31))
         return fail(FTD_ERR_INVALID_ARG, "%s: prefix_rows %lld", what, static_cast<long long>(prefix_rows));
     if (!prefix_lens || !aligned(prefix_lens, 4) || !out || !aligned16(out))
         return fail(FTD_ERR_INVALID_ARG, "%s: prefix_lens (4-byte aligned) and out (16-byte aligned) must be non-NULL", what);

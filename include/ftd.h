@@ -97,7 +97,8 @@ typedef enum {
     FTD_ERR_CUDA = 4,            /* a CUDA runtime call failed */
     FTD_ERR_SEQ_OVERFLOW = 5,    /* some seq_lens[b] + q_len > max_len in a past call */
     FTD_ERR_DEVICE_TIMEOUT = 6,  /* a kernel gave up waiting for a copy (bounded wait) */
-    FTD_ERR_BAD_PAGE = 7         /* a block-table entry read in a past call was outside [0, num_pages) */
+    FTD_ERR_BAD_PAGE = 7         /* in a past call a block-table entry was outside [0, num_pages), or a token's
+                                    place or a count of free pages outside the cache (ftd_norm_rope_qkv, ftd_build_tables) */
 } ftd_status;
 
 typedef enum { FTD_F32 = 0, FTD_F16 = 1, FTD_BF16 = 2, FTD_I8 = 3 } ftd_dtype;
@@ -335,7 +336,7 @@ ftd_status ftd_debug_kernel(ftd_ctx* ctx, int entry, int* block_rows, int* tenso
  * the step of slots that share a prefix.  They take the context's shapes, types and caches, follow the
  * conventions above, launch on the caller's stream without allocating or
  * synchronising, and may be captured into a graph (after one call of
- * ftd_enable_scores, and of ftd_cross_mha, outside the capture).  Calls on one
+ * ftd_enable_scores, of ftd_enable_prefix, and of ftd_cross_mha, outside the capture).  Calls on one
  * context must not overlap in time, whichever entry points they are: graphs
  * captured from one context share its workspace too.
  */
@@ -539,9 +540,10 @@ ftd_status ftd_cross_mha(ftd_ctx* ctx, const void* q, const void* q_bias, const 
                          const int32_t* mem_lens, const float* scales, void* out, void* stream);
 
 /*
- * ftd_enable_prefix -- allocate the workspace of ftd_decode_mha_prefix: an fp32 copy of
- * out, two numbers per query row, and one partial block per SM and per kv head and block of query
- * rows.  One cudaMalloc, freed by ftd_destroy.  A second call does nothing.  UNSUPPORTED
+ * ftd_enable_prefix -- allocate the workspace of ftd_decode_mha_prefix: for each SM and for each
+ * kv head and block of query rows a partial result over the prefix; for the slots' own rows
+ * either an fp32 copy of out and two numbers per query row, or, where the prefix's kernel takes
+ * them too, two partial results per SM and one per slot and kv head.  One cudaMalloc, freed by ftd_destroy.  A second call does nothing.  UNSUPPORTED
  * above 32768 query rows per kv head (B * T * Hq / Hkv), INVALID_ARG with a window.
  */
 ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);

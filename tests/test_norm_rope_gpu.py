@@ -247,6 +247,56 @@ def test_fill_is_the_dense_rows(dt):
     step.close()
 
 
+@pytest.mark.parametrize("dt,shift", [("f16", 0), ("f16", 4), ("f32", 0), ("f32", 1), ("f32", 2)])
+def test_codes_are_rounded_quotients(dt, shift):
+    """INT8 codes are rint(x / absmax * 127) as IEEE divisions give it, exactly: halves and their neighbours (scales of
+    a power of two make x / scale a half), rows of any magnitude, zeros, infinities and NaN."""
+    import torch
+    n, D = 1500, 128
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((n, D)).astype(np.float32)
+    x[:700] *= np.exp2(rng.integers(-9, 9, (700, 1))).astype(np.float32)
+    half = rng.integers(-127, 127, (400, D)) + 0.5
+    half[:, 0] = 127.0  # the scale is 1, 2 or 1/4
+    half *= np.exp2(rng.integers(-2, 2, (400, 1)))
+    x[700:1100] = half
+    if dt == "f32":  # and one step on either side of a half
+        x[900:1100, 1:] = np.nextafter(x[900:1100, 1:], rng.choice([-1e9, 1e9], (200, D - 1)).astype(np.float32))
+    x[1100:1110] = 0.0
+    x[1110, 5] = np.inf
+    x[1111, 7] = np.nan
+    x[1112:1120] *= 1e-6
+    x = x.astype(np.float16).astype(np.float32) if dt == "f16" else x
+    step = ftd.DecodeStep(1, 1, 1, D, 1504, dt, "i8")
+    step.set_rope()
+    t = getattr(torch, TORCH[dt])
+    v = torch.zeros(n * D + shift, dtype=t, device="cuda")[shift:].view(n, D)
+    v.copy_(dev(x))
+    zero, out = torch.zeros((n, D), dtype=t, device="cuda"), torch.empty((n, D), dtype=t, device="cuda")
+    kc, vc = (torch.zeros((1, 1, 1504, D), dtype=torch.int8, device="cuda") for _ in range(2))
+    sc = torch.zeros((2, 1, 1, 1504), device="cuda")
+    step.norm_rope(zero, zero, v, dev(np.zeros((1, n), np.int32)), out, slots=dev(np.arange(n, dtype=np.int32)), k_cache=kc,
+                   v_cache=vc, scales=sc)
+    torch.cuda.synchronize()
+    assert step.get_error() == ftd.FTD_OK
+    ok = np.ones(n, bool)
+    ok[1110:1112] = False
+    amax = np.abs(x[ok]).max(1)
+    scale = np.where(amax == 0, np.float32(1), amax / np.float32(127)).astype(np.float32)
+    codes = np.rint(x[ok] / scale[:, None])
+    assert np.abs(codes).max() <= 127
+    assert np.array_equal(sc[1, 0, 0, :n].cpu().numpy()[ok], scale)
+    assert np.array_equal(vc[0, 0, :n].cpu().numpy()[ok], codes.astype(np.int8))
+    # beside an infinity the scale is infinite and every finite code is 0; beside a NaN the others are as without it
+    others = np.arange(D) != 5
+    assert np.isinf(float(sc[1, 0, 0, 1110])) and not vc[0, 0, 1110].cpu().numpy()[others].any()
+    others = np.arange(D) != 7
+    s = np.abs(x[1111, others]).max() / np.float32(127)
+    assert np.array_equal(vc[0, 0, 1111].cpu().numpy()[others], np.rint(x[1111, others] / s).astype(np.int8))
+    assert not kc.any() and bool((sc[0, 0, 0, :n] == 1).all())
+    step.close()
+
+
 def test_slots_past_the_end():
     """Slots past the cache write nothing and raise the error; the pool serves where no caches are given."""
     import torch

@@ -374,6 +374,10 @@ def test_refusals():
     for kw in (dict(), dict(block_table=i(2, 2), k_prefix=k, v_prefix=v), dict(block_table=i(2, 2), prefix_table=i(2).long())):
         with pytest.raises((ftd.FtdError, ValueError)):
             paged.prefix(**dict(ok, **kw))
+    a = [ok[x].data_ptr() for x in ("q", "k_new", "v_new", "seq_lens", "prefix_lens", "out")]
+    for rows in (-1, 1 << 30, 1 << 31, 1 << 62, (1 << 63) - 1):  # (times two heads)
+        assert ftd.ftd_decode_mha_prefix(flat.ctx, a[0], a[1], a[2], 0, 0, 0, 0, a[3], 0, k.data_ptr(), v.data_ptr(), 0, 0, rows,
+                                         a[4], a[5], 0) == ftd.FTD_ERR_INVALID_ARG
     assert ftd.ftd_kernel_launches() == n
     for s in (flat, paged, windowed, many):
         s.close()
