@@ -166,7 +166,7 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
                                  ((c.max_len + 127) / 128);
     const bool wide = half && D == 128 && rows_q % 32 == 0 && wide_tiles > kSmCount;
     if (mode != kStep && (D == 128 || D == 64) && !forced && encode_tiled() && (half || c.cache_dtype == FTD_I8) && !wide) {
-        // The scored step and cross attention: blocks of any size up to 16 rows (INT8: 8), the
+        // The scored step, cross attention and the step beside a prefix: blocks of any size up to 16 rows (INT8: 8), the
         // columns past them zero; the largest block that divides the rows, the CUDA cores when
         // that is too small to pay for the tensor cores.
         int blk = half ? 16 : 8;
@@ -176,8 +176,9 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
         const int Gt = blk > 8 ? 16 : 8;
         r.qblk = blk;
         r.nhb = rows_q / blk;
-        r.tki = mode == kScored ? (half ? select_tc_scored(bf, D, Gt, mt) : select_tc_i8_scored(D, mt))
-                                : (half ? select_tc_cross(bf, D, Gt, mt) : select_tc_i8_cross(D, mt));
+        r.tki = mode == kScored  ? (half ? select_tc_scored(bf, D, Gt, mt) : select_tc_i8_scored(D, mt))
+                : mode == kCross ? (half ? select_tc_cross(bf, D, Gt, mt) : select_tc_i8_cross(D, mt))
+                                 : (half ? select_tc_beside(bf, D, Gt, mt) : select_tc_i8_beside(D, mt));
         return r;
     }
     const bool want_tc = half && c.head_dim == 128 && rows_q % 4 == 0 && !forced;
@@ -189,6 +190,7 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
             r.qblk = rows_q % 64 == 0 ? 64 : 32;
             r.tki = mode == kScored  ? select_tc_scored(c.cache_dtype == FTD_BF16, D, r.qblk, c.q_len > 1)
                     : mode == kCross ? select_tc_cross(c.cache_dtype == FTD_BF16, D, r.qblk, c.q_len > 1)
+                    : mode == kBeside ? select_tc_beside(c.cache_dtype == FTD_BF16, D, r.qblk, c.q_len > 1)
                                      : select_wide(c.cache_dtype == FTD_BF16, r.qblk, c.q_len > 1);
         } else {
             const int Gt = (rows_q % 16 == 0 && !want_tc_i8) ? 16 : 8;
@@ -201,12 +203,14 @@ __attribute__((visibility("hidden"))) TcChoice choose_tc(const ftd_config& c, in
 }
 
 __attribute__((visibility("hidden"))) KernelInfo choose_cc(ftd_dtype dt, int D, int G, int mode) {
-    switch (dt) {
-        case FTD_F32: return mode == kScored ? select_f32_scored(D, G) : mode == kCross ? select_f32_cross(D, G) : select_f32(D, G);
-        case FTD_F16: return mode == kScored ? select_f16_scored(D, G) : mode == kCross ? select_f16_cross(D, G) : select_f16(D, G);
-        case FTD_BF16: return mode == kScored ? select_bf16_scored(D, G) : mode == kCross ? select_bf16_cross(D, G) : select_bf16(D, G);
-        case FTD_I8: return mode == kScored ? select_i8_scored(D, G) : mode == kCross ? select_i8_cross(D, G) : select_i8(D, G);
-    }
+    using Select = KernelInfo (*)(int, int);
+    static constexpr Select select[4][4] = {  // [mode][dt]
+        {select_f32, select_f16, select_bf16, select_i8},
+        {select_f32_scored, select_f16_scored, select_bf16_scored, select_i8_scored},
+        {select_f32_cross, select_f16_cross, select_bf16_cross, select_i8_cross},
+        {select_f32_beside, select_f16_beside, select_bf16_beside, select_i8_beside}};
+    static_assert(FTD_F32 == 0 && FTD_F16 == 1 && FTD_BF16 == 2 && FTD_I8 == 3, "order of the table");
+    if (mode >= kStep && mode <= kBeside && dt >= FTD_F32 && dt <= FTD_I8) return select[mode][dt](D, G);
     return KernelInfo{};
 }
 
@@ -409,7 +413,7 @@ struct ftd_ctx {
         bool ready = false;
         ftd::KernelInfo ki{};
         ftd::TcChoice tcc{};
-    } mode[3];
+    } mode[4];
     // ftd_enable_scores: workspace of ftd_decode_mha_scored and ftd_cache_evict
     void* sc_pool = nullptr;
     float* scores = nullptr;
@@ -658,7 +662,7 @@ static ftd_status cache_maps(ftd_ctx* ctx, void* k_cache, void* v_cache) {
 static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new,
                                 const void* bias, void* k_cache, void* v_cache, const int32_t* block_table,
                                 const int32_t* seq_lens, float* scales, void* out, cudaStream_t stream,
-                                bool proj = false, int mode = ftd::kStep, float2* stats = nullptr) {
+                                bool proj = false, int mode = ftd::kStep) {
     if (!k_cache) k_cache = ctx->k_cache;
     if (!v_cache) v_cache = ctx->v_cache;
     const bool i8 = ctx->cfg.cache_dtype == FTD_I8;
@@ -694,8 +698,7 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
     p.nhb = ctx->nhb;
     p.qkv_dtype = static_cast<int>(c.qkv_dtype);
     p.qscale = ctx->qscale;
-    p.out_dtype = stats ? ftd::kF32 : static_cast<int>(c.out_dtype);
-    p.stats = stats;
+    p.out_dtype = static_cast<int>(c.out_dtype);
     p.window = c.window;
     p.nq = ctx->nq;
     p.block_table = ctx->paged ? block_table : nullptr;
@@ -720,6 +723,10 @@ static ftd_status launch_decode(ftd_ctx* ctx, const void* q, const void* k_new, 
         // the softmax scale as a power of two, which leaves q's bits as they are, times the rest
         p.qscale = exp2f(floorf(log2f(ctx->qscale)));
         p.sscale = ctx->qscale / p.qscale;
+    }
+    if (mode == ftd::kBeside) {
+        p.stats = ctx->pre_ml;
+        p.out_dtype = ftd::kF32;
     }
     p.stall = 0;
     if (ctx->stall_calls > 0) {
@@ -1516,15 +1523,16 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     const size_t R = B * T * (Hq / Hkv);
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");
-    // fp16 and bf16 caches on the tensor cores
-    const bool half = c.cache_dtype == FTD_F16 || c.cache_dtype == FTD_BF16;
-    const bool tc = half && c.kernel != FTD_KERNEL_CUDA_CORE && encode_tiled();
+    // fp16, bf16 and INT8 caches on the tensor cores
+    const bool i8 = c.cache_dtype == FTD_I8;
+    const bool tc = c.cache_dtype != FTD_F32 && c.kernel != FTD_KERNEL_CUDA_CORE && (i8 || encode_tiled());
     if (R > 32768) return fail(FTD_ERR_UNSUPPORTED, "%s: %zu query rows per kv head, at most 32768", what, R);
     ftd::PrefixKernel k[3];
     size_t blocks = 0, ws = 0;
     for (int i = 0; i < 3; ++i) {
-        k[i] = tc ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i)
-                  : ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
+        k[i] = tc && i8 ? ftd::select_prefix_tc_i8(c.qkv_dtype == FTD_BF16, c.head_dim, i)
+               : tc     ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i)
+                        : ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
         const size_t n = (R + k[i].block_rows - 1) / k[i].block_rows;
         const size_t floats = (Hkv * n + ctx->grid) * ftd::prefix_slot_floats(k[i].slot_rows, c.head_dim);
         if (n > blocks) blocks = n;
@@ -1545,12 +1553,16 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     // 190 rows, 32 heads 46 / 54 / 62 against 57 / 55 / 57.
     const int per = static_cast<int>(T * (Hq / Hkv));
     const size_t own_tiles = B * Hkv * ((static_cast<size_t>(c.max_len) + 127) / 128);
-    const bool own = tc && per <= ftd::kMostOwnRows && ((per >= 4 && c.max_len <= 4096) || own_tiles <= static_cast<size_t>(4 * ctx->grid));
+    const bool own = tc && !i8 && per <= ftd::kMostOwnRows && ((per >= 4 && c.max_len <= 4096) || own_tiles <= static_cast<size_t>(4 * ctx->grid));
     const size_t o_own = carve(own ? 0 : B * T * Hq * D * sizeof(float)), o_ml = carve(own ? 0 : Hkv * R * sizeof(float2));
     const size_t o_ows = carve(own ? (B * Hkv + 2 * ctx->grid) * ftd::own_slot_floats(per, c.head_dim) * sizeof(float) : 0);
     const size_t o_oinfo = carve(own ? B * Hkv * sizeof(int2) : 0);
     const size_t o_info = carve(Hkv * blocks * sizeof(int2));
     const size_t o_ws = carve(ws * sizeof(float));
+    if (!own) {
+        const ftd_status st = ready_mode(ctx, ftd::kBeside);
+        if (st != FTD_OK) return st;
+    }
     void* pool = nullptr;
     const cudaError_t e = cudaMalloc(&pool, off);
     if (e != cudaSuccess) {
@@ -1618,7 +1630,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     } else {
         // the slots' own rows by the step's kernel, into the workspace, beside the prefix
         st = launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, ctx->pre_own, s, false,
-                           ftd::kStep, ctx->pre_ml);
+                           ftd::kBeside);
     }
     if (st != FTD_OK) return st;
     ftd::PrefixParams p{};
@@ -1658,7 +1670,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.P = static_cast<int>(prefix_rows);
     p.R = p.B * p.T * p.group;
     // q as one 16-bit number where it is one, the weights where out keeps no more; else as two
-    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 ? 2 : qkv_bias || c.qkv_dtype != c.cache_dtype ? 1 : 0];
+    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 ? 2 : qkv_bias || c.qkv_dtype != (i8 && c.qkv_dtype != FTD_F32 ? c.qkv_dtype : c.cache_dtype) ? 1 : 0];
     p.block_rows = k.block_rows;
     p.slot_rows = k.slot_rows;
     p.split = k.split;
@@ -1673,7 +1685,8 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     cudaError_t e;
     if (ctx->pre_tc) {
         const size_t rows = ctx->paged ? ctx->rows : static_cast<size_t>(prefix_rows) * c.n_kv_heads;
-        if (ctx->tm_pk_base != p.k || ctx->tm_pv_base != p.v || ctx->tm_p_rows != rows) {
+        // (codes are read without maps)
+        if (!i8 && (ctx->tm_pk_base != p.k || ctx->tm_pv_base != p.v || ctx->tm_p_rows != rows)) {
             ctx->tm_p_rows = 0;
             if (!encode_cache_map(&ctx->tmpk, const_cast<unsigned char*>(p.k), c.cache_dtype, rows, c.head_dim) ||
                 !encode_cache_map(&ctx->tmpv, const_cast<unsigned char*>(p.v), c.cache_dtype, rows, c.head_dim))

@@ -35,9 +35,11 @@ constexpr int kThreads = kWarps * 32;
 enum QkvType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
 
 // What a decode kernel is compiled for: the step; the step that also keeps every visible
-// score and each query row's softmax statistics, for the accumulated weights; or cross
-// attention to a memory of M rows (no append, every query row sees all of them).
-enum StepMode : int { kStep = 0, kScored = 1, kCross = 2 };
+// score and each query row's softmax statistics, for the accumulated weights; cross
+// attention to a memory of M rows (no append, every query row sees all of them); or the step
+// beside a shared prefix, which keeps the statistics (as a branch of the step's own kernels on p.stats that cost
+// the tensor-core ones 0.5 to 5 %).
+enum StepMode : int { kStep = 0, kScored = 1, kCross = 2, kBeside = 3 };
 
 // Arguments of one decode step, resolved by the host entry point.
 struct DecodeParams {
@@ -73,7 +75,7 @@ struct DecodeParams {
     void* proj_hi;          // nullptr: no projection
     void* proj_lo;
     int proj_dt;
-    // kStep with stats: each query row's (m, 1 / sum of 2^(s - m)) beside its output, laid out as for kScored,
+    // kBeside: each query row's (m, 1 / sum of 2^(s - m)) beside its output, laid out as for kScored,
     // for the join with a shared prefix (ftd_prefix.cu).
     // kScored: the scores of query row qi of (b, kv head) at [((b * Hkv + kvh) * nq * group + qi) * Lmax + position],
     // in the log2 domain, and the row's (reference m, 1 / sum of 2^(s - m)).  There qscale is the
@@ -107,9 +109,9 @@ __device__ __forceinline__ int cached_rows(int L) {
 // Scale of an INT8 row from its largest magnitude (0: 1).  The step divides by 127; the scored
 // step and the step beside a shared prefix multiply by the fp32 value of 1 / 127, within an ulp of that.
 template <int MODE>
-__device__ __forceinline__ float i8_row_scale(const DecodeParams& p, float amax) {
+__device__ __forceinline__ float i8_row_scale(float amax) {
     if (amax == 0.f) return 1.f;
-    if (MODE == kScored || (MODE == kStep && p.stats)) return amax * (1.f / 127.f);
+    if constexpr (MODE == kScored || MODE == kBeside) return amax * (1.f / 127.f);
     return __fdiv_rn(amax, 127.f);
 }
 // Index of the score (kScored) and statistics row of query row qi of (b, kvh).
@@ -117,11 +119,10 @@ __device__ __forceinline__ size_t score_row(const DecodeParams& p, int b, int kv
     return (static_cast<size_t>(b) * p.Hkv + kvh) * (p.nq * p.group) + qi;
 }
 
-// Whether a row's softmax statistics are stored: by the scored step always, by the step when asked to.
+// Whether a row's softmax statistics are stored.
 template <int MODE>
-__device__ __forceinline__ bool keeps_stats(const DecodeParams& p) {
-    if constexpr (MODE == kStep) return p.stats != nullptr;
-    return MODE == kScored;
+__host__ __device__ constexpr bool keeps_stats() {
+    return MODE == kScored || MODE == kBeside;
 }
 
 // First visible position of a slot with L cached tokens (the window start).

@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                             amax = fmaxf(amax, fabsf(x[e]));
                         }
                         amax = warp_max(amax);
-                        const float qs = i8_row_scale<MODE>(p, amax);
+                        const float qs = i8_row_scale<MODE>(amax);
                         uint32_t w = 0u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -1271,7 +1271,7 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                 const float inv = 1.f / lt[jj];
                                 if (BOXES > 1 || r < D)
                                     store_out1(p, ((static_cast<size_t>(cu.b) * p.nq + tok) * p.Hq + kvh * p.group + g) * D + r, o[jj] * inv);
-                                if (MODE == kScored && r == 0)
+                                if (keeps_stats<MODE>() && r == 0)
                                     p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] = make_float2(m[jj], inv);
                             });
                         } else {
@@ -1279,8 +1279,6 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                         for (int jj = 0; jj < GH; ++jj)
                             if (c0 + jj < QB) {
                                 store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r, o[jj] / lt[jj]);
-                                if (keeps_stats<MODE>(p) && r == 0)
-                                    p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] = make_float2(m[jj], 1.f / lt[jj]);
                             }
                         }
                     } else {
@@ -1375,9 +1373,10 @@ __global__ void __launch_bounds__(tc::threads_for(G, std::is_same_v<CT, int8_t>)
                                 if (c0 + jj < QB && (BOXES > 1 || r < D)) {
                                     store_out1(p, orow(cu.b, kvh, hb * QB + c0 + jj) * D + r,
                                                Ac[jj] / Ls_[jj]);
-                                    if (keeps_stats<MODE>(p) && r == 0)
-                                        p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] =
-                                            make_float2(Mx[jj], 1.f / Ls_[jj]);
+                                    if constexpr (keeps_stats<MODE>())
+                                        if (r == 0)
+                                            p.stats[score_row(p, cu.b, kvh, hb * QB + c0 + jj)] =
+                                                make_float2(Mx[jj], 1.f / Ls_[jj]);
                                 }
                             if (leader) p.counters[segg] = 0u;
                         }
@@ -1427,10 +1426,12 @@ TcKernelInfo tc_kernel_info() {
 
 TcKernelInfo select_tc(bool bf16, int G, bool multi_token);
 TcKernelInfo select_tc_i8(bool multi_token);
-// the same for kScored and kCross: head dimension D, blocks of 8, 16 and, for 128, 32 and 64 query rows
+// the same for kScored, kCross and kBeside: head dimension D, blocks of 8, 16 and, for 128, 32 and 64 query rows
 TcKernelInfo select_tc_scored(bool bf16, int D, int G, bool multi_token);
 TcKernelInfo select_tc_i8_scored(int D, bool multi_token);
 TcKernelInfo select_tc_cross(bool bf16, int D, int G, bool multi_token);
 TcKernelInfo select_tc_i8_cross(int D, bool multi_token);
+TcKernelInfo select_tc_beside(bool bf16, int D, int G, bool multi_token);
+TcKernelInfo select_tc_i8_beside(int D, bool multi_token);
 
 }  // namespace ftd

@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
         for (int j = 0; j < G; ++j) {
             const size_t dst = q_row(p, mc.b, kvh, hb * G + j) * D + lane * DL;
             const float inv = 1.f / Ls_[j];
-            if (keeps_stats<MODE>(p) && lane == 0) p.stats[score_row(p, mc.b, kvh, hb * G + j)] = make_float2(Mx[j], inv);
+            if constexpr (keeps_stats<MODE>())
+                if (lane == 0) p.stats[score_row(p, mc.b, kvh, hb * G + j)] = make_float2(Mx[j], inv);
             if constexpr (DL == 4) {
                 store_out4(p, dst, Ac[j][0] * inv, Ac[j][1] * inv, Ac[j][2] * inv, Ac[j][3] * inv);
             } else {
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
                 for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
                 for (int mm = 8; mm >= 1; mm >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, mm));
-                const float qs = i8_row_scale<MODE>(p, amax);
+                const float qs = i8_row_scale<MODE>(amax);
                 uint32_t w[EPL / 4];
 #pragma unroll
                 for (int k4 = 0; k4 < EPL / 4; ++k4) w[k4] = 0u;
@@ -1132,8 +1133,8 @@ __global__ void __launch_bounds__(Tiling<CT, D, G>::WARPS * 32, 1) decode_splitk
 #pragma unroll
                     for (int j = 0; j < G; ++j) {
                         const float inv = 1.f / l[j];
-                        if (keeps_stats<MODE>(p) && c == 0)
-                            p.stats[score_row(p, cc.b, kvh, hb * G + j)] = make_float2(m[j], inv);
+                        if constexpr (keeps_stats<MODE>())
+                            if (c == 0) p.stats[score_row(p, cc.b, kvh, hb * G + j)] = make_float2(m[j], inv);
                         const size_t dst = q_row(p, cc.b, kvh, hb * G + j) * D + c * EPL;
 #pragma unroll
                         for (int e4 = 0; e4 < EPL / 4; ++e4)
@@ -1243,7 +1244,7 @@ KernelInfo select_f32(int D, int G);
 KernelInfo select_f16(int D, int G);
 KernelInfo select_bf16(int D, int G);
 KernelInfo select_i8(int D, int G);
-// the same for the step with scores (kScored) and for cross attention (kCross)
+// the same for the step with scores (kScored), cross attention (kCross) and the step beside a prefix (kBeside)
 KernelInfo select_f32_scored(int D, int G);
 KernelInfo select_f16_scored(int D, int G);
 KernelInfo select_bf16_scored(int D, int G);
@@ -1252,5 +1253,9 @@ KernelInfo select_f32_cross(int D, int G);
 KernelInfo select_f16_cross(int D, int G);
 KernelInfo select_bf16_cross(int D, int G);
 KernelInfo select_i8_cross(int D, int G);
+KernelInfo select_f32_beside(int D, int G);
+KernelInfo select_f16_beside(int D, int G);
+KernelInfo select_bf16_beside(int D, int G);
+KernelInfo select_i8_beside(int D, int G);
 
 }  // namespace ftd

@@ -1074,8 +1074,8 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                     }
                 }
                 if (fin) {
-                    if (keeps_stats<MODE>(p) && st < QB)
-                        p.stats[score_row(p, cu.b, kvh, hb * QB + st)] = make_float2(mrg[st], 1.f / mrg[G + st]);
+                    if constexpr (keeps_stats<MODE>())
+                        if (st < QB) p.stats[score_row(p, cu.b, kvh, hb * QB + st)] = make_float2(mrg[st], 1.f / mrg[G + st]);
                     // the block's rows: O / l, one 16-byte store per 4 dimensions
 #pragma unroll 1
                     for (int idx = st; idx < QB * (D / 4); idx += SMX) {

@@ -1,4 +1,4 @@
-// ftd_prefix_tc.cuh -- selection of the tensor-core kernel over a shared prefix (ftd_prefix_tc.cu).
+// ftd_prefix_tc.cuh -- selection of the tensor-core kernel over a shared prefix (ftd_prefix_tc_kernel.cuh).
 #pragma once
 
 #include "ftd_prefix.cuh"
@@ -6,4 +6,6 @@
 namespace ftd {
 // Cache type, head dimension, and what is kept as pairs of 16-bit numbers: 0 nothing, 1 q, 2 q and the weights.
 PrefixKernel select_prefix_tc(bool bf16, int D, int pairs);
+// INT8 caches: q's own type where it is no pair (bf16, else fp16).
+PrefixKernel select_prefix_tc_i8(bool q_bf16, int D, int pairs);
 }  // namespace ftd

@@ -289,10 +289,9 @@ def test_empty_prefix(cache):
     step.prefix(*args, dev(inp["prefix_lens"]), outs[2], k_prefix=dev(inp["k_prefix"]), v_prefix=dev(inp["v_prefix"]), **kw)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1])
-    if cache == "f32":  # the step's kernel takes the own rows: (o l) / l, two roundings more
-        assert torch.all((outs[2] - outs[0]).abs() <= outs[0].abs() * 4 * 2.0 ** -24)
-    else:  # the prefix's kernel takes them: within the bounds of any call
-        run(w, inp)
+    # beside a prefix the own rows' tiles are cut differently, so their sums are taken in another order than the
+    # step's: within the bounds of any call
+    run(w, inp)
     assert step.get_error() == ftd.FTD_OK
     step.close()
 
