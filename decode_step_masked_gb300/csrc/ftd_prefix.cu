@@ -262,17 +262,21 @@ __global__ void __launch_bounds__(kCcThreads, 1) prefix_cc_kernel(const PrefixPa
     grid_dep_wait();  // the step before has ended when this grid has: the join reads both
 }
 
-// 32 query rows of a kv head per block (all of one row block, so 16 where those have no more): a lane per row, a warp for every D / 8 outputs, so a partial's
-// loads are whole lines of neighbouring rows; the sums then go through shared memory to meet the row's own output
-// and leave as rows.
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+// A block joins 32 query rows of a kv head (all of one row block, so 16 where those have no more) and 32 outputs of each: a
+// lane per row, so a partial's loads are whole lines of neighbouring rows, and a warp for 16 outputs of every fourth partial;
+// the sums then go through shared memory to meet each other and the row's own output and leave as rows. It is bound by the
+// chain of dependent loads: with all outputs and every partial in one warp's turn (a quarter of the blocks), 20 partials of 256
+// rows took 22 us.
+constexpr int kJoinRows = 32, kJoinThreads = 256, kJoinOut = 32, kJoinParts = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixParams p) {
-    constexpr int N = D / 8;  // outputs of a thread
-    __shared__ float acc_s[kJoinRows][D + 1];
-    __shared__ float M_s[kJoinRows], S_s[kJoinRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = warp * N;
-    const int h = blockIdx.x % p.Hkv, row0 = static_cast<int>(blockIdx.x / p.Hkv) * min(kJoinRows, p.block_rows);
+    constexpr int N = kJoinOut * kJoinParts / (kJoinThreads / 32);  // outputs of a thread
+    static_assert(N == 16, "two warps for the outputs");
+    __shared__ float acc_s[kJoinParts][kJoinRows][kJoinOut + 1];
+    __shared__ float M_s[kJoinParts][kJoinRows], S_s[kJoinParts][kJoinRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 1, d_at = (warp & 1) * N;
+    const int d_block = static_cast<int>(blockIdx.x) % (D / kJoinOut) * kJoinOut, hr = static_cast<int>(blockIdx.x) / (D / kJoinOut);
+    const int h = hr % p.Hkv, row0 = hr / p.Hkv * min(kJoinRows, p.block_rows), d0 = d_block + d_at;
     grid_dep_wait();
     grid_dep_launch();
     const int rb = row0 / p.block_rows;
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.f;
 #pragma unroll 2
-    for (int k = 0; k < n; ++k) {
+    for (int k = part; k < n; k += kJoinParts) {
         const float* s = slot + (twice ? k >> 1 : k) * stride + (twice ? r + (k & 1) * half : r);
         const float mk = __ldcg(s), lk = __ldcg(s + p.slot_rows);
         float o[N];
@@ -300,23 +304,22 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
         M = mn;
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc_s[lane][d0 + e] = acc[e];
-    if (warp == 0) {
-        M_s[lane] = M;
-        S_s[lane] = S;
+    for (int e = 0; e < N; ++e) acc_s[part][lane][d_at + e] = acc[e];
+    if (!(warp & 1)) {
+        M_s[part][lane] = M;
+        S_s[part][lane] = S;
     }
     __syncthreads();
     // ---- with the rows' own parts ----
-    for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
-        const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4, row = row0 + rr;
+    for (int i = threadIdx.x; i < kJoinRows * (kJoinOut / 4); i += kJoinThreads) {
+        const int rr = i / (kJoinOut / 4), c = (i - rr * (kJoinOut / 4)) * 4, d = d_block + c, row = row0 + rr;
         if (row >= p.R || row0 - rb * p.block_rows + rr >= p.block_rows) continue;
         const int b = prefix_slot_of(p, row), L = __ldcg(p.seq_lens + b);
         const size_t at = prefix_q_row(p, h, row) * D + d;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (L >= 0 && L <= p.Lmax - p.T) {
             const int per = p.T * p.group, r_own = row - b * per;
-            float M = M_s[rr], S = S_s[rr];
-            x = make_float4(acc_s[rr][d], acc_s[rr][d + 1], acc_s[rr][d + 2], acc_s[rr][d + 3]);
+            float M = kNone, S = 0.f;
             // a part without weight leaves the sums as they are
             auto add = [&](float m, float l, float o_l, const float4& o) {
                 const float mn = fmaxf(M, m), f = exp2f(m - mn) * o_l, a = S == 0.f ? 0.f : exp2f(M - mn);
@@ -324,6 +327,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixP
                 x = make_float4(x.x * a + o.x * f, x.y * a + o.y * f, x.z * a + o.z * f, x.w * a + o.w * f);
                 M = mn;
             };
+#pragma unroll
+            for (int k = 0; k < kJoinParts; ++k) {
+                const float* o = &acc_s[k][rr][c];
+                if (S_s[k][rr] != 0.f || M_s[k][rr] > kNone) add(M_s[k][rr], S_s[k][rr], 1.f, make_float4(o[0], o[1], o[2], o[3]));
+            }
             if (p.own) {
                 const int2 v = __ldcg(p.own_info + static_cast<size_t>(b) * p.Hkv + h);
                 const size_t step = own_slot_floats(per, D);
@@ -367,7 +375,7 @@ PrefixKernel select_prefix_cc(int cache_dt, int D, int R) {
 
 cudaError_t launch_prefix_join(PrefixParams p, cudaStream_t stream) {
     const int per = p.block_rows < kJoinRows ? p.block_rows : kJoinRows;  // rows of a block
-    const dim3 grid(static_cast<unsigned>((p.R + per - 1) / per) * static_cast<unsigned>(p.Hkv));
+    const dim3 grid(static_cast<unsigned>((p.R + per - 1) / per) * static_cast<unsigned>(p.Hkv) * static_cast<unsigned>(p.D / kJoinOut));
     void* args[] = {&p};
     const void* fn = p.D == 64 ? reinterpret_cast<const void*>(&prefix_join_kernel<64>)
                                : reinterpret_cast<const void*>(&prefix_join_kernel<128>);
