@@ -1,6 +1,5 @@
 // ftd_prefix_tc_kernel.cuh -- attention to a shared prefix, and to the slots' own rows beside it, on the
-// tensor cores (fp16 and bf16 caches; ftd_prefix.cuh has the mathematics, the cut into work and the layout of
-// the partials).
+// tensor cores (ftd_prefix.cuh has the mathematics, the cut into work and the layout of the partials).
 //
 // With every slot's rows together the products over the prefix are dense: per tile of 128 prefix rows and 128 query rows
 //   S [128 x 128] = Q [128 x D] . K^T          (both K-major in shared memory, S in TMEM)
@@ -14,8 +13,7 @@
 // The slots' own rows run through the same streams, each block taking its share of the prefix's tiles
 // and its share of the own ones (odd blocks the own ones first, so that the memory works while other blocks
 // compute).  An own segment, a slot's kv head, has a few query rows only (T * group, at most 32); the products over
-// them are mostly empty, but even so cost less than a tile's way from memory: 1.0 us of tensor time a tile where the memory
-// takes 1.5.  Here each stream walks its own range of tiles, and no stream waits at a segment's end: the next q
+// them are mostly empty, but even so cost less than a tile's way from memory.  Here each stream walks its own range of tiles, and no stream waits at a segment's end: the next q
 // is already in its other buffer, O is read while the next scores are made.  The decode step's kernel, whose
 // roles meet at every segment's end, takes 79 us for the own rows of a ragged 70B-shaped batch (64 slots of 1 to 1023
 // rows, 8 heads: 134 MB).
@@ -28,6 +26,16 @@
 // PQ, PP: q and the weights as pairs of 16-bit numbers, hi and lo, two products each (about 16 mantissa bits with
 // bf16, 22 with fp16): q where it is no 16-bit number of the cache's type (a bias, another type) and
 // for fp32 out, the weights for fp32 out.  With PQ both streams share one row block of 128.
+//
+// I8: codes become 16-bit numbers on the chip, exactly: K's of the type of q (or bf16 where q is a pair), V's bf16. K's scales
+// multiply the scores and V's the weights, in the softmax threads (take_tile_i8).  Four warps more read tiles of codes
+// straight from memory, one ahead of the ones they convert, in place of the copying warp and of warp 2.  The slots' own
+// rows go by the decode step's kernel.
+//
+// Measured, all launches of a call: 64 70B-shaped slots of two tokens (1024 query rows a kv head) behind 32768 rows, bf16,
+// 146 us, 941 TFLOP/s of useful products; a tile of both streams takes 5300 cycles, of which its products 1024, the softmax
+// threads the rest (128 ex2 a thread and tile are 2048 cycles of the SM's units for two streams).  INT8 for the same shapes: 259 us,
+// 5800 cycles a tile.
 //
 // Roles (384 threads, one block an SM): warp 0 copies K and V tiles (TMA, a ring of whole tiles), then writes for the
 // join which blocks hold what; warps 1 and 3 issue the products, each of one stream (one warp for both was busy all the
@@ -100,6 +108,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -475,9 +488,51 @@ static __device__ __noinline__ void scale_scores(uint32_t ts, int lim, const flo
     wide::tmem_st_wait();
 }
 
+// A new reference for a row in the middle of a tile of codes, whose chunks of 32 columns before c hold weights already: the
+// largest of its scores from there on.  What the old one has made (weights, O, the sum) is rescaled.
+template <int D, bool PP>
+static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, int c0, bool sees, bool chained, float2 ml, const float* ks) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 4 * c0; c < TK / 8; ++c) {
+        float x[8];
+        wide::tmem_ld_rows<8>(ts + 8 * c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e] * ks[8 * c + e]);
+    }
+    const float mn = sees ? fmaxf(ml.x, top) : ml.x, alpha = wide::ex2(ml.x - mn);
+#pragma unroll 1
+    for (int c = 0; c < (PP ? 4 : 2) * c0; ++c) {  // (those weights are less than 2^-kReach of the new ones: a second rounding is nothing)
+        float x[8];
+        wide::tmem_ld_rows<8>(ts + 8 * c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t w = __float_as_uint(x[e]);
+            x[e] = __uint_as_float(pack_ct<__nv_bfloat16>(__uint_as_float(w << 16) * alpha, __uint_as_float(w & 0xFFFF0000u) * alpha));
+        }
+        wide::tmem_st8(ts + 8 * c, x);
+    }
+    if (chained) {
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+            float o[8];
+            wide::tmem_ld_rows<8>(to + 8 * c, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= alpha;
+            wide::tmem_st8(to + 8 * c, o);
+        }
+    }
+    wide::tmem_st_wait();
+    return make_float2(mn, alpha);
+}
+
 // take_tile for codes: S and the weights are of codes, whose rows' scales are in shared memory.  K's (times the softmax scale)
-// multiply the scores, V's the weights behind their sum: bf16 numbers, whose range takes any scale.  ones: 128 of them, for
-// scores that are scaled already.  In two passes of 32 columns: 128 registers a thread.
+// multiply the scores, V's the weights behind their sum: bf16 numbers, whose range takes any scale, and any weight up to 2^kReach
+// besides, so the reference stays where it is until a score is that far above it, and one pass over the scores is enough (a pass for
+// the largest score first took 304 us instead of 259 for 64 70B-shaped slots of two tokens behind
+// 32768 rows, their own rows included).  ones: 128 of them, for scores
+// that are scaled already.  In chunks of 32 columns: 128 registers a thread.
+constexpr float kReach = 40.f;
 template <int D, bool PP>
 static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int lim, bool chained, float2 ml, const float* ks, const float* vs,
                                                    const float* ones) {
@@ -487,65 +542,52 @@ static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int
         scale_scores(ts, masked ? lim : TK, ks);
         ks = ones;
     }
-    float m = ml.x, l = ml.y;
     uint32_t v[32];
-    float t0 = -INFINITY, t1 = -INFINITY;
     fetch_scores(ts, v);
-#pragma unroll 1
-    for (int c = 0; c < TK / 32; ++c) {
-        land_scores(v);
-        float x[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
-        fetch_scores(ts + 32 * ((c + 1) & (TK / 32 - 1)), v);  // (the last ones: the first again, for the pass below)
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + e);
-            t0 = fmaxf(t0, fmaxf(x[e] * k.x, x[e + 1] * k.y));
-            t1 = fmaxf(t1, fmaxf(x[e + 2] * k.z, x[e + 3] * k.w));
-        }
-    }
-    const float top = fmaxf(t0, t1);
-    if (__any_sync(FULL, sees && top > m + tc::kRescaleLog2)) {
-        const float mn = sees ? fmaxf(m, top) : m, alpha = wide::ex2(m - mn);
-        m = mn;
-        l *= alpha;
-        if (chained) {
-            land_scores(v);
-#pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-                float o[8];
-                wide::tmem_ld_rows<8>(to + 8 * c, o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= alpha;
-                wide::tmem_st8(to + 8 * c, o);
-            }
-        }
-    }
-    const float ref = sees ? -m : -INFINITY;
-    const uint64_t m2 = pack2(ref, ref);
+    float ref = sees ? -ml.x : -INFINITY;  // (a row that sees nothing of the tile: weights of 2^-inf)
     uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
 #pragma unroll 1
     for (int c = 0; c < TK / 32; ++c) {
         land_scores(v);
-        uint32_t hi[16], lo[PP ? 16 : 1];
-        float x[32];
+        float x[32], t0 = -INFINITY, t1 = -INFINITY;
+        auto relative = [&] {
+            const uint64_t m2 = pack2(ref, ref);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
-        if (c + 1 < TK / 32) fetch_scores(ts + 32 * (c + 1), v);
+            for (int e = 0; e < 32; e += 4) {
+                const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + e);
+                unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pack2(k.x, k.y), m2), x[e], x[e + 1]);
+                unpack2(fma2(pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), pack2(k.z, k.w), m2), x[e + 2], x[e + 3]);
+            }
+        };
+        relative();
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-            const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + e), w = *reinterpret_cast<const float4*>(vs + 32 * c + e);
+            t0 = fmaxf(t0, fmaxf(x[e], x[e + 1]));
+            t1 = fmaxf(t1, fmaxf(x[e + 2], x[e + 3]));
+        }
+        if (__any_sync(FULL, sees && fmaxf(t0, t1) > kReach)) {
+            const float2 moved = move_reference<D, PP>(ts, to, c, sees, chained, ml, ks);
+            const uint64_t a2 = pack2(moved.y, moved.y);
+            ml = make_float2(moved.x, ml.y * moved.y);
+            acc0 = mul2(acc0, a2);
+            acc1 = mul2(acc1, a2);
+            ref = sees ? -ml.x : -INFINITY;
+            fetch_scores(ts + 32 * c, v);
+            land_scores(v);
+            relative();
+        }
+        if (c + 1 < TK / 32) fetch_scores(ts + 32 * (c + 1), v);
+        uint32_t hi[16], lo[PP ? 16 : 1];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(vs + 32 * c + e);
 #pragma unroll
             for (int g = 0; g < 4; g += 2) {
-                float a, b;
-                unpack2(fma2(pack2(x[e + g], x[e + g + 1]), g ? pack2(k.z, k.w) : pack2(k.x, k.y), m2), a, b);
-                a = wide::ex2(a);
-                b = wide::ex2(b);
-                if (g) acc1 = add2(acc1, pack2(a, b));
-                else acc0 = add2(acc0, pack2(a, b));
-                a *= g ? w.z : w.x;
-                b *= g ? w.w : w.y;
+                float a = wide::ex2(x[e + g]), b = wide::ex2(x[e + g + 1]);
+                const uint64_t ab = pack2(a, b);
+                if (g) acc1 = add2(acc1, ab);
+                else acc0 = add2(acc0, ab);
+                unpack2(mul2(ab, g ? pack2(w.z, w.w) : pack2(w.x, w.y)), a, b);
                 if constexpr (PP) wide::split_pair<__nv_bfloat16>(a, b, hi[(e + g) / 2], lo[(e + g) / 2]);
                 else hi[(e + g) / 2] = pack_ct<__nv_bfloat16>(a, b);
             }
@@ -557,7 +599,7 @@ static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int
     unpack2(add2(acc0, acc1), a, b);
     wide::tmem_st_wait();
     tc::tc_fence_before();
-    return make_float2(m, l + (a + b));
+    return make_float2(ml.x, ml.y + (a + b));
 }
 
 // Two codes (bytes of x by sel, 0x4140 or 0x4342) as a pair of bf16 numbers: under the exponent of 128 the low seven bits are
@@ -613,7 +655,7 @@ struct Codes {
 
 // The products take their operands as uniform registers.  What is the same for the whole warp is handed round once, so that
 // the compiler knows it to be, and descriptors are built from their low halves (the high ones are all alike: rows 1 KB apart
-// in groups of eight, 128-byte swizzle): 65 cycles from one product to the next, 115 with every operand moved over.
+// in groups of eight, 128-byte swizzle).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }

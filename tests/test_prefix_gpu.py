@@ -30,7 +30,9 @@ def case(cache, qkv, B, Hq, Hkv, D, Lmax, lens, P, seen, T=1, seed=61, bias=0.1,
     from synthetic import gen_all, to_storage
     pre = gen_all(pw, seed=seed + 1, seq_lens=np.array([most], np.int32), fill_beyond="nan")
     k = pre["k_cache"][0, :, :P]
-    if heavy:
+    if heavy and cache == "i8":
+        pre["scales"][0] *= (1.0 + heavy * np.arange(pre["scales"].shape[-1]) / P).astype(np.float32)
+    elif heavy:
         x = ref.widen(k, cache) * (1.0 + heavy * np.arange(P) / P)[None, :, None]
         k = np.where(np.isnan(x), k, to_storage(x.astype(np.float32), cache)) if cache != "bf16" else \
             np.where(np.isnan(x), k, to_storage(np.nan_to_num(x).astype(np.float32), cache))
@@ -220,11 +222,11 @@ def test_who_sees_what(cache, seen):
     run(w, inp)
 
 
-@pytest.mark.parametrize("cache,out", [("bf16", "bf16"), ("f16", "f16"), ("f16", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("cache,out", [("bf16", "bf16"), ("f16", "f16"), ("f16", "f32"), ("bf16", "f32"), ("i8", "f16"), ("i8", "f32")])
 @pytest.mark.parametrize("heavy", [4.0, 30.0])
 def test_rising_scores(cache, out, heavy):
     """Keys that grow along the prefix: the running maxima move far, and more than once."""
-    w, inp = case(cache, cache, 5, 16, 2, 128, 32, [0, 3, 9, 20, 31], 1500, [1500, 1500, 800, 0, 1500], heavy=heavy)
+    w, inp = case(cache, "f16" if cache == "i8" else cache, 5, 16, 2, 128, 32, [0, 3, 9, 20, 31], 1500, [1500, 1500, 800, 0, 1500], heavy=heavy)
     run(w, inp, out_dtype=out, bias=out == "f32")
 
 
