@@ -423,7 +423,7 @@ struct ftd_ctx {
     uint32_t* evict_count = nullptr;
     // ftd_enable_prefix: kernel and workspace of ftd_decode_mha_prefix
     void* pre_pool = nullptr;
-    ftd::PrefixKernel pre[3];     // [pairs] of select_prefix_tc (all alike on CUDA cores)
+    ftd::PrefixKernel pre[3];     // [pairs] of select_prefix_tc (INT8: [1], [2] q as a pair; all alike on CUDA cores)
     bool pre_tc = false;
     bool pre_own_rows = false;    // the prefix's kernel takes the slots' own rows too
     float* pre_own_ws = nullptr;  // their partials
@@ -1530,7 +1530,7 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     ftd::PrefixKernel k[3];
     size_t blocks = 0, ws = 0;
     for (int i = 0; i < 3; ++i) {
-        k[i] = tc && i8 ? ftd::select_prefix_tc_i8(c.qkv_dtype == FTD_BF16, c.head_dim, i)
+        k[i] = tc && i8 ? ftd::select_prefix_tc_i8(c.qkv_dtype == FTD_BF16, c.head_dim, i > 0, c.out_dtype != FTD_BF16)
                : tc     ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i)
                         : ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
         const size_t n = (R + k[i].block_rows - 1) / k[i].block_rows;
@@ -1669,8 +1669,10 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.Lmax = c.max_len;
     p.P = static_cast<int>(prefix_rows);
     p.R = p.B * p.T * p.group;
-    // q as one 16-bit number where it is one, the weights where out keeps no more; else as two
-    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 ? 2 : qkv_bias || c.qkv_dtype != (i8 && c.qkv_dtype != FTD_F32 ? c.qkv_dtype : c.cache_dtype) ? 1 : 0];
+    // q as one 16-bit number where it is one, the weights where out keeps no more; else as two (INT8, whose weights are bf16:
+    // as two for fp16 out as well)
+    const bool pair_q = qkv_bias || (i8 ? c.qkv_dtype == FTD_F32 : c.qkv_dtype != c.cache_dtype);
+    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 && !i8 ? 2 : pair_q ? 1 : 0];
     p.block_rows = k.block_rows;
     p.slot_rows = k.slot_rows;
     p.split = k.split;

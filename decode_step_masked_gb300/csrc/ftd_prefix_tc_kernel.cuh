@@ -632,14 +632,12 @@ template <int D>
 struct Codes {
     static constexpr int N = D / 16;  // pieces of a thread, and of a row
     uint4 w[N];
-    float scale;
-    __device__ __forceinline__ void load(const unsigned char* base, const float* scales, long long row, int rows, int t) {
+    __device__ __forceinline__ void load(const unsigned char* base, long long row, int rows, int t) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int i = t + 128 * k, r = i / N;
             w[k] = r < rows ? __ldcg(reinterpret_cast<const uint4*>(base + (row + r) * D) + i % N) : make_uint4(0u, 0u, 0u, 0u);
         }
-        scale = t < rows ? __ldcg(scales + row + t) : 0.f;
     }
     template <typename CT>
     __device__ __forceinline__ void store(unsigned char* tile, int t) const {
@@ -1150,17 +1148,25 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
             __syncwarp();
             if (lane == 0 && !held) mbar_arrive(bar(kReady + slot));
         };
+        // a row's two scales go with its K: the softmax takes both as soon as there are scores
         Codes<D> k, v;
-        place();
-        k.load(p.k, p.k_scales, row, rows, t);
+        float k_scale, v_scale;
+        auto load_k = [&] {
+            place();
+            k.load(p.k, row, rows, t);
+            k_scale = t < rows ? __ldcg(p.k_scales + row + t) : 0.f;
+            v_scale = t < rows ? __ldcg(p.v_scales + row + t) : 0.f;
+        };
+        load_k();
 #pragma unroll 1
         while (ok) {
             float* sc = scales + tile % (I8 ? LY::NSC : 1) * (2 * TK);
-            v.load(p.v, p.v_scales, row, rows, t);
+            v.load(p.v, row, rows, t);
             if (tile >= NK) ok = wait(kEmpty + k_slot(tile), k_par(tile) ^ 1);
             if (!ok) break;
             k.template store<CT>(ring + k_slot(tile) * TILE, t);
-            sc[t] = k.scale * p.qscale;
+            sc[t] = k_scale * p.qscale;
+            sc[TK + t] = v_scale;
             publish(k_slot(tile), withhold && tile == 0);
             if (++i == x.nt) {
                 u += x.nt;
@@ -1171,14 +1177,10 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
                 }
             }
             const bool more = u < u_end;
-            if (more) {
-                place();
-                k.load(p.k, p.k_scales, row, rows, t);
-            }
+            if (more) load_k();
             if (tile >= NV) ok = wait(kEmpty + v_slot(tile), v_par(tile) ^ 1);
             if (!ok) break;
             v.template store<WT>(ring + v_slot(tile) * TILE, t);
-            sc[TK + t] = v.scale;
             publish(v_slot(tile), false);
             ++tile;
             if (!more) break;

@@ -147,7 +147,8 @@ def run(w, inp, out_dtype="f32", page=0, cuda_core=False, bias=True, step=None, 
     if own:
         step.close()
     inp = inp if use else dict(inp, bias=None)
-    single = out_dtype != "f32" and not cuda_core and w.cache_dtype != "f32"  # weights of one 16-bit number
+    # weights of one 16-bit number (INT8's are of bf16: two for fp16 out)
+    single = out_dtype != "f32" and not cuda_core and w.cache_dtype != "f32" and (w.cache_dtype, out_dtype) != ("i8", "f16")
     want, tol = expect(w, inp, ka, va, sa, single)
     if out_dtype != "f32":
         tol = tol + np.abs(want) * ref.HALF_STEP[out_dtype] * (1 + 2.0 ** -7) + (2.0 ** -25 if out_dtype == "f16" else 0.0)
@@ -236,6 +237,19 @@ def test_slots_without_work(cache):
     w, inp = case(cache, "f16" if cache == "i8" else cache, 5, 8, 2, 64, 48, [-1, 48, 5, 47, 100], 400, [400, 400, 200, 100, 400])
     got, _ = run(w, inp, status=ftd.FTD_ERR_SEQ_OVERFLOW)
     assert not got[[0, 1, 4]].any() and got[[2, 3]].any()
+
+
+@pytest.mark.parametrize("cache,qkv,out,D,bias", [("i8", "f16", "f16", 128, None), ("i8", "bf16", "bf16", 64, 0.1), ("i8", "f16", "f32", 128, 0.1),
+                                                  ("i8", "bf16", "f32", 64, None), ("f16", "f16", "f16", 128, None), ("bf16", "bf16", "f32", 128, 0.1),
+                                                  ("f32", "f32", "f32", 64, None)])
+@pytest.mark.parametrize("B", [3, 40])
+def test_many_tiles_a_block(cache, qkv, out, D, bias, B):
+    """Every block goes through its buffers many times, over pieces of several kv heads: few rows (each tile is one stream's)
+    and, with more heads of a kv head, two row blocks."""
+    g, P = (1, 4110) if B == 3 else (5, 4110)
+    hkv = 40 if B == 3 else 12
+    w, inp = case(cache, qkv, B, hkv * g, hkv, D, 32, [b % 30 for b in range(B)], P, [P - 7 * b for b in range(B)], bias=bias)
+    run(w, inp, out_dtype=out, bias=bias is not None)
 
 
 def test_prefix_lens_too_long():
