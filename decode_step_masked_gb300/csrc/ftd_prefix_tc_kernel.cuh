@@ -1209,7 +1209,7 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
                     const Piece x = piece_at(u);
                     const int n = tiles_of(x, s);
                     const int row = x.c.rb * p.block_rows + (x.twice ? r : s * TK + r);
-                    const bool live = row < p.R;
+                    const bool live = row < p.R, any_live = __any_sync(FULL, live);  // (a warp past the last row: its O is nobody's)
                     {
                         // q: neighbouring lanes take neighbouring 16 bytes of a row (a pair's q is made by both streams, half
                         // of the rows each)
@@ -1229,7 +1229,8 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
                         ++ns;
                         tc::tc_fence_after();
                         const int at = tile_of(x, s, j), lim = seen - (x.c.tile + at) * TK;
-                        if constexpr (I8) {
+                        if (!any_live) {
+                        } else if constexpr (I8) {
                             const float* sc = scales + (tiles + at) % LY::NSC * (2 * TK);
                             ml = take_tile_i8<D, PP>(ts, to, lim, j > 0, ml, sc, sc + TK, scales + 2 * LY::NSC * TK);
                         } else {
@@ -1248,7 +1249,7 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
                     if (!ok) break;
                     ++no[s];
                     tc::tc_fence_after();
-                    if (n > 0) {
+                    if (n > 0 && any_live) {
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
