@@ -79,22 +79,24 @@ __device__ __forceinline__ void weigh(float (&y)[VEC], float r, const float (&w)
             unpack2(mul2(mul2(pack2(y[e], y[e + 1]), pack2(r, r)), pack2(w[e], w[e + 1])), y[e], y[e + 1]);
     }
 }
-// (a, b) -> (a c - b s, b c + a s); sn holds s and, for the packed form, b's products take their sign in the last step
+// (a, b) -> (a c - b s, b c + a s); b s takes its sign in the last step, which is not packed
 template <int VEC>
 __device__ __forceinline__ void turn(float (&a)[VEC], float (&b)[VEC], const float (&c)[VEC], const float (&s)[VEC], bool adjacent) {
-    if (VEC == 1 || adjacent) {
+    if constexpr (VEC == 1) {
         turn_pairs<VEC>(a, b, c, s, adjacent);
-        return;
-    }
+    } else if (adjacent) {
+        turn_pairs<VEC>(a, b, c, s, true);
+    } else {
 #pragma unroll
-    for (int e = 0; e < VEC / 2 * 2; e += 2) {
-        const uint64_t c2 = pack2(c[e], c[e + 1]), s2 = pack2(s[e], s[e + 1]);
-        const uint64_t a2 = pack2(a[e], a[e + 1]), b2 = pack2(b[e], b[e + 1]);
-        float t0, t1;
-        unpack2(mul2(b2, s2), t0, t1);
-        unpack2(fma2(a2, s2, mul2(b2, c2)), b[e], b[e + 1]);
-        a[e] = fmaf(a[e], c[e], -t0);
-        a[e + 1] = fmaf(a[e + 1], c[e + 1], -t1);
+        for (int e = 0; e < VEC; e += 2) {
+            const uint64_t c2 = pack2(c[e], c[e + 1]), s2 = pack2(s[e], s[e + 1]);
+            const uint64_t a2 = pack2(a[e], a[e + 1]), b2 = pack2(b[e], b[e + 1]);
+            float t0, t1;
+            unpack2(mul2(b2, s2), t0, t1);
+            unpack2(fma2(a2, s2, mul2(b2, c2)), b[e], b[e + 1]);
+            a[e] = fmaf(a[e], c[e], -t0);
+            a[e + 1] = fmaf(a[e + 1], c[e + 1], -t1);
+        }
     }
 }
 
