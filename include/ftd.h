@@ -555,7 +555,7 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  * of the prefix and to the slot's own rows, those of its cache and the new ones,
  *   out[b][j][h] = softmax over both of scale * q'[b][j][h] . K, times V.
  * The prefix is read once for all slots: with B slots its products are matrix products
- * with B * T * Hq / Hkv rows, which fp16 and bf16 caches make on the tensor cores.
+ * with B * T * Hq / Hkv rows, on the tensor cores for fp16, bf16 and INT8 caches.
  *   k_prefix, v_prefix : device [Hkv][prefix_rows][D] of the cache dtype, 16-byte aligned, read
  *               only; INT8 with prefix_scales, device fp32 [2][Hkv][prefix_rows].  On a
  *               paged context NULL: the prefix lies in pages of the pool, and
@@ -574,7 +574,9 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  * FTD_ERR_BAD_PAGE, and what the slots see of it is undefined.
  * fp16 and bf16 caches: the tensor cores take the weights rounded to that type where out is a
  * 16-bit type, and q as it is where it is of the cache's type and has no bias; else each as a
- * pair of its numbers (about 16 mantissa bits with bf16), as ftd_decode_mha does.  Launches two or
+ * pair of its numbers (about 16 mantissa bits with bf16), as ftd_decode_mha does.  INT8 caches:
+ * codes are exact, scales multiply scores and weights in fp32; q is one fp16 or bf16 number without a bias, the
+ * weights one bf16 number for bf16 out, else each a pair of bf16 numbers.  Launches two or
  * three kernels: the slots' own rows are taken beside the prefix or by the step's kernel.
  */
 ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new, const void* qkv_bias,
