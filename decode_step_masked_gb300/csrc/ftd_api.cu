@@ -423,7 +423,7 @@ struct ftd_ctx {
     uint32_t* evict_count = nullptr;
     // ftd_enable_prefix: kernel and workspace of ftd_decode_mha_prefix
     void* pre_pool = nullptr;
-    ftd::PrefixKernel pre[3];     // [pairs] of select_prefix_tc (INT8: [1], [2] q as a pair; all alike on CUDA cores)
+    ftd::PrefixKernel pre[2];     // q as it is, and as a pair of 16-bit numbers (alike on CUDA cores)
     bool pre_tc = false;
     bool pre_own_rows = false;    // the prefix's kernel takes the slots' own rows too
     float* pre_own_ws = nullptr;  // their partials
@@ -1529,11 +1529,11 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     const bool i8 = c.cache_dtype == FTD_I8;
     const bool tc = c.cache_dtype != FTD_F32 && c.kernel != FTD_KERNEL_CUDA_CORE && (i8 || encode_tiled());
     if (R > 32768) return fail(FTD_ERR_UNSUPPORTED, "%s: %zu query rows per kv head, at most 32768", what, R);
-    ftd::PrefixKernel k[3];
+    ftd::PrefixKernel k[2];
     size_t blocks = 0, ws = 0;
-    for (int i = 0; i < 3; ++i) {
-        k[i] = tc && i8 ? ftd::select_prefix_tc_i8(c.qkv_dtype == FTD_BF16, c.head_dim, i > 0, c.out_dtype != FTD_BF16)
-               : tc     ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i)
+    for (int i = 0; i < 2; ++i) {
+        k[i] = tc && i8 ? ftd::select_prefix_tc_i8(c.qkv_dtype == FTD_BF16, c.head_dim, i > 0)
+               : tc     ? ftd::select_prefix_tc(c.cache_dtype == FTD_BF16, c.head_dim, i > 0)
                         : ftd::select_prefix_cc(static_cast<int>(c.cache_dtype), c.head_dim, static_cast<int>(R));
         const size_t n = (R + k[i].block_rows - 1) / k[i].block_rows;
         const size_t floats = (Hkv * n + ctx->grid) * ftd::prefix_slot_floats(k[i].slot_rows, c.head_dim);
@@ -1573,7 +1573,7 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
     }
     unsigned char* base = static_cast<unsigned char*>(pool);
     ctx->pre_pool = pool;
-    for (int i = 0; i < 3; ++i) ctx->pre[i] = k[i];
+    for (int i = 0; i < 2; ++i) ctx->pre[i] = k[i];
     ctx->pre_tc = tc;
     ctx->pre_own_rows = own;
     ctx->pre_own_ws = reinterpret_cast<float*>(base + o_ows);
@@ -1671,10 +1671,9 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.Lmax = c.max_len;
     p.P = static_cast<int>(prefix_rows);
     p.R = p.B * p.T * p.group;
-    // q as one 16-bit number where it is one, the weights where out keeps no more; else as two (INT8, whose weights are bf16:
-    // as two for fp16 out as well)
+    // q as one 16-bit number of the products' type where it is one, else as two
     const bool pair_q = qkv_bias || (i8 ? c.qkv_dtype == FTD_F32 : c.qkv_dtype != c.cache_dtype);
-    const ftd::PrefixKernel& k = ctx->pre[c.out_dtype == FTD_F32 && !i8 ? 2 : pair_q ? 1 : 0];
+    const ftd::PrefixKernel& k = ctx->pre[pair_q];
     p.block_rows = k.block_rows;
     p.slot_rows = k.slot_rows;
     p.split = k.split;

@@ -5,16 +5,14 @@ namespace ftd {
 
 namespace {
 template <typename CT, int D>
-PrefixKernel pick(int pairs) {
-    return pairs == 2   ? ptc::kernel_of<CT, D, true, true, false>()
-           : pairs == 1 ? ptc::kernel_of<CT, D, true, false, false>()
-                        : ptc::kernel_of<CT, D, false, false, false>();
+PrefixKernel pick(bool pair_q) {
+    return pair_q ? ptc::kernel_of<CT, D, true, false>() : ptc::kernel_of<CT, D, false, false>();
 }
 }  // namespace
 
-PrefixKernel select_prefix_tc(bool bf16, int D, int pairs) {
-    if (bf16) return D == 64 ? pick<__nv_bfloat16, 64>(pairs) : pick<__nv_bfloat16, 128>(pairs);
-    return D == 64 ? pick<__half, 64>(pairs) : pick<__half, 128>(pairs);
+PrefixKernel select_prefix_tc(bool bf16, int D, bool pair_q) {
+    if (bf16) return D == 64 ? pick<__nv_bfloat16, 64>(pair_q) : pick<__nv_bfloat16, 128>(pair_q);
+    return D == 64 ? pick<__half, 64>(pair_q) : pick<__half, 128>(pair_q);
 }
 
 }  // namespace ftd

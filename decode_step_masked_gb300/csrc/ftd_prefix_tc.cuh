@@ -4,8 +4,8 @@
 #include "ftd_prefix.cuh"
 
 namespace ftd {
-// Cache type, head dimension, and what is kept as pairs of 16-bit numbers: 0 nothing, 1 q, 2 q and the weights.
-PrefixKernel select_prefix_tc(bool bf16, int D, int pairs);
-// INT8 caches: q's own type where it is no pair (bf16, else fp16); what is a pair of bf16 numbers.
-PrefixKernel select_prefix_tc_i8(bool q_bf16, int D, bool pair_q, bool pair_weights);
+// Cache type, head dimension, and whether q is kept as a pair of 16-bit numbers.
+PrefixKernel select_prefix_tc(bool bf16, int D, bool pair_q);
+// INT8 caches: q's own type where it is no pair (bf16, else fp16); a pair is of bf16 numbers.
+PrefixKernel select_prefix_tc_i8(bool q_bf16, int D, bool pair_q);
 }  // namespace ftd

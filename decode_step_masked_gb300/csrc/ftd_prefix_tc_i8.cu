@@ -4,17 +4,14 @@
 namespace ftd {
 
 namespace {
-template <int D, bool PP>
+template <int D>
 PrefixKernel pick(bool q_bf16, bool pair_q) {
-    return pair_q   ? ptc::kernel_of<__nv_bfloat16, D, true, PP, true>()
-           : q_bf16 ? ptc::kernel_of<__nv_bfloat16, D, false, PP, true>()
-                    : ptc::kernel_of<__half, D, false, PP, true>();
+    return pair_q   ? ptc::kernel_of<__nv_bfloat16, D, true, true>()
+           : q_bf16 ? ptc::kernel_of<__nv_bfloat16, D, false, true>()
+                    : ptc::kernel_of<__half, D, false, true>();
 }
 }  // namespace
 
-PrefixKernel select_prefix_tc_i8(bool q_bf16, int D, bool pair_q, bool pair_weights) {
-    if (pair_weights) return D == 64 ? pick<64, true>(q_bf16, pair_q) : pick<128, true>(q_bf16, pair_q);
-    return D == 64 ? pick<64, false>(q_bf16, pair_q) : pick<128, false>(q_bf16, pair_q);
-}
+PrefixKernel select_prefix_tc_i8(bool q_bf16, int D, bool pair_q) { return D == 64 ? pick<64>(q_bf16, pair_q) : pick<128>(q_bf16, pair_q); }
 
 }  // namespace ftd

@@ -23,9 +23,10 @@
 // m and rescales its row of O; the product of the tile before has ended by then, since the score product
 // behind it has.
 //
-// PQ, PP: q and the weights as pairs of 16-bit numbers, hi and lo, two products each (about 16 mantissa bits with
-// bf16, 22 with fp16): q where it is no 16-bit number of the cache's type (a bias, another type) and
-// for fp32 out, the weights for fp32 out.  With PQ both streams share one row block of 128.
+// The weights are pairs of 16-bit numbers, hi and lo, two products each (about 16 mantissa bits with bf16, 22 with fp16),
+// whatever the type of out, as in the decode step: single ones made a 16-bit out, whose own rounding is 1.65e-3
+// (bf16) or 2.07e-4 (fp16) in the 2-norm, 2.2e-3 to 2.4e-3 and 2.65e-4.  PQ: q too, where it is no 16-bit number of the cache's
+// type (a bias, another type).  With PQ both streams share one row block of 128.
 //
 // I8: codes become 16-bit numbers on the chip, exactly: K's of the type of q (or bf16 where q is a pair), V's bf16. K's scales
 // multiply the scores and V's the weights, in the softmax threads (take_tile_i8).  Four warps more read tiles of codes
@@ -33,8 +34,8 @@
 // rows go by the decode step's kernel.
 //
 // Measured, all launches of a call: 64 70B-shaped slots of two tokens (1024 query rows a kv head) behind 32768 rows, bf16,
-// 146 us, 941 TFLOP/s of useful products; a tile of both streams takes 5300 cycles, of which its products 1024, the softmax
-// threads the rest (128 ex2 a thread and tile are 2048 cycles of the SM's units for two streams).  INT8 for the same shapes: 259 us,
+// 192 us, 718 TFLOP/s of useful products (with single weights 147); a tile of both streams takes some 6900 cycles, of which its
+// products 1536, the softmax threads the rest (128 ex2 a thread and tile are 2048 cycles of the SM's units for two streams).  INT8 for the same shapes: 259 us,
 // 5800 cycles a tile.
 //
 // Roles (384 threads, one block an SM): warp 0 copies K and V tiles (TMA, a ring of whole tiles), then writes for the
@@ -352,7 +353,7 @@ static __device__ __noinline__ void mask_scores(uint32_t ts, int lim) {
 }
 
 // The weights of a tile in two passes over its scores: the largest, then the weights against the reference that it leaves.
-template <typename CT, int D, bool PP>
+template <typename CT, int D>
 static __device__ __noinline__ float2 weigh_tile(uint32_t ts, uint32_t to, bool sees, bool chained, float2 ml, float qscale) {
     constexpr unsigned FULL = 0xffffffffu;
     float m = ml.x, l = ml.y;
@@ -391,12 +392,12 @@ static __device__ __noinline__ float2 weigh_tile(uint32_t ts, uint32_t to, bool 
     const float ref = sees ? -m : -INFINITY;
     const uint64_t sc2 = pack2(qscale, qscale), m2 = pack2(ref, ref);
     uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
-    // a loop of 32 keys, the next ones' scores under way: the code of all 128 (18 KB with pairs) would not stay in the
+    // a loop of 32 keys, the next ones' scores under way: the code of all 128 (18 KB) would not stay in the
     // instruction cache beside the other roles'
 #pragma unroll 1
     for (int c = 0; c < TK / 32; ++c) {
         land_scores(v);
-        uint32_t hi[16], lo[PP ? 16 : 1];
+        uint32_t hi[16], lo[16];
         float x[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
@@ -409,12 +410,11 @@ static __device__ __noinline__ float2 weigh_tile(uint32_t ts, uint32_t to, bool 
             b = wide::ex2(b);
             if (e & 2) acc1 = add2(acc1, pack2(a, b));
             else acc0 = add2(acc0, pack2(a, b));
-            if constexpr (PP) wide::split_pair<CT>(a, b, hi[e / 2], lo[e / 2]);
-            else hi[e / 2] = pack_ct<CT>(a, b);
+            wide::split_pair<CT>(a, b, hi[e / 2], lo[e / 2]);
         }
-        // 32 keys' weights: 16 columns, or 16 of hi and 16 of lo, over scores that have been read
-        tc::tmem_st16(ts + (PP ? 32 : 16) * c, hi);
-        if constexpr (PP) tc::tmem_st16(ts + 32 * c + 16, lo);
+        // 32 keys' weights: 16 columns of hi and 16 of lo, over scores that have been read
+        tc::tmem_st16(ts + 32 * c, hi);
+        tc::tmem_st16(ts + 32 * c + 16, lo);
     }
     float a, b;
     unpack2(add2(acc0, acc1), a, b);
@@ -425,54 +425,13 @@ static __device__ __noinline__ float2 weigh_tile(uint32_t ts, uint32_t to, bool 
 
 // A tile whose scores are in TMEM at ts: the weights of this thread's row, which sees the first `lim` of its columns (none:
 // <= 0), over them.  Columns from `edge` on belong to nobody and may hold anything.  live: the row is one; chained: its row of O, at to, holds earlier tiles.  ml: running reference and sum.
-template <typename CT, int D, bool PP>
+template <typename CT, int D>
 static __device__ __noinline__ float2 take_tile(uint32_t ts, uint32_t to, int lim, int edge, bool live, bool chained, float2 ml, float qscale) {
     constexpr unsigned FULL = 0xffffffffu;
     const bool sees = live && lim > 0;
     const bool masked = live && lim < TK && (lim > 0 || edge < TK);
     if (__any_sync(FULL, masked)) mask_scores(ts, masked ? lim : TK);
-    if constexpr (!PP) {
-        if (chained) {
-            // One pass: the weights against the reference as it is, kept until the largest score is known to allow it (1500
-            // against 1050 cycles a tile).
-            const float ref = sees ? -ml.x : -INFINITY;
-            const uint64_t sc2 = pack2(qscale, qscale), m2 = pack2(ref, ref);
-            uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
-            uint32_t hi[TK / 2], v[32];
-            float t0 = -INFINITY, t1 = -INFINITY;
-            fetch_scores(ts, v);
-#pragma unroll
-            for (int c = 0; c < TK / 32; ++c) {
-                land_scores(v);
-                float x[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]);
-                if (c + 1 < TK / 32) fetch_scores(ts + 32 * (c + 1), v);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    if (e & 2) t1 = fmaxf(t1, fmaxf(x[e], x[e + 1]));
-                    else t0 = fmaxf(t0, fmaxf(x[e], x[e + 1]));
-                    float a, b;
-                    unpack2(fma2(pack2(x[e], x[e + 1]), sc2, m2), a, b);
-                    a = wide::ex2(a);
-                    b = wide::ex2(b);
-                    if (e & 2) acc1 = add2(acc1, pack2(a, b));
-                    else acc0 = add2(acc0, pack2(a, b));
-                    hi[16 * c + e / 2] = pack_ct<CT>(a, b);
-                }
-            }
-            if (!__any_sync(FULL, sees && fmaxf(t0, t1) * qscale > ml.x + tc::kRescaleLog2)) {
-#pragma unroll
-                for (int c = 0; c < TK / 32; ++c) tc::tmem_st16(ts + 16 * c, hi + 16 * c);
-                float a, b;
-                unpack2(add2(acc0, acc1), a, b);
-                wide::tmem_st_wait();
-                tc::tc_fence_before();
-                return make_float2(ml.x, ml.y + (a + b));
-            }
-        }
-    }
-    return weigh_tile<CT, D, PP>(ts, to, sees, chained, ml, qscale);
+    return weigh_tile<CT, D>(ts, to, sees, chained, ml, qscale);
 }
 
 // INT8: a tile's scores, times its rows' scales; those from column lim on become -inf.  In TMEM.
@@ -490,7 +449,7 @@ static __device__ __noinline__ void scale_scores(uint32_t ts, int lim, const flo
 
 // A new reference for a row in the middle of a tile of codes, whose chunks of 32 columns before c hold weights already: the
 // largest of its scores from there on.  What the old one has made (weights, O, the sum) is rescaled.
-template <int D, bool PP>
+template <int D>
 static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, int c0, bool sees, bool chained, float2 ml, const float* ks) {
     float top = -INFINITY;
 #pragma unroll 1
@@ -502,7 +461,7 @@ static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, i
     }
     const float mn = sees ? fmaxf(ml.x, top) : ml.x, alpha = wide::ex2(ml.x - mn);
 #pragma unroll 1
-    for (int c = 0; c < (PP ? 4 : 2) * c0; ++c) {  // (those weights are less than 2^-kReach of the new ones: a second rounding is nothing)
+    for (int c = 0; c < 4 * c0; ++c) {  // (those weights are less than 2^-kReach of the new ones: a second rounding is nothing)
         float x[8];
         wide::tmem_ld_rows<8>(ts + 8 * c, x);
 #pragma unroll
@@ -533,7 +492,7 @@ static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, i
 // 32768 rows, their own rows included).  ones: 128 of them, for scores
 // that are scaled already.  In chunks of 32 columns: 128 registers a thread.
 constexpr float kReach = 40.f;
-template <int D, bool PP>
+template <int D>
 static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int lim, bool chained, float2 ml, const float* ks, const float* vs,
                                                    const float* ones) {
     constexpr unsigned FULL = 0xffffffffu;
@@ -566,7 +525,7 @@ static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int
             t1 = fmaxf(t1, fmaxf(x[e + 2], x[e + 3]));
         }
         if (__any_sync(FULL, sees && fmaxf(t0, t1) > kReach)) {
-            const float2 moved = move_reference<D, PP>(ts, to, c, sees, chained, ml, ks);
+            const float2 moved = move_reference<D>(ts, to, c, sees, chained, ml, ks);
             const uint64_t a2 = pack2(moved.y, moved.y);
             ml = make_float2(moved.x, ml.y * moved.y);
             acc0 = mul2(acc0, a2);
@@ -577,7 +536,7 @@ static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int
             relative();
         }
         if (c + 1 < TK / 32) fetch_scores(ts + 32 * (c + 1), v);
-        uint32_t hi[16], lo[PP ? 16 : 1];
+        uint32_t hi[16], lo[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
             const float4 w = *reinterpret_cast<const float4*>(vs + 32 * c + e);
@@ -588,12 +547,11 @@ static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int
                 if (g) acc1 = add2(acc1, ab);
                 else acc0 = add2(acc0, ab);
                 unpack2(mul2(ab, g ? pack2(w.z, w.w) : pack2(w.x, w.y)), a, b);
-                if constexpr (PP) wide::split_pair<__nv_bfloat16>(a, b, hi[(e + g) / 2], lo[(e + g) / 2]);
-                else hi[(e + g) / 2] = pack_ct<__nv_bfloat16>(a, b);
+                wide::split_pair<__nv_bfloat16>(a, b, hi[(e + g) / 2], lo[(e + g) / 2]);
             }
         }
-        tc::tmem_st16(ts + (PP ? 32 : 16) * c, hi);
-        if constexpr (PP) tc::tmem_st16(ts + 32 * c + 16, lo);
+        tc::tmem_st16(ts + 32 * c, hi);
+        tc::tmem_st16(ts + 32 * c + 16, lo);
     }
     float a, b;
     unpack2(add2(acc0, acc1), a, b);
@@ -688,19 +646,15 @@ __device__ __forceinline__ void issue_scores(uint32_t ts, uint32_t qa, uint32_t 
 }
 
 // The weights (TMEM at tp) times V at vb into O at to, which begins (more 0) or goes on.  One thread.
-template <int D, bool PP>
+template <int D>
 __device__ __forceinline__ void issue_values(uint32_t to, uint32_t tp, uint32_t vb, uint32_t more, uint32_t id) {
     tc::tc_fence_after();
 #pragma unroll
     for (int kq = 0; kq < TK / 16; ++kq) {
-        const uint32_t v = vb + (kq * 2048 >> 4);
-        if constexpr (PP) {  // chunks of 32 keys: 16 columns of hi, 16 of lo
-            const uint32_t c = tp + (kq >> 1) * 32 + (kq & 1) * 8;
-            product_ts(to, c, v, id, kq > 0 ? 1u : more);
-            product_ts(to, c + 16, v, id, 1u);
-        } else {
-            product_ts(to, tp + kq * 8, v, id, kq > 0 ? 1u : more);
-        }
+        // (chunks of 32 keys: 16 columns of hi, 16 of lo)
+        const uint32_t v = vb + (kq * 2048 >> 4), c = tp + (kq >> 1) * 32 + (kq & 1) * 8;
+        product_ts(to, c, v, id, kq > 0 ? 1u : more);
+        product_ts(to, c + 16, v, id, 1u);
     }
 }
 
@@ -791,7 +745,7 @@ struct OwnSplit {
 };
 
 // CT: the type of q and K as operands, and without I8 of V and the weights too (with it those are bf16)
-template <typename CT, int D, bool PQ, bool PP, bool I8>
+template <typename CT, int D, bool PQ, bool I8>
 __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ CUtensorMap tmk_own, const __grid_constant__ CUtensorMap tmv_own,
@@ -984,7 +938,7 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
             const uint32_t does = uniform((v >= 0) | (k >= 0) << 1 | end << 2 | both << 3 | !fresh << 4);
             if (elect_one()) {
                 if (does & 1) {
-                    issue_values<D, PP>(to, ts, dv0 + vs * (TILE >> 4), does >> 4, id_o);
+                    issue_values<D>(to, ts, dv0 + vs * (TILE >> 4), does >> 4, id_o);
                     release(vs, does & 8);
                     if (does & 4) tc::mma_commit(bar(kOFull + s));
                 }
@@ -1232,9 +1186,9 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
                         if (!any_live) {
                         } else if constexpr (I8) {
                             const float* sc = scales + (tiles + at) % LY::NSC * (2 * TK);
-                            ml = take_tile_i8<D, PP>(ts, to, lim, j > 0, ml, sc, sc + TK, scales + 2 * LY::NSC * TK);
+                            ml = take_tile_i8<D>(ts, to, lim, j > 0, ml, sc, sc + TK, scales + 2 * LY::NSC * TK);
                         } else {
-                            ml = take_tile<CT, D, PP>(ts, to, lim, most - (x.c.tile + at) * TK, true, j > 0, ml, p.qscale);
+                            ml = take_tile<CT, D>(ts, to, lim, most - (x.c.tile + at) * TK, true, j > 0, ml, p.qscale);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kPFull + s));
@@ -1306,7 +1260,7 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
                         if (!ok) break;
                         ++ns;
                         tc::tc_fence_after();
-                        if constexpr (!I8) ml = take_tile<CT, D, PP>(ts, to, k.L + tok + 1 - k.tile * TK, k.L + p.T - k.tile * TK, live, !fresh, ml, p.qscale);
+                        if constexpr (!I8) ml = take_tile<CT, D>(ts, to, k.L + tok + 1 - k.tile * TK, k.L + p.T - k.tile * TK, live, !fresh, ml, p.qscale);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kPFull + s));
                     }
@@ -1407,9 +1361,9 @@ __global__ void __launch_bounds__(I8 ? kThreadsI8 : kThreads, 1)
     if (!p.own) grid_dep_wait();  // the step before has ended when this grid has: the join reads both
 }
 
-template <typename CT, int D, bool PQ, bool PP, bool I8>
+template <typename CT, int D, bool PQ, bool I8>
 PrefixKernel kernel_of() {
-    return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, PQ, PP, I8>), Layout<D, I8>::SMEM, I8 ? kThreadsI8 : kThreads,
+    return {reinterpret_cast<const void*>(&prefix_tc_kernel<CT, D, PQ, I8>), Layout<D, I8>::SMEM, I8 ? kThreadsI8 : kThreads,
             PQ ? TK : 2 * TK, 2 * TK, true};
 }
 

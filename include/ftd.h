@@ -572,11 +572,10 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  * Other arguments, out, the appended rows (an INT8 row's scale as in ftd_decode_mha_scored) and
  * the sticky errors as in ftd_decode_mha; a page of the prefix outside [0, num_pages) raises
  * FTD_ERR_BAD_PAGE, and what the slots see of it is undefined.
- * fp16 and bf16 caches: the tensor cores take the weights rounded to that type where out is a
- * 16-bit type, and q as it is where it is of the cache's type and has no bias; else each as a
- * pair of its numbers (about 16 mantissa bits with bf16), as ftd_decode_mha does.  INT8 caches:
- * codes are exact, scales multiply scores and weights in fp32; q is one fp16 or bf16 number without a bias, the
- * weights one bf16 number for bf16 out, else each a pair of bf16 numbers.  Launches two or
+ * fp16 and bf16 caches: the tensor cores take the weights as pairs of numbers of that type (about 16 mantissa bits with
+ * bf16, 22 with fp16), as ftd_decode_mha does, and q as it is where it is of the cache's type and has no bias, else as a pair
+ * too.  INT8 caches: codes are exact, scales multiply scores and weights in fp32; the weights are pairs of bf16 numbers, q one
+ * fp16 or bf16 number where it is of that type and has no bias, else such a pair too.  Launches two or
  * three kernels: the slots' own rows are taken beside the prefix or by the step's kernel.
  */
 ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new, const void* v_new, const void* qkv_bias,
