@@ -451,6 +451,7 @@ static __device__ __noinline__ void scale_scores(uint32_t ts, int lim, const flo
 // largest of its scores from there on.  What the old one has made (weights, O, the sum) is rescaled.
 template <int D>
 static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, int c0, bool sees, bool chained, float2 ml, const float* ks) {
+    wide::tmem_st_wait();  // the chunks before c0 are read below: a load is not ordered behind the stores of their weights
     float top = -INFINITY;
 #pragma unroll 1
     for (int c = 4 * c0; c < TK / 8; ++c) {
