@@ -447,12 +447,15 @@ static __device__ __noinline__ void scale_scores(uint32_t ts, int lim, const flo
     wide::tmem_st_wait();
 }
 
-// A new reference for a row in the middle of a tile of codes, whose chunks of 32 columns before c hold weights already: the
-// largest of its scores from there on.  What the old one has made (weights, O, the sum) is rescaled.
+// A new reference for the rows of a warp that need one (moves) in the middle of a tile of codes, whose chunks of 32 columns before
+// c0 hold weights already: the largest of the row's scores from there on, rounded up to a whole number.  What the old
+// one has made (weights, O, the sum) is rescaled, by a power of two: exactly, so that the pairs keep their bits, which may
+// count as much as the new weights (they may be 2^kReach of the old reference).  The other rows keep theirs, and nothing of
+// them changes.
 template <int D>
-static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, int c0, bool sees, bool chained, float2 ml, const float* ks) {
-    wide::tmem_st_wait();  // the chunks before c0 are read below: a load is not ordered behind the stores of their weights
+static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, int c0, bool moves, bool chained, float2 ml, const float* ks) {
     float top = -INFINITY;
+    wide::tmem_st_wait();  // the chunks before c0 are read below: a load is not ordered behind the stores of their weights
 #pragma unroll 1
     for (int c = 4 * c0; c < TK / 8; ++c) {
         float x[8];
@@ -460,9 +463,10 @@ static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e] * ks[8 * c + e]);
     }
-    const float mn = sees ? fmaxf(ml.x, top) : ml.x, alpha = wide::ex2(ml.x - mn);
+    const float mn = moves ? ceilf(top) : ml.x, down = mn - ml.x;  // (whole numbers, or the first reference)
+    const float alpha = down > 126.f ? 0.f : __int_as_float((127 - static_cast<int>(down)) << 23);
 #pragma unroll 1
-    for (int c = 0; c < 4 * c0; ++c) {  // (those weights are less than 2^-kReach of the new ones: a second rounding is nothing)
+    for (int c = 0; c < 4 * c0; ++c) {
         float x[8];
         wide::tmem_ld_rows<8>(ts + 8 * c, x);
 #pragma unroll
@@ -525,8 +529,9 @@ static __device__ __noinline__ float2 take_tile_i8(uint32_t ts, uint32_t to, int
             t0 = fmaxf(t0, fmaxf(x[e], x[e + 1]));
             t1 = fmaxf(t1, fmaxf(x[e + 2], x[e + 3]));
         }
-        if (__any_sync(FULL, sees && fmaxf(t0, t1) > kReach)) {
-            const float2 moved = move_reference<D>(ts, to, c, sees, chained, ml, ks);
+        const bool moves = sees && fmaxf(t0, t1) > kReach;
+        if (__any_sync(FULL, moves)) {
+            const float2 moved = move_reference<D>(ts, to, c, moves, chained, ml, ks);
             const uint64_t a2 = pack2(moved.y, moved.y);
             ml = make_float2(moved.x, ml.y * moved.y);
             acc0 = mul2(acc0, a2);

@@ -116,3 +116,57 @@ def test_a_row_that_leaps(shape, qkv):
     assert np.all(np.abs(got[rest] - want * sign) <= tol), float(np.abs(got[rest] - want * sign).max() / tol)
     # the row that leaps sees nothing but the last steep key
     assert np.all(np.abs(got[leads] - sign) <= 2.0 ** -16 + SUMS)
+
+
+def second_roundings(off, s, v):
+    """What the weights' second roundings (in units of each tile's reference) would change the outputs by."""
+    x = np.append(s, 0.0)
+    top = s.reshape(TILES, TILE)[:, EARLY:].max(1)
+    return abs((off * np.exp2(top - x.max())[:, None] * v.reshape(TILES, TILE)).sum() / np.exp2(x - x.max()).sum())
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("qkv", ["f16", "bf16", "f32"])
+def test_neighbours_of_a_row_that_leaps(shape, qkv):
+    """The others' weights stay pairs, whose roundings are far below those of a second one, which would add up here."""
+    B, hkv, every = SHAPES[shape]
+    s, steep, v = ramp(every)
+    leads = [3, 35]
+    got, eff = run(s, steep, v, B, hkv, qkv, leads)
+    want, tol = bound(np.where(steep == 0, eff, 0.0), v)
+    assert second_roundings(moved_twice(s.reshape(TILES, TILE), every), s, v) > 4 * tol
+    sign = np.where(np.arange(DIM) % 2, -1.0, 1.0)
+    rest = np.setdiff1d(np.arange(8 * B), leads)
+    err = np.abs(got[rest] - want * sign)
+    assert np.all(np.isfinite(err)) and np.all(err <= tol), float(err.max() / tol)
+
+
+def cliffs(step):
+    """The prefix's last tiles: scores that come as near to the reach of the running reference as they may, then one that passes it,
+    so that the weights behind the move weigh no more than those ahead of it."""
+    s, h = np.zeros((TILES, TILE)), np.zeros(TILES)
+    rng = np.random.default_rng(4)
+    for i in range(TILES - 6, TILES):
+        if i - step < TILES - 6:
+            continue
+        low = h[i - step]
+        s[i] = low + 39.0 + 0.9 * rng.random(TILE)
+        s[i, AT] = h[i] = low + 40.6
+    # (the pattern's own moved_twice: the reference of a stream's tile before is that tile's cliff)
+    off = moved_twice(s, step)
+    off[:TILES - 6 + step] = 0.0
+    v = np.sign(off).astype(np.int8)
+    return s.reshape(-1), off, v.reshape(-1)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("qkv", ["f16", "f32"])
+def test_weights_ahead_of_a_move_that_count(shape, qkv):
+    """Every row moves in the middle of a tile, by little more than the weights before it are above the old reference."""
+    B, hkv, every = SHAPES[shape]
+    s, off, v = cliffs(every)
+    got, eff = run(s, np.zeros(s.shape), v, B, hkv, qkv, [])
+    want, tol = bound(eff, v)
+    assert second_roundings(off, s, v) > 4 * tol
+    err = np.abs(got - want * np.where(np.arange(DIM) % 2, -1.0, 1.0))
+    assert np.all(np.isfinite(err)) and np.all(err <= tol), float(err.max() / tol)
