@@ -313,7 +313,7 @@ def _expect(name, t, n, dtype=None, itemsize=0, dense=True, tail=()):
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, {n} are needed")
     if (dtype is not None and t.dtype is not dtype) or (itemsize and t.element_size() != itemsize):
-        raise ValueError(f"{name} is {t.dtype}, it has to be {dtype or f'the qkv type of {itemsize} bytes'}")
+        raise ValueError(f"{name} is {t.dtype}, it has to be {dtype or f'a type of {itemsize} bytes'}")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name} has to be contiguous")
     if t.numel() > n and t.dim() > 1 and any(a != b for a, b in zip(reversed(t.shape), reversed(tail))):
@@ -362,6 +362,7 @@ class DecodeStep:
         self._widths = (n_q_heads * head_dim, n_kv_heads * head_dim, head_dim)
         self._qkv_bytes = 4 if qkv_dtype == "f32" else 2
         self._cache_bytes = {"f32": 4, "f16": 2, "bf16": 2, "i8": 1}[cache_dtype]
+        self._out_bytes = 4 if out_dtype == "f32" else 2
         self._int32 = torch.int32
         self._axes = 0
         self._float32 = torch.float32
@@ -597,6 +598,18 @@ class DecodeStep:
         """Allocate what ``prefix`` needs."""
         check(ftd_enable_prefix(self.ctx, _current_stream(self.device) if stream is None else stream))
 
+    def _check_step(self, q, k_new, v_new, out, bias, k_cache, v_cache, scales):
+        """Raise where a tensor of a step holds too little, or another type or layout than the kernels take."""
+        qw, kw, d = self._widths
+        n, eb, cb = self.cfg.max_batch * max(self.cfg.q_len, 1), self._qkv_bytes, self._cache_bytes
+        for name, t, size, eb, tail in (("q", q, n * qw, eb, (d,)), ("k_new", k_new, n * kw, eb, (d,)), ("v_new", v_new, n * kw, eb, (d,)),
+                                        ("out", out, n * qw, self._out_bytes, (d,)), ("bias", bias, qw + 2 * kw, eb, ()),
+                                        ("k_cache", k_cache, self._rows * d, cb, self._plane_tail + (d,)),
+                                        ("v_cache", v_cache, self._rows * d, cb, self._plane_tail + (d,)),
+                                        ("scales", scales, 2 * self._rows, 4, self._plane_tail)):
+            if t is not None and (t.nbytes != size * eb or t.itemsize != eb or not t.is_contiguous()):
+                _expect(name, t, size, itemsize=eb, tail=tail)
+
     def _prefix_rows(self, k_prefix, v_prefix, prefix_scales, prefix_table):
         """Rows of the prefix by its tensors, which have to agree."""
         d, hkv = self._widths[2], self.cfg.n_kv_heads
@@ -625,6 +638,7 @@ class DecodeStep:
         is [n_kv_heads, rows, head_dim] (INT8: and scales [2, n_kv_heads, rows]), or the pool's pages that
         ``prefix_table`` names.  After ``enable_prefix``."""
         self._check_planes((seq_lens, prefix_lens), table=block_table)
+        self._check_step(q, k_new, v_new, out, bias, k_cache, v_cache, scales)
         rows = self._prefix_rows(k_prefix, v_prefix, prefix_scales, prefix_table)
         s = _current_stream(self.device) if stream is None else stream
         st = ftd_decode_mha_prefix(self.ctx, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _ptr(bias), _ptr(k_cache),
