@@ -107,7 +107,8 @@ __device__ __forceinline__ int cached_rows(int L) {
     return L;
 }
 // Scale of an INT8 row from its largest magnitude (0: 1).  The step divides by 127; the scored
-// step and the step beside a shared prefix multiply by the fp32 value of 1 / 127, within an ulp of that.
+// step and the step beside a shared prefix multiply by the fp32 value of 1 / 127, within an ulp of that: their codes have to agree
+// with those of a quotient by 127.0 formed on the device's tensors, which torch computes as this product.
 template <int MODE>
 __device__ __forceinline__ float i8_row_scale(float amax) {
     if (amax == 0.f) return 1.f;

@@ -569,7 +569,7 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  * positions already, so the slot's own rows start wherever the caller turned them to.
  * Rows of the prefix from the longest prefix_lens on may hold anything; rows that some slot
  * sees hold finite values.
- * Other arguments, out, the appended rows (an INT8 row's scale as in ftd_decode_mha_scored) and
+ * Other arguments, out, the appended rows (with prefix_rows above 0 an INT8 row's scale as in ftd_decode_mha_scored) and
  * the sticky errors as in ftd_decode_mha; a page of the prefix outside [0, num_pages) raises
  * FTD_ERR_BAD_PAGE, and what the slots see of it is undefined.
  * fp16 and bf16 caches: the tensor cores take the weights as pairs of numbers of that type (about 16 mantissa bits with
