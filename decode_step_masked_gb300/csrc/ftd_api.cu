@@ -1614,6 +1614,18 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
             return fail(FTD_ERR_INVALID_ARG, "%s: k_prefix and v_prefix (INT8: and prefix_scales) must be non-NULL", what);
         if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned(prefix_scales, 4))
             return fail(FTD_ERR_INVALID_ARG, "%s: k_prefix and v_prefix must be 16-byte aligned", what);
+        // the prefix is read beside the slots' appends, by other blocks than theirs
+        const size_t row = static_cast<size_t>(c.head_dim) * elem_bytes(c.cache_dtype), shared = static_cast<size_t>(prefix_rows) * c.n_kv_heads;
+        struct Span { const void* p; size_t bytes; };
+        const Span read[] = {{k_prefix, shared * row}, {v_prefix, shared * row}, {i8 ? prefix_scales : nullptr, 2 * shared * sizeof(float)}};
+        const Span written[] = {{k_cache ? k_cache : ctx->k_cache, ctx->rows * row},
+                                {v_cache ? v_cache : ctx->v_cache, ctx->rows * row},
+                                {i8 ? (scales ? scales : ctx->scales) : nullptr, 2 * ctx->rows * sizeof(float)},
+                                {out, static_cast<size_t>(c.max_batch) * ctx->nq * c.n_q_heads * c.head_dim * elem_bytes(c.out_dtype)}};
+        for (const Span& r : read)
+            for (const Span& w : written)
+                if (prefix_rows > 0 && r.p && w.p && overlaps(r.p, r.bytes, w.p, w.bytes))
+                    return fail(FTD_ERR_INVALID_ARG, "%s: the prefix overlaps the caches, their scales or out", what);
     }
     DeviceScope dev(ctx->device);
     if (dev.err != cudaSuccess) return cuda_fail(dev.err, "cudaSetDevice");

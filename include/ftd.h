@@ -557,7 +557,7 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  * The prefix is read once for all slots: with B slots its products are matrix products
  * with B * T * Hq / Hkv rows, on the tensor cores for fp16, bf16 and INT8 caches.
  *   k_prefix, v_prefix : device [Hkv][prefix_rows][D] of the cache dtype, 16-byte aligned, read
- *               only; INT8 with prefix_scales, device fp32 [2][Hkv][prefix_rows].  On a
+ *               only, apart from the caches and out; INT8 with prefix_scales, device fp32 [2][Hkv][prefix_rows].  On a
  *               paged context NULL: the prefix lies in pages of the pool, and
  *   prefix_table : device int32 [ceil(prefix_rows / page_size)] names them (NULL on a
  *               contiguous context).  No slot's block table may have them in reach of a
