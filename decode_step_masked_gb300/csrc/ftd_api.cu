@@ -1632,6 +1632,14 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (prefix_rows == 0)  // nothing to share: straight to out
         return launch_decode(ctx, q, k_new, v_new, qkv_bias, k_cache, v_cache, block_table, seq_lens, scales, out, s);
+    // q as one 16-bit number of the products' type where it is one, else as two
+    const bool pair_q = qkv_bias || (i8 ? c.qkv_dtype == FTD_F32 : c.qkv_dtype != c.cache_dtype);
+    const ftd::PrefixKernel& k = ctx->pre[pair_q];
+    // (the kernels count a kv head's tiles, of 64 rows at least, in 31 bits)
+    const int64_t rows_q = static_cast<int64_t>(c.max_batch) * ctx->nq * (c.n_q_heads / c.n_kv_heads);
+    if ((rows_q + k.block_rows - 1) / k.block_rows * ((prefix_rows + 63) / 64) >= (static_cast<int64_t>(1) << 31))
+        return fail(FTD_ERR_INVALID_ARG, "%s: prefix_rows %lld with %lld query rows per kv head", what, static_cast<long long>(prefix_rows),
+                    static_cast<long long>(rows_q));
     const bool stall = ctx->stall_calls > 0;
     if (ctx->pre_own_rows) {
         if (!k_cache) k_cache = ctx->k_cache;
@@ -1682,10 +1690,7 @@ ftd_status ftd_decode_mha_prefix(ftd_ctx* ctx, const void* q, const void* k_new,
     p.D = c.head_dim;
     p.Lmax = c.max_len;
     p.P = static_cast<int>(prefix_rows);
-    p.R = p.B * p.T * p.group;
-    // q as one 16-bit number of the products' type where it is one, else as two
-    const bool pair_q = qkv_bias || (i8 ? c.qkv_dtype == FTD_F32 : c.qkv_dtype != c.cache_dtype);
-    const ftd::PrefixKernel& k = ctx->pre[pair_q];
+    p.R = static_cast<int>(rows_q);
     p.block_rows = k.block_rows;
     p.slot_rows = k.slot_rows;
     p.split = k.split;

@@ -562,7 +562,8 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  *   prefix_table : device int32 [ceil(prefix_rows / page_size)] names them (NULL on a
  *               contiguous context).  No slot's block table may have them in reach of a
  *               new row.
- *   prefix_rows : rows of the prefix, >= 0; 0: ftd_decode_mha's call.
+ *   prefix_rows : rows of the prefix, >= 0; 0: ftd_decode_mha's call.  Refused where prefix_rows * Hkv, or ceil(prefix_rows / 64)
+ *               times the blocks of 64 to 256 query rows of a kv head, passes 31 bits.
  *   prefix_lens : device int32 [B].  A slot that shares nothing has 0 (or less); one above
  *               prefix_rows sees prefix_rows and raises FTD_ERR_SEQ_OVERFLOW.
  * seq_lens counts the slot's own rows: 0 as long as it has only the prefix.  Keys carry their
