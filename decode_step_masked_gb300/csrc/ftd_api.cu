@@ -1548,14 +1548,16 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream) {
         off = align_up(off + bytes, 256);
         return o;
     };
-    // The prefix's kernel takes the own rows too (partials in place of the step's output) where a slot has 4 to 32 query rows and
-    // short contexts, or where there is little of them.  Own rows with it / by the step's kernel, us: 64 slots of 1 to
-    // 1023 rows, 8 kv heads of 128 behind 8192, with 1 / 2 / 4 / 8 / 32 query rows 118 / 111 / 104 / 107 / 178 against 93 / 96 /
-    // 110 / 115 / 262; 16 slots of 7000 to 8000 rows, 8 query rows 153 against 137; 4 / 8 / 16 slots of 17 to
-    // 190 rows, 32 heads 46 / 54 / 62 against 57 / 55 / 57.
+    // The prefix's kernel takes the own rows too (partials in place of the step's output) where a slot has many query rows (up to 32),
+    // or some and short contexts, or where there is little of them.  Own rows with it / by the step's kernel, us, bf16, 8 kv heads of
+    // 128 behind 8192 rows: 64 slots of 1 to 1023 rows with 1 / 4 / 8 / 12 / 16 / 24 / 32 query rows 93 / 96 / 108 / 124 / 134 / 180 / 202 against
+    // 71 / 82 / 93 / 109 / 129 / 192 / 272; of 33 to 300 rows with 4 / 8 / 10 / 12 / 16 / 32 74 / 88 / 93 / 96 / 104 / 172 against 69 / 83 / 100 / 96 / 112 / 209; of
+    // 1 to 63 rows with 1 / 4 / 8 60 / 64 / 72 against 51 / 69 / 82; 16 slots of 7000 to 8000 rows with 8 / 16 / 24 / 32 140 / 143 / 154 / 159 against 123 / 141 /
+    // 233 / 160; 4 / 8 slots of 17 to 190 rows, 32 heads behind 777 46 / 50 against 45 / 49, 16 / 32 slots 58 / 81 against 49 / 55.
     const int per = static_cast<int>(T * (Hq / Hkv));
     const size_t own_tiles = B * Hkv * ((static_cast<size_t>(c.max_len) + 127) / 128);
-    const bool own = tc && !i8 && per <= ftd::kMostOwnRows && ((per >= 4 && c.max_len <= 4096) || own_tiles <= static_cast<size_t>(4 * ctx->grid));
+    const bool own = tc && !i8 && per <= ftd::kMostOwnRows &&
+                     (per > 16 || (per > 8 && c.max_len <= 512) || own_tiles <= static_cast<size_t>(4 * ctx->grid));
     const size_t o_own = carve(own ? 0 : B * T * Hq * D * sizeof(float)), o_ml = carve(own ? 0 : Hkv * R * sizeof(float2));
     const size_t o_ows = carve(own ? (B * Hkv + 2 * ctx->grid) * ftd::own_slot_floats(per, c.head_dim) * sizeof(float) : 0);
     const size_t o_oinfo = carve(own ? B * Hkv * sizeof(int2) : 0);

@@ -27,12 +27,12 @@ def lengths(B, lmax, T):
 
 @pytest.mark.parametrize("cache,out,D", [("bf16", "bf16", 128), ("f16", "f16", 64), ("f16", "f32", 128), ("bf16", "f32", 64)])
 @pytest.mark.parametrize("heavy", [4.0, 30.0, -30.0])
-@pytest.mark.parametrize("B,T", [(40, 1), (5, 2)])
+@pytest.mark.parametrize("B,T", [(40, 1), (5, 1)])
 def test_rising_scores(cache, out, D, heavy, B, T):
     """Own keys that grow along a slot's rows (or shrink), in segments of one tile to eight, several of them a block's."""
     lmax, P = 1024, 300
     lens = lengths(B, lmax, T)
-    w, inp = case(cache, cache, B, 16, 2, D, lmax, lens, P, [P - 7 * (b % 5) for b in range(B)], T=T)
+    w, inp = case(cache, cache, B, 48, 2, D, lmax, lens, P, [P - 7 * (b % 5) for b in range(B)], T=T)
     grow = 1.0 + heavy * (np.arange(lmax) if heavy > 0 else np.arange(lmax) - lmax) / lmax
     x = ref.widen(inp["k_cache"], cache)
     inp["k_cache"] = np.where(np.isnan(x), inp["k_cache"], to_storage((np.nan_to_num(x) * grow[:, None]).astype(np.float32), cache))
@@ -45,7 +45,7 @@ def test_waits_that_run_out(out, B):
     """Slots that see nothing of the prefix, so that the copy that is withheld, block 0's first, is of an own tile: the bounded waits give
     up, the error is reported, and the next call is right.  With one tile a block, and with several under way."""
     lmax = 1024
-    w, inp = case("bf16", "bf16", B, 16, 2, 128, lmax, lengths(B, lmax, 1), 200, [0] * B, bias=None)
+    w, inp = case("bf16", "bf16", B, 48, 2, 128, lmax, lengths(B, lmax, 1), 200, [0] * B, bias=None)
     step = make_step(w, out_dtype=out, wait_limit_us=2000)
     step.enable_prefix()
     run(w, inp, out_dtype=out, step=step)
