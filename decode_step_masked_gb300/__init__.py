@@ -369,6 +369,10 @@ class DecodeStep:
         # cache rows: elements of a plane
         self._rows = num_pages * n_kv_heads * page_size if page_size else max_batch * n_kv_heads * max_len
         self._plane_tail = (n_kv_heads, page_size or max_len)
+        n, eb, cb = max_batch * max(int(q_len), 1), self._qkv_bytes, self._cache_bytes
+        # bytes of a step's q, new rows, output and caches, and of an element of each
+        self._step_bytes = (n * n_q_heads * head_dim * eb, n * n_kv_heads * head_dim * eb, n * n_q_heads * head_dim * self._out_bytes,
+                            self._rows * head_dim * cb, eb, self._out_bytes, cb)
         self._entries = max_batch * -(-max_len // page_size) if page_size else 0  # of a block table
         if scored:
             self.enable_scores(s)
@@ -638,7 +642,14 @@ class DecodeStep:
         is [n_kv_heads, rows, head_dim] (INT8: and scales [2, n_kv_heads, rows]), or the pool's pages that
         ``prefix_table`` names.  After ``enable_prefix``."""
         self._check_planes((seq_lens, prefix_lens), table=block_table)
-        self._check_step(q, k_new, v_new, out, bias, k_cache, v_cache, scales)
+        bq, bk, bo, bc, eb, ob, cb = self._step_bytes
+        if (q.nbytes != bq or q.itemsize != eb or not q.is_contiguous() or k_new.nbytes != bk or k_new.itemsize != eb
+                or not k_new.is_contiguous() or v_new.nbytes != bk or v_new.itemsize != eb or not v_new.is_contiguous()
+                or out.nbytes != bo or out.itemsize != ob or not out.is_contiguous()
+                or k_cache is not None and (k_cache.nbytes != bc or k_cache.itemsize != cb or not k_cache.is_contiguous())
+                or v_cache is not None and (v_cache.nbytes != bc or v_cache.itemsize != cb or not v_cache.is_contiguous())
+                or bias is not None or scales is not None):
+            self._check_step(q, k_new, v_new, out, bias, k_cache, v_cache, scales)
         rows = self._prefix_rows(k_prefix, v_prefix, prefix_scales, prefix_table)
         s = _current_stream(self.device) if stream is None else stream
         st = ftd_decode_mha_prefix(self.ctx, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _ptr(bias), _ptr(k_cache),
