@@ -53,3 +53,14 @@ def test_waits_that_run_out(out, B):
     run(w, inp, out_dtype=out, step=step, status=ftd.FTD_ERR_DEVICE_TIMEOUT, values=False)
     run(w, inp, out_dtype=out, step=step)
     step.close()
+
+
+@pytest.mark.parametrize("group,T", [(1, 1), (3, 1), (4, 1), (5, 1), (7, 1), (8, 1), (3, 3), (11, 1), (12, 1), (7, 2), (5, 3), (16, 1), (1, 13)])
+@pytest.mark.parametrize("cache,qkv,D,page", [("bf16", "bf16", 128, 0), ("f16", "f16", 64, 128), ("bf16", "f32", 64, 0), ("f16", "f16", 128, 256)])
+def test_by_the_steps_kernel(group, T, cache, qkv, D, page):
+    """Few query rows a slot and enough own rows that the step's kernel takes them beside the prefix."""
+    B, lmax = 40, 1024
+    lens = lengths(B, lmax, T)
+    w, inp = case(cache, qkv, B, 2 * group, 2, D, lmax, lens, 300, [300 - 7 * (b % 5) for b in range(B)], T=T)
+    run(w, inp, page=page)
+    run(w, inp, out_dtype="bf16" if qkv == "f32" else qkv, page=page, bias=False)
