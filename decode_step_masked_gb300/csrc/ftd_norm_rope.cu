@@ -14,8 +14,8 @@
 // its bias and weights in registers as fp32 (read anew for every token they cost many instructions, and
 // the kernel was bound by those); the next token's loads go out before the present one is
 // worked on.  A block takes a tile of tokens and forms their cosines, sines and cache rows once in shared memory.
-// Measured: 16381 tokens of 64 + 2 * 8 heads, bf16, into pages, 146 us (69 % of the copy peak; with bias and weights read for each
-// token 169, in registers 162, with packed arithmetic and blocks without idle lanes 144): loads in flight bound it, 15 warps
+// Measured: 16381 tokens of 64 + 2 * 8 heads, bf16, into pages, 147 us (67 % of the copy peak; with bias and weights read for each
+// token 169, in registers 162, with packed arithmetic and blocks without idle lanes 147): loads in flight bound it, 15 warps
 // an SM with one token ahead.  4001 tokens of 32 + 2 * 32 heads into an INT8 cache 54 us (with a quotient for every code 70).
 #include <cuda_runtime.h>
 
@@ -364,8 +364,10 @@ cudaError_t launch_norm_rope(NormRopeParams p, int vec, int sms, cudaStream_t st
         if (g * heads_of(g) < gy * heads_of(gy)) gy = g;
     p.heads_per_block = heads_of(gy);
     gy = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
-    // Tokens of a tile: fewer where that would leave an SM fewer than two blocks.  As many blocks as are resident at once
-    // (two of 256 threads an SM) walk the tiles, each as many.
+    // Tokens of a tile: fewer where that would leave an SM fewer than two blocks.  Three times as many blocks as are resident at
+    // once (two of 256 threads an SM) walk the tiles, each as many: bias and weights are loaded three times, but a late block
+    // holds up less.  As many as are resident / three times as many, us, with the L2 flushed: 16381 tokens of 64 + 2 * 8 heads into bf16 pages
+    // 150 / 154 and dense 146 / 150, 4001 of them 52 / 54, 4001 tokens of 32 + 2 * 32 heads into an INT8 cache 66 / 62.
     p.tile = kNormTile;
     while (p.tile > 1 && (p.n + p.tile - 1) / p.tile * gy < 2LL * sms) p.tile >>= 1;
     const long long tiles = (p.n + p.tile - 1) / p.tile;

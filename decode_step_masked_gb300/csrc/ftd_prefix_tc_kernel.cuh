@@ -14,9 +14,8 @@
 // and its share of the own ones (odd blocks the own ones first, so that the memory works while other blocks
 // compute).  An own segment, a slot's kv head, has a few query rows only (T * group, at most 32); the products over
 // them are mostly empty, but even so cost less than a tile's way from memory.  Here each stream walks its own range of tiles, and no stream waits at a segment's end: the next q
-// is already in its other buffer, O is read while the next scores are made.  The decode step's kernel, whose
-// roles meet at every segment's end, takes 79 us for the own rows of a ragged 70B-shaped batch (64 slots of 1 to 1023
-// rows, 8 heads: 134 MB).
+// is already in its other buffer, O is read while the next scores are made.  Which own rows come here, and which go by the decode
+// step's kernel before, is a rule with both sides measured at ftd_enable_prefix.
 //
 // A softmax thread owns one query row: no exchange between threads.  It reads its scores once for the largest and once for
 // the weights, and only when a score passes its running reference m by more than 2^8 (the first tile always) moves
@@ -34,9 +33,9 @@
 // rows go by the decode step's kernel.
 //
 // Measured, all launches of a call: 64 70B-shaped slots of two tokens (1024 query rows a kv head) behind 32768 rows, bf16,
-// 192 us, 718 TFLOP/s of useful products (with single weights 147); a tile of both streams takes some 6900 cycles, of which its
-// products 1536, the softmax threads the rest (128 ex2 a thread and tile are 2048 cycles of the SM's units for two streams).  INT8 for the same shapes: 259 us,
-// 5800 cycles a tile.
+// 193 us, 714 TFLOP/s of useful products (with single weights 147); a tile of both streams takes some 6900 cycles (the time over a
+// block's tiles), of which its products 1536, the softmax threads the rest (128 ex2 a thread and tile are 2048 cycles of the SM's
+// units for two streams).  INT8 for the same shapes: 312 us (with single weights 259, 5800 cycles a tile).
 //
 // Roles (384 threads, one block an SM): warp 0 copies K and V tiles (TMA, a ring of whole tiles), then writes for the
 // join which blocks hold what; warps 1 and 3 issue the products, each of one stream (one warp for both was busy all the
@@ -493,7 +492,7 @@ static __device__ __noinline__ float2 move_reference(uint32_t ts, uint32_t to, i
 // take_tile for codes: S and the weights are of codes, whose rows' scales are in shared memory.  K's (times the softmax scale)
 // multiply the scores, V's the weights behind their sum: bf16 numbers, whose range takes any scale, and any weight up to 2^kReach
 // besides, so the reference stays where it is until a score is that far above it, and one pass over the scores is enough (a pass for
-// the largest score first took 304 us instead of 259 for 64 70B-shaped slots of two tokens behind
+// the largest score first took 304 us instead of 259, with single weights, for 64 70B-shaped slots of two tokens behind
 // 32768 rows, their own rows included).  ones: 128 of them, for scores
 // that are scaled already.  In chunks of 32 columns: 128 registers a thread.
 constexpr float kReach = 40.f;

@@ -432,13 +432,15 @@ ftd_status ftd_norm_rope_qkv(ftd_ctx* ctx, const void* q, const void* k, const v
  *   free_pages, n_free : device int32 [num_pages] and [1]: a stack, its top at n_free - 1.
  *               Entries that slots give back are pushed in (slot, entry) order, then those
  *               asked for are popped in that order, so pages given back are used again first.
+ *               Pages have no counts of users: one that two slots' tables hold comes back twice,
+ *               and a shared prefix's pages belong to a slot of their own that outlives the others.
  *   n_free_out : device int32 [1], NULL or n_free: in place.
  *   offsets   : device int32 [B + 1] or NULL: new tokens of the slots before b, packed.
  *   slots     : device int32 [max_tokens] or NULL: for each new token, in packed order, its
  *               place in the cache as ftd_norm_rope_qkv takes it; -1 from offsets[B] on.
  *   positions : device int32 [max_tokens] or NULL: its position; 0 from offsets[B] on.
  *               More than max_tokens new tokens raise FTD_ERR_SEQ_OVERFLOW, and those past
- *               it are left out of both lists.
+ *               it are left out of both lists.  max_tokens 0: as with both lists NULL.
  * On a contiguous context block_table, free_pages, n_free and n_free_out are NULL.  A page
  * outside [0, num_pages) that changes hands or holds a new token raises FTD_ERR_BAD_PAGE (its
  * tokens get -1), and so do an n_free outside [0, num_pages] and pages given back that the
@@ -543,7 +545,8 @@ ftd_status ftd_cross_mha(ftd_ctx* ctx, const void* q, const void* q_bias, const 
  * ftd_enable_prefix -- allocate the workspace of ftd_decode_mha_prefix: for each SM and for each
  * kv head and block of query rows a partial result over the prefix; for the slots' own rows
  * either an fp32 copy of out and two numbers per query row, or, where the prefix's kernel takes
- * them too, two partial results per SM and one per slot and kv head.  One cudaMalloc, freed by ftd_destroy.  A second call does nothing.  UNSUPPORTED
+ * them too, two partial results per SM and one per slot and kv head.  One cudaMalloc, freed by ftd_destroy; nothing is launched, so
+ * the stream is not used.  A second call does nothing.  UNSUPPORTED
  * above 32768 query rows per kv head (B * T * Hq / Hkv), INVALID_ARG with a window.
  */
 ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
@@ -556,6 +559,11 @@ ftd_status ftd_enable_prefix(ftd_ctx* ctx, void* stream);
  *   out[b][j][h] = softmax over both of scale * q'[b][j][h] . K, times V.
  * The prefix is read once for all slots: with B slots its products are matrix products
  * with B * T * Hq / Hkv rows, on the tensor cores for fp16, bf16 and INT8 caches.
+ * It pays from about B * prefix_rows * Hkv = 500000 rows of 128 (8 slots behind 8192 rows with 8 kv heads, 4 with 32; INT8
+ * as much with 8 kv heads and two to eight times that with 32; multi-query caches always with up to 8 slots): below, ftd_decode_mha_paged over block tables that name the
+ * prefix's pages in every slot is as fast or faster.  Here / there, us: 32 kv heads, fp16, behind 768 rows 4 / 16 / 64 slots
+ * 42 / 47 / 66 against 25 / 50 / 150, behind 8192 rows 2 / 4 / 16 slots 61 / 66 / 73 against 58 / 93 / 320; 64 on 8 heads, bf16, behind 2048 rows 16 / 32 slots
+ * 46 / 50 against 40 / 62, behind 32768 rows 2 / 4 / 64 slots 62 / 62 / 128 against 60 / 89 / 1092.
  *   k_prefix, v_prefix : device [Hkv][prefix_rows][D] of the cache dtype, 16-byte aligned, read
  *               only, apart from the caches and out; INT8 with prefix_scales, device fp32 [2][Hkv][prefix_rows].  On a
  *               paged context NULL: the prefix lies in pages of the pool, and
