@@ -369,6 +369,7 @@ class DecodeStep:
         # cache rows: elements of a plane
         self._rows = num_pages * n_kv_heads * page_size if page_size else max_batch * n_kv_heads * max_len
         self._plane_tail = (n_kv_heads, page_size or max_len)
+        self._scales_tail = (num_pages if page_size else max_batch,) + self._plane_tail  # (V's plane lies right behind K's)
         n, eb, cb = max_batch * max(int(q_len), 1), self._qkv_bytes, self._cache_bytes
         # bytes of a step's q, new rows, output and caches, and of an element of each
         self._step_bytes = (n * n_q_heads * head_dim * eb, n * n_kv_heads * head_dim * eb, n * n_q_heads * head_dim * self._out_bytes,
@@ -544,7 +545,7 @@ class DecodeStep:
                 if t is not None:
                     _expect(name, t, self._rows * d, itemsize=self._cache_bytes, tail=self._plane_tail + (d,))
             if scales is not None:
-                _expect("scales", scales, 2 * self._rows, dtype=self._float32, tail=self._plane_tail)
+                _expect("scales", scales, 2 * self._rows, dtype=self._float32, tail=self._scales_tail)
 
     def norm_rope(self, q, k, v, positions, q_out, k_out=None, v_out=None, bias=None, q_weight=None, k_weight=None, eps=1e-6,
                   weight_offset=0.0, slots=None, k_cache=None, v_cache=None, scales=None, stream: Optional[int] = None):
@@ -606,13 +607,13 @@ class DecodeStep:
         """Raise where a tensor of a step holds too little, or another type or layout than the kernels take."""
         qw, kw, d = self._widths
         n, eb, cb = self.cfg.max_batch * max(self.cfg.q_len, 1), self._qkv_bytes, self._cache_bytes
-        for name, t, size, eb, tail in (("q", q, n * qw, eb, (d,)), ("k_new", k_new, n * kw, eb, (d,)), ("v_new", v_new, n * kw, eb, (d,)),
-                                        ("out", out, n * qw, self._out_bytes, (d,)), ("bias", bias, qw + 2 * kw, eb, ()),
+        for name, t, size, eb, tail in (("q", q, n * qw, eb, None), ("k_new", k_new, n * kw, eb, None), ("v_new", v_new, n * kw, eb, None),
+                                        ("out", out, n * qw, self._out_bytes, None), ("bias", bias, qw + 2 * kw, eb, None),
                                         ("k_cache", k_cache, self._rows * d, cb, self._plane_tail + (d,)),
                                         ("v_cache", v_cache, self._rows * d, cb, self._plane_tail + (d,)),
-                                        ("scales", scales, 2 * self._rows, 4, self._plane_tail)):
+                                        ("scales", scales, 2 * self._rows, 4, self._scales_tail)):
             if t is not None and (t.nbytes != size * eb or t.itemsize != eb or not t.is_contiguous()):
-                _expect(name, t, size, itemsize=eb, tail=tail)
+                _expect(name, t, size, itemsize=eb, tail=t.shape if tail is None else tail)
 
     def _prefix_rows(self, k_prefix, v_prefix, prefix_scales, prefix_table):
         """Rows of the prefix by its tensors, which have to agree."""
